@@ -8,7 +8,10 @@ the library is missing, every call raises.
 The C ABI (``include/gdn.h``) is mirrored name for name:
 ``gdn_workspace_bytes``, ``gdn_forward``, ``gdn_status_string``,
 ``gdn_version`` and the ``gdn_problem_t`` structure.  ``forward`` is a
-convenience wrapper that allocates outputs and workspace with torch.
+convenience wrapper that allocates outputs and workspace with torch.  The
+operators a recurrent layer runs around its scan (``causal_conv``, ``rotary``,
+``selective_scan``) and the single-token steps (``causal_conv_step``,
+``selective_step``, ``delta_step``) are in ``layer.py``.
 """
 from __future__ import annotations
 
@@ -44,7 +47,15 @@ EXCLUSIVE = {"none": 0, "fwd": GDN_OPT_EXCLUSIVE_FORWARD, "rev": GDN_OPT_EXCLUSI
 
 GDN_VDA_OPT_ADDITIVE = 1
 
+GDN_ACT_NONE = 0
+GDN_ACT_SILU = 1
+ACTIVATIONS = {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU}
+GDN_SSM_OPT_SOFTPLUS = 1
+GDN_ROTARY_OPT_INTERLEAVED = 1
+GDN_ROTARY_OPT_INVERSE = 2
+
 EXPORTED = ("gdn_workspace_bytes", "gdn_forward", "gdn_forward_noalloc", "gdn_vda_workspace_bytes", "gdn_vda_forward",
+            "gdn_conv_forward", "gdn_conv_step", "gdn_ssm_forward", "gdn_ssm_step", "gdn_rotary", "gdn_step",
             "gdn_status_string", "gdn_version")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # GDN_NOALLOC_SCRATCH_BYTES
 
@@ -72,6 +83,62 @@ class gdn_vda_problem_t(ctypes.Structure):
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("stream", ctypes.c_void_p),
         ("timing_events", ctypes.c_void_p),
+    ]
+
+
+class gdn_conv_problem_t(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64),
+        ("x_stride_b", ctypes.c_int64), ("x_stride_t", ctypes.c_int64),
+        ("out_stride_b", ctypes.c_int64), ("out_stride_t", ctypes.c_int64),
+        ("slots", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("width", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("seq_offsets", ctypes.c_void_p), ("state_index", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class gdn_ssm_problem_t(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64), ("N", ctypes.c_int64),
+        ("G", ctypes.c_int64),
+        ("x_stride_b", ctypes.c_int64), ("x_stride_t", ctypes.c_int64),
+        ("dt_stride_b", ctypes.c_int64), ("dt_stride_t", ctypes.c_int64),
+        ("z_stride_b", ctypes.c_int64), ("z_stride_t", ctypes.c_int64),
+        ("b_stride_b", ctypes.c_int64), ("b_stride_t", ctypes.c_int64),
+        ("c_stride_b", ctypes.c_int64), ("c_stride_t", ctypes.c_int64),
+        ("out_stride_b", ctypes.c_int64), ("out_stride_t", ctypes.c_int64),
+        ("slots", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("options", ctypes.c_int32),
+        ("seq_offsets", ctypes.c_void_p), ("state_index", ctypes.c_void_p),
+        ("z", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("skip", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class gdn_rotary_problem_t(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64),
+        ("d", ctypes.c_int64), ("rot", ctypes.c_int64),
+        ("q_stride_b", ctypes.c_int64), ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+        ("k_stride_b", ctypes.c_int64), ("k_stride_t", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+        ("q_out_stride_b", ctypes.c_int64), ("q_out_stride_t", ctypes.c_int64), ("q_out_stride_h", ctypes.c_int64),
+        ("k_out_stride_b", ctypes.c_int64), ("k_out_stride_t", ctypes.c_int64), ("k_out_stride_h", ctypes.c_int64),
+        ("position0", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("options", ctypes.c_int32), ("position_bits", ctypes.c_int32),
+        ("axes", ctypes.c_int32), ("section", ctypes.c_int32 * 4), ("scale", ctypes.c_float),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class gdn_step_problem_t(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("H", ctypes.c_int64), ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
+        ("slots", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("options", ctypes.c_int32),
+        ("state_index", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p),
+        ("norm_eps", ctypes.c_float),
+        ("stream", ctypes.c_void_p),
     ]
 
 
@@ -104,6 +171,14 @@ def lib() -> ctypes.CDLL:
         L.gdn_vda_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_vda_forward.argtypes = [PV, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int32]
         L.gdn_vda_forward.restype = ctypes.c_int
+        for name, struct, pointers in (("gdn_conv_forward", gdn_conv_problem_t, 6),
+                                       ("gdn_conv_step", gdn_conv_problem_t, 5),
+                                       ("gdn_ssm_forward", gdn_ssm_problem_t, 8),
+                                       ("gdn_ssm_step", gdn_ssm_problem_t, 7),
+                                       ("gdn_rotary", gdn_rotary_problem_t, 6), ("gdn_step", gdn_step_problem_t, 7)):
+            fn = getattr(L, name)
+            fn.argtypes = [ctypes.POINTER(struct)] + [vp] * pointers
+            fn.restype = ctypes.c_int
         L.gdn_status_string.argtypes = [ctypes.c_int32]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_version.argtypes = []
@@ -140,6 +215,36 @@ def gdn_vda_forward(problem: gdn_vda_problem_t, q: int, k: int, v: int, log_alph
     """Raw call of the frame-wise operator with integer device pointers; returns the status."""
     return int(lib().gdn_vda_forward(ctypes.byref(problem), q, k, v, log_alpha, beta, state_in, state_out, out,
                                      int(direction)))
+
+
+def gdn_conv_forward(problem: gdn_conv_problem_t, x, weight, bias, state_in, state_out, out) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_conv_forward(ctypes.byref(problem), x, weight, bias, state_in, state_out, out)
+
+
+def gdn_conv_step(problem: gdn_conv_problem_t, x, weight, bias, state, out) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_conv_step(ctypes.byref(problem), x, weight, bias, state, out)
+
+
+def gdn_ssm_forward(problem: gdn_ssm_problem_t, x, dt, A, Bm, Cm, state_in, state_out, out) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_ssm_forward(ctypes.byref(problem), x, dt, A, Bm, Cm, state_in, state_out, out)
+
+
+def gdn_ssm_step(problem: gdn_ssm_problem_t, x, dt, A, Bm, Cm, state, out) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_ssm_step(ctypes.byref(problem), x, dt, A, Bm, Cm, state, out)
+
+
+def gdn_rotary(problem: gdn_rotary_problem_t, q, k, inv_freq, positions, q_out, k_out) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_rotary(ctypes.byref(problem), q, k, inv_freq, positions, q_out, k_out)
+
+
+def gdn_step(problem: gdn_step_problem_t, q, k, v, log_alpha, beta, state, out) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_step(ctypes.byref(problem), q, k, v, log_alpha, beta, state, out)
 
 
 def gdn_status_string(status: int) -> str:
@@ -337,7 +442,23 @@ def vda_forward(q, k, v, log_alpha, beta, state_in=None, direction: str = "fwd",
     return out, state_out
 
 
-# ---- torch.library custom ops: the two calls as graph-safe operators ----
+# ---- the layer operators (layer.py, imported on first use: it needs torch) ----
+
+LAYER = ("causal_conv", "causal_conv_step", "selective_scan", "selective_step", "rotary", "rotary_frequencies",
+         "delta_step")
+
+
+def __getattr__(name: str):
+    if name in LAYER:
+        from . import layer
+
+        for n in LAYER:
+            globals()[n] = getattr(layer, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+# ---- torch.library custom ops: the calls as graph-safe operators ----
 # (torch.compile traces them as opaque nodes with the output shapes below,
 # instead of breaking the graph at the ctypes call)
 
@@ -345,9 +466,10 @@ _ops_registered = False
 
 
 def register_torch_ops() -> None:
-    """Register torch.ops.gdn.forward and torch.ops.gdn.vda_forward (CUDA
-    tensors; outputs allocated by the op) with fake implementations for
-    tracing.  Idempotent."""
+    """Register torch.ops.gdn.forward, torch.ops.gdn.vda_forward and the layer
+    operators (causal_conv, causal_conv_step, selective_scan, selective_step,
+    rotary, delta_step) for CUDA tensors (outputs allocated by the op) with
+    fake implementations for tracing.  Idempotent."""
     global _ops_registered
     if _ops_registered:
         return
@@ -388,4 +510,7 @@ def register_torch_ops() -> None:
         return (q.new_empty((B, T, H, dv), dtype=torch.float32),
                 q.new_empty((dirs, B, H, dv, dk), dtype=torch.float32))
 
+    from . import layer
+
+    layer.register_ops()
     _ops_registered = True

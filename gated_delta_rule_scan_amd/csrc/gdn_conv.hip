@@ -1,0 +1,235 @@
+// Short causal depthwise convolution over time, for prompts and for single
+// tokens:
+//
+//   y[t, d] = act(bias[d] + sum_{j < W} w[d, j] x[t - (W - 1) + j, d])
+//
+// with the rows before a sequence's first taken from its state (the last
+// W - 1 input rows).  Memory-bound: 2 W flops per element against one read
+// and one write of it.
+//
+// Prompt split: a thread owns V neighbouring channels (16 bytes of a row, or
+// one channel where rows are not 16-byte aligned) and a run of tokens, which
+// it walks in batches of kConvRows.  A batch's rows are all in flight at once,
+// the last W - 1 rows of the batch before stay in registers, and the next
+// batch's loads are issued before the current one is computed; a run re-reads
+// only its W - 1 rows of history.  A wave covers up to 64 V channels of a row,
+// so rows are read and written in whole cache lines.
+#include "gdn_layer.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kConvRows = 8;  // tokens in flight per thread
+
+// V channels as stored: 16 aligned bytes, or a single element
+template <typename MT, int V>
+struct Pack {
+  MT e[V];
+};
+template <typename MT, int V>
+__device__ __forceinline__ Pack<MT, V> load_pack(const MT* p) {
+  Pack<MT, V> r;
+  if constexpr (V == 1) {
+    r.e[0] = *p;
+  } else {
+    const f32x4 raw = *reinterpret_cast<const f32x4*>(p);
+    __builtin_memcpy(&r, &raw, 16);
+  }
+  return r;
+}
+template <typename MT, int V>
+__device__ __forceinline__ void store_pack(MT* p, const Pack<MT, V>& v) {
+  if constexpr (V == 1) {
+    *p = v.e[0];
+  } else {
+    f32x4 raw;
+    __builtin_memcpy(&raw, &v, 16);
+    *reinterpret_cast<f32x4*>(p) = raw;
+  }
+}
+template <typename MT, int V>
+__device__ __forceinline__ Pack<MT, V> zero_pack() {
+  Pack<MT, V> r;
+#pragma unroll
+  for (int e = 0; e < V; ++e) r.e[e] = (MT)0.0f;
+  return r;
+}
+
+// row `pos` of a sequence: its own rows from `x`, the W - 1 before them from
+// the state (zeros without one)
+template <typename MT, int W, int V>
+__device__ __forceinline__ Pack<MT, V> load_row(const MT* x, int64_t st, const MT* state, int64_t D, int64_t pos) {
+  if (pos >= 0) return load_pack<MT, V>(x + pos * st);
+  if (state) return load_pack<MT, V>(state + (W - 1 + pos) * D);
+  return zero_pack<MT, V>();
+}
+
+template <typename MT, int W, int V>
+__global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int channel_tiles, int64_t chunks) {
+  const int TX = 1 << tx_log2, TY = 256 >> tx_log2;
+  const int tx = threadIdx.x & (TX - 1), ty = threadIdx.x >> tx_log2;
+  const int64_t item = blockIdx.x / channel_tiles;
+  const int64_t d = ((int64_t)(blockIdx.x % channel_tiles) * TX + tx) * V;
+  const int64_t run = (int64_t)a.batches * kConvRows, C = run * TY;
+  SeqItem s;
+  int64_t x0, o0;
+  if (a.off) {
+    s = find_packed(a.off, a.B, a.T, C, item);
+    x0 = s.row0 * a.x_st;
+    o0 = s.row0 * a.o_st;
+  } else {
+    s.b = item / chunks;
+    s.chunk = item % chunks;
+    s.len = a.T;
+    x0 = s.b * a.x_sb;
+    o0 = s.b * a.o_sb;
+  }
+  if (d >= a.D || s.chunk < 0) return;
+  const int64_t t0 = s.chunk * C + ty * run;
+  const bool writes_state = s.chunk == 0 && ty == 0 && a.state_out;
+  if (t0 >= s.len && !writes_state) return;
+  const MT* x = static_cast<const MT*>(a.x) + x0 + d;
+  MT* out = static_cast<MT*>(a.out) + o0 + d;
+  const int64_t slot = slot_of(a.index, s.b, a.slots);
+  const MT* state = a.state_in && slot >= 0 ? static_cast<const MT*>(a.state_in) + slot * (W - 1) * a.D + d : nullptr;
+
+  if (t0 < s.len) {
+    float w[V][W], bias[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      bias[e] = a.bias ? a.bias[d + e] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[e][j] = a.weight[(d + e) * W + j];
+    }
+    Pack<MT, V> r[kConvRows + W - 1], nx[kConvRows];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) r[j] = load_row<MT, W, V>(x, a.x_st, state, a.D, t0 - (W - 1) + j);
+    const int64_t tend = t0 + run < s.len ? t0 + run : s.len;
+#pragma unroll
+    for (int i = 0; i < kConvRows; ++i)  // rows past the end repeat the last one; they are not stored
+      nx[i] = load_pack<MT, V>(x + (t0 + i < tend ? t0 + i : tend - 1) * a.x_st);
+    for (int64_t t = t0; t < tend; t += kConvRows) {
+#pragma unroll
+      for (int i = 0; i < kConvRows; ++i) r[W - 1 + i] = nx[i];
+      if (t + kConvRows < tend) {
+#pragma unroll
+        for (int i = 0; i < kConvRows; ++i) {
+          const int64_t u = t + kConvRows + i;
+          nx[i] = load_pack<MT, V>(x + (u < tend ? u : tend - 1) * a.x_st);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kConvRows; ++i) {
+        Pack<MT, V> y;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float acc = bias[e];
+#pragma unroll
+          for (int j = 0; j < W; ++j) acc = fmaf(w[e][j], to_float(r[i + j].e[e]), acc);
+          y.e[e] = (MT)(a.silu ? silu(acc) : acc);
+        }
+        if (t + i < tend) store_pack<MT, V>(out + (t + i) * a.o_st, y);
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) r[j] = r[kConvRows + j];
+    }
+  }
+  // The final state: written by the thread that alone reads this sequence's
+  // initial state for these channels, after that read, so the two may be one
+  // buffer.
+  if (writes_state && slot >= 0) {
+    Pack<MT, V> keep[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) keep[j] = load_row<MT, W, V>(x, a.x_st, state, a.D, s.len - (W - 1) + j);
+    MT* so = static_cast<MT*>(a.state_out) + slot * (W - 1) * a.D + d;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) store_pack<MT, V>(so + j * a.D, keep[j]);
+  }
+}
+
+// One token per sequence: a thread takes V channels of one sequence.
+template <typename MT, int W, int V>
+__global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int tx_log2, int channel_tiles) {
+  const int TX = 1 << tx_log2, TY = 256 >> tx_log2;
+  const int64_t b = (int64_t)(blockIdx.x / channel_tiles) * TY + (threadIdx.x >> tx_log2);
+  const int64_t d = ((int64_t)(blockIdx.x % channel_tiles) * TX + (threadIdx.x & (TX - 1))) * V;
+  if (b >= a.B || d >= a.D) return;
+  const int64_t slot = slot_of(a.index, b, a.slots);
+  if (slot < 0) return;
+  MT* state = static_cast<MT*>(a.state_out) + slot * (W - 1) * a.D + d;
+  Pack<MT, V> r[W], y;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) r[j] = load_pack<MT, V>(state + j * a.D);
+  r[W - 1] = load_pack<MT, V>(static_cast<const MT*>(a.x) + b * a.x_sb + d);
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    float acc = a.bias ? a.bias[d + e] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc = fmaf(a.weight[(d + e) * W + j], to_float(r[j].e[e]), acc);
+    y.e[e] = (MT)(a.silu ? silu(acc) : acc);
+  }
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) store_pack<MT, V>(state + j * a.D, r[j + 1]);
+  store_pack<MT, V>(static_cast<MT*>(a.out) + b * a.o_sb + d, y);
+}
+
+// lanes across channels: enough for the row, at most a wave
+int lanes_log2(int64_t lanes) {
+  int l = 3;
+  while (l < 6 && ((int64_t)1 << l) < lanes) ++l;
+  return l;
+}
+
+template <typename MT, int W, int V>
+hipError_t conv_launch(ConvArgs a, hipStream_t stream) {
+  const int64_t lanes = (a.D + V - 1) / V;
+  const int txl = lanes_log2(lanes), TY = 256 >> txl;
+  const int64_t ctiles = (lanes + ((int64_t)1 << txl) - 1) >> txl;
+  // four batches a run where that still gives every compute unit eight waves
+  // (2048 in all); shorter work takes one batch, for more threads
+  const int64_t rows = a.off ? a.T : a.B * a.T;
+  a.batches = ((rows * ctiles) << txl) >= (int64_t)2048 * 64 * 4 * kConvRows ? 4 : 1;
+  const int64_t C = (int64_t)a.batches * kConvRows * TY;
+  const int64_t chunks = (a.T + C - 1) / C > 0 ? (a.T + C - 1) / C : 1;
+  const int64_t items = a.off ? a.T / C + a.B : a.B * chunks;
+  if (!grid_fits(items * ctiles, 256)) return hipErrorNotSupported;
+  hipLaunchKernelGGL((conv_kernel<MT, W, V>), dim3((unsigned)(items * ctiles)), dim3(256), 0, stream, a, txl, (int)ctiles,
+                     chunks);
+  return hipGetLastError();
+}
+
+template <typename MT, int W, int V>
+hipError_t conv_step_launch(const ConvArgs& a, hipStream_t stream) {
+  const int64_t lanes = (a.D + V - 1) / V;
+  const int txl = lanes_log2(lanes), TY = 256 >> txl;
+  const int64_t ctiles = (lanes + ((int64_t)1 << txl) - 1) >> txl, items = (a.B + TY - 1) / TY;
+  if (!grid_fits(items * ctiles, 256)) return hipErrorNotSupported;
+  hipLaunchKernelGGL((conv_step_kernel<MT, W, V>), dim3((unsigned)(items * ctiles)), dim3(256), 0, stream, a, txl,
+                     (int)ctiles);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+template <typename MT>
+hipError_t launch_conv(const ConvArgs& a, int width, bool aligned, hipStream_t stream) {
+  constexpr int V = 16 / sizeof(MT);
+  if (width == 2) return aligned ? conv_launch<MT, 2, V>(a, stream) : conv_launch<MT, 2, 1>(a, stream);
+  if (width == 3) return aligned ? conv_launch<MT, 3, V>(a, stream) : conv_launch<MT, 3, 1>(a, stream);
+  return aligned ? conv_launch<MT, 4, V>(a, stream) : conv_launch<MT, 4, 1>(a, stream);
+}
+
+template <typename MT>
+hipError_t launch_conv_step(const ConvArgs& a, int width, bool aligned, hipStream_t stream) {
+  constexpr int V = 16 / sizeof(MT);
+  if (width == 2) return aligned ? conv_step_launch<MT, 2, V>(a, stream) : conv_step_launch<MT, 2, 1>(a, stream);
+  if (width == 3) return aligned ? conv_step_launch<MT, 3, V>(a, stream) : conv_step_launch<MT, 3, 1>(a, stream);
+  return aligned ? conv_step_launch<MT, 4, V>(a, stream) : conv_step_launch<MT, 4, 1>(a, stream);
+}
+
+template hipError_t launch_conv<float>(const ConvArgs&, int, bool, hipStream_t);
+template hipError_t launch_conv<bf16>(const ConvArgs&, int, bool, hipStream_t);
+template hipError_t launch_conv_step<float>(const ConvArgs&, int, bool, hipStream_t);
+template hipError_t launch_conv_step<bf16>(const ConvArgs&, int, bool, hipStream_t);
+
+}  // namespace gdn

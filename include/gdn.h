@@ -299,6 +299,183 @@ gdn_status_t gdn_vda_forward(const gdn_vda_problem_t* p,
                              const float* state_in, float* state_out,
                              float* out, int32_t direction);
 
+/* ---- What a recurrent layer runs around its scan, and its single-token form --
+ *
+ * The short causal convolution in front of the scan, rotary positions on q
+ * and k, the other common recurrent scan (a selective state space), and the
+ * single-token steps of all three recurrences.  Everything below runs on the
+ * problem's `stream`, allocates nothing, does not synchronise, can be captured
+ * into a graph, and uses no atomics: results are bitwise deterministic.
+ * Errors as for gdn_forward: a rejected call leaves every buffer untouched.
+ *
+ * Rows and strides.  An operand described with strides holds, for sequence b
+ * and token t, one row of contiguous channels at element b * stride_b +
+ * t * stride_t (strides in elements, >= 0); base pointers need only the
+ * alignment of their type.  Aligned operands are faster: 16-byte aligned
+ * pointers and strides that keep every row so.  The rows of an output must
+ * not meet each other, nor any row of another operand (rows of one wider
+ * buffer that lie beside each other may share it), except where an in-place
+ * call is allowed.
+ *
+ * Packed batches.  With seq_offsets != NULL ([B + 1] int32 in device memory,
+ * from 0 rising to at most T), sequence b is the rows seq_offsets[b] ..
+ * seq_offsets[b+1] - 1 of buffers of T rows; stride_b is not used.  A sequence
+ * may be empty; rows behind the last sequence are not touched.  Offsets
+ * outside 0..T are clamped to it, so no call reads or writes out of bounds.
+ * Without it every sequence has T tokens.
+ *
+ * State slots.  A recurrent state lives in one of `slots` rows of a state
+ * buffer.  With state_index != NULL ([B] int32 in device memory), sequence b
+ * uses row state_index[b]; an index outside 0..slots-1 means no state (a
+ * prompt then starts from zero and writes no final state; a step skips the
+ * row: its output row and every state stay as they were).  No two sequences
+ * of one call may name the same slot.  Without it, slots = B and sequence b
+ * uses row b.
+ *
+ * A float parameter pointer is fp32; x-like operands are fp32 or bf16
+ * (`dtype`).  All arithmetic is fp32 with one rounding at the end. */
+
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation_t;
+
+/* Short causal depthwise convolution over time:
+ *   y[t] = act(bias + sum_{j < width} weight[:, j] * x[t - (width - 1) + j]),
+ * rows before the sequence's first coming from its state: the last width - 1
+ * input rows, oldest first.
+ *   x, out     rows of D channels (dtype)
+ *   weight     [D, width] fp32; bias [D] fp32 or NULL
+ *   state_in   [slots, width - 1, D] (dtype), or NULL for zeros
+ *   state_out  the same, or NULL; may be state_in (an in-place carry)
+ * Supported: width 2, 3 or 4; B, D >= 1, T >= 0. */
+typedef struct {
+  int64_t B, T, D;
+  int64_t x_stride_b, x_stride_t;
+  int64_t out_stride_b, out_stride_t;
+  int64_t slots;
+  int32_t dtype;             /* gdn_dtype_t: type of x, out and the states */
+  int32_t width;
+  int32_t activation;        /* gdn_activation_t */
+  const int32_t* seq_offsets;
+  const int32_t* state_index;
+  void* stream;
+} gdn_conv_problem_t;
+
+gdn_status_t gdn_conv_forward(const gdn_conv_problem_t* p, const void* x, const float* weight, const float* bias,
+                              const void* state_in, void* state_out, void* out);
+
+/* One new token for each of B sequences: row b of x and out lies at element
+ * b * stride_b (T, stride_t and seq_offsets are not used); `state` is read and
+ * advanced in place. */
+gdn_status_t gdn_conv_step(const gdn_conv_problem_t* p, const void* x, const float* weight, const float* bias,
+                           void* state, void* out);
+
+/* Selective state space scan: per channel d an fp32 state h of N entries,
+ *   dt'  = softplus(dt + dt_bias)   (without GDN_SSM_OPT_SOFTPLUS: dt + dt_bias)
+ *   h_n  = exp(dt' A[d, n]) h_n + dt' x B[t, g, n]
+ *   y    = sum_n h_n C[t, g, n] + skip[d] x
+ *   out  = y * z * sigmoid(z)       (without z: y)
+ * with g = d / (D / G), the group of the channel.
+ *   x, dt, z, out  rows of D channels (dtype); z may be NULL
+ *   A              [D, N] fp32, <= 0 with dt' >= 0 (caller's contract: a
+ *                  decay above 1 overflows)
+ *   Bm, Cm         rows of G * N contiguous elements (dtype)
+ *   dt_bias, skip  [D] fp32, or NULL
+ *   state_in       [slots, D, N] fp32, or NULL for zeros
+ *   state_out      the same, or NULL; may be state_in (an in-place carry)
+ * Supported: 1 <= N <= 256, G divides D. */
+typedef enum { GDN_SSM_OPT_SOFTPLUS = 1 } gdn_ssm_option_t;
+
+typedef struct {
+  int64_t B, T, D, N, G;
+  int64_t x_stride_b, x_stride_t;
+  int64_t dt_stride_b, dt_stride_t;
+  int64_t z_stride_b, z_stride_t;
+  int64_t b_stride_b, b_stride_t;   /* rows of Bm */
+  int64_t c_stride_b, c_stride_t;   /* rows of Cm */
+  int64_t out_stride_b, out_stride_t;
+  int64_t slots;
+  int32_t dtype;             /* gdn_dtype_t: type of x, dt, z, Bm, Cm and out */
+  int32_t options;           /* 0 or GDN_SSM_OPT_SOFTPLUS */
+  const int32_t* seq_offsets;
+  const int32_t* state_index;
+  const void* z;
+  const float* dt_bias;
+  const float* skip;
+  void* stream;
+} gdn_ssm_problem_t;
+
+gdn_status_t gdn_ssm_forward(const gdn_ssm_problem_t* p, const void* x, const void* dt, const float* A,
+                             const void* Bm, const void* Cm, const float* state_in, float* state_out, void* out);
+
+/* One new token for each of B sequences (rows at b * stride_b; T, stride_t and
+ * seq_offsets are not used); `state` is read and advanced in place. */
+gdn_status_t gdn_ssm_step(const gdn_ssm_problem_t* p, const void* x, const void* dt, const float* A, const void* Bm,
+                          const void* Cm, float* state, void* out);
+
+/* Rotary positions on q and k.  Pair i < rot / 2 of every head is turned by
+ * the angle position * inv_freq[i], taken in 64 bits (off by at most 2^-51 of
+ * itself: below fp32's rounding for angles up to 2^26), and scaled:
+ *   (u, v) -> scale * (u cos - v sin, v cos + u sin)
+ * in the half layout (u, v) = (x[i], x[i + rot / 2]); with
+ * GDN_ROTARY_OPT_INTERLEAVED (x[2i], x[2i + 1]).  Channels from rot on pass
+ * through.  GDN_ROTARY_OPT_INVERSE turns back (the gradient of the call, with
+ * the same scale).
+ *   q, k        head h of token (b, t) at b * stride_b + t * stride_t +
+ *               h * stride_h, d contiguous channels; k may be NULL (Hk = 0)
+ *   q_out,k_out the same; each may be its input, with the input's strides
+ *   inv_freq    [rot / 2] fp64
+ *   positions   [axes, B, T], int32 or int64 (position_bits 32 or 64), or NULL
+ *               (position_bits 0, one axis): position0 + t.  With several axes
+ *               the first section[0] pairs take axis 0, the next section[1]
+ *               axis 1 and so on; the sections add up to rot / 2.
+ * Supported: rot even, 2 <= rot <= d <= 256, 1 to 4 axes, Hq, Hk <= 65536,
+ * B * T < 2^31. */
+typedef enum { GDN_ROTARY_OPT_INTERLEAVED = 1, GDN_ROTARY_OPT_INVERSE = 2 } gdn_rotary_option_t;
+
+typedef struct {
+  int64_t B, T, Hq, Hk, d, rot;
+  int64_t q_stride_b, q_stride_t, q_stride_h;
+  int64_t k_stride_b, k_stride_t, k_stride_h;
+  int64_t q_out_stride_b, q_out_stride_t, q_out_stride_h;
+  int64_t k_out_stride_b, k_out_stride_t, k_out_stride_h;
+  int64_t position0;
+  int32_t dtype;
+  int32_t options;
+  int32_t position_bits;
+  int32_t axes;
+  int32_t section[4];        /* pairs per axis */
+  float scale;
+  void* stream;
+} gdn_rotary_problem_t;
+
+gdn_status_t gdn_rotary(const gdn_rotary_problem_t* p, const void* q, const void* k, const double* inv_freq,
+                        const void* positions, void* q_out, void* k_out);
+
+/* The token scan's single-token step: one token of gdn_forward (forward
+ * direction) for each of B sequences, the state advanced in place:
+ *   S' = a S (I - beta k^ k^T) + beta v k^T,  o = S' q^
+ * with q^, k^ normalised and a = exp(log_alpha), as in gdn_forward.  Options:
+ * GDN_OPT_NO_ERASE and GDN_OPT_EXCLUSIVE_FORWARD (o = a S q^); gate,
+ * norm_weight and norm_eps are gdn_problem_t's readout epilogue.
+ *   q, k       [B, H, dk] (dtype); v, gate [B, H, dv] (dtype), 16-byte aligned
+ *   log_alpha, beta  [B, H] fp32
+ *   state      [slots, H, dv, dk] fp32, 16-byte aligned
+ *   out        [B, H, dv] fp32
+ * Supported: dk, dv in {64, 128}, B * H < 2^31. */
+typedef struct {
+  int64_t B, H, dk, dv;
+  int64_t slots;
+  int32_t dtype;
+  int32_t options;
+  const int32_t* state_index;
+  const void* gate;
+  const float* norm_weight;
+  float norm_eps;
+  void* stream;
+} gdn_step_problem_t;
+
+gdn_status_t gdn_step(const gdn_step_problem_t* p, const void* q, const void* k, const void* v,
+                      const float* log_alpha, const float* beta, float* state, float* out);
+
 /* Static description of a status code. */
 const char* gdn_status_string(int32_t status);
 
