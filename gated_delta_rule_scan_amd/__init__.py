@@ -55,8 +55,8 @@ GDN_ROTARY_OPT_INTERLEAVED = 1
 GDN_ROTARY_OPT_INVERSE = 2
 
 EXPORTED = ("gdn_workspace_bytes", "gdn_forward", "gdn_forward_noalloc", "gdn_vda_workspace_bytes", "gdn_vda_forward",
-            "gdn_conv_forward", "gdn_conv_step", "gdn_ssm_forward", "gdn_ssm_step", "gdn_rotary", "gdn_step",
-            "gdn_status_string", "gdn_version")
+            "gdn_conv_forward", "gdn_conv_step", "gdn_ssm_workspace_bytes", "gdn_ssm_forward", "gdn_ssm_step",
+            "gdn_rotary", "gdn_step", "gdn_status_string", "gdn_version")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # GDN_NOALLOC_SCRATCH_BYTES
 
 
@@ -112,6 +112,7 @@ class gdn_ssm_problem_t(ctypes.Structure):
         ("dtype", ctypes.c_int32), ("options", ctypes.c_int32),
         ("seq_offsets", ctypes.c_void_p), ("state_index", ctypes.c_void_p),
         ("z", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("skip", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("stream", ctypes.c_void_p),
     ]
 
@@ -179,6 +180,8 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.argtypes = [ctypes.POINTER(struct)] + [vp] * pointers
             fn.restype = ctypes.c_int
+        L.gdn_ssm_workspace_bytes.argtypes = [ctypes.POINTER(gdn_ssm_problem_t)]
+        L.gdn_ssm_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_status_string.argtypes = [ctypes.c_int32]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_version.argtypes = []
@@ -225,6 +228,10 @@ def gdn_conv_forward(problem: gdn_conv_problem_t, x, weight, bias, state_in, sta
 def gdn_conv_step(problem: gdn_conv_problem_t, x, weight, bias, state, out) -> int:
     """Raw call with integer device pointers (None for NULL); returns the status."""
     return lib().gdn_conv_step(ctypes.byref(problem), x, weight, bias, state, out)
+
+
+def gdn_ssm_workspace_bytes(problem: gdn_ssm_problem_t) -> int:
+    return lib().gdn_ssm_workspace_bytes(ctypes.byref(problem))
 
 
 def gdn_ssm_forward(problem: gdn_ssm_problem_t, x, dt, A, Bm, Cm, state_in, state_out, out) -> int:

@@ -43,7 +43,21 @@ struct SsmArgs {
   int64_t B, T, D, N, G, slots;
   int64_t x_sb, x_st, dt_sb, dt_st, z_sb, z_st, b_sb, b_st, c_sb, c_st, o_sb, o_st;
   int softplus;
+  // prompts: tokens per chunk, chunks of an unpacked sequence, and where
+  // sequences are split (else null) the workspace: chunk end states, then
+  // entering states [item][N][D], and sums of step sizes [item][D]
+  int64_t chunk, chunks;
+  float* ends;
+  float* steps;
 };
+
+// How a selective scan over prompts is split, and the workspace that takes.
+struct SsmPlan {
+  bool split;
+  int64_t chunk, chunks;
+  size_t ends_bytes, total_bytes;
+};
+SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool packed);
 
 struct RotaryArgs {
   const void* q;

@@ -157,17 +157,25 @@ gdn_status_t conv_check(const gdn_conv_problem_t* p, bool step, const void* x, c
   return GDN_OK;
 }
 
-gdn_status_t ssm_check(const gdn_ssm_problem_t* p, bool step, const void* x, const void* dt, const float* A,
-                       const void* Bm, const void* Cm, const float* state_in, const float* state_out, const void* out,
-                       SsmArgs* a) {
+// the sizes and options alone
+gdn_status_t ssm_sizes(const gdn_ssm_problem_t* p, bool step) {
   if (!p) return GDN_ERR_INVALID_ARGUMENT;
   const int64_t B = p->B, T = step ? 1 : p->T, D = p->D, N = p->N, G = p->G;
-  const int32_t* off = step ? nullptr : p->seq_offsets;
   if (B < 1 || B > kMost || T < 0 || T > kMost || D < 1 || D > kMost || N < 1 || G < 1 || G > D || D % G != 0)
     return GDN_ERR_INVALID_ARGUMENT;
   if (p->options & ~GDN_SSM_OPT_SOFTPLUS) return GDN_ERR_INVALID_ARGUMENT;
   if (p->dtype != GDN_DTYPE_F32 && p->dtype != GDN_DTYPE_BF16) return GDN_ERR_UNSUPPORTED;
   if (N > 256) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+gdn_status_t ssm_check(const gdn_ssm_problem_t* p, bool step, const void* x, const void* dt, const float* A,
+                       const void* Bm, const void* Cm, const float* state_in, const float* state_out, const void* out,
+                       SsmArgs* a) {
+  const gdn_status_t sizes = ssm_sizes(p, step);
+  if (sizes != GDN_OK) return sizes;
+  const int64_t B = p->B, T = step ? 1 : p->T, D = p->D, N = p->N, G = p->G;
+  const int32_t* off = step ? nullptr : p->seq_offsets;
   const int64_t sb[6] = {p->x_stride_b, p->dt_stride_b, p->b_stride_b, p->c_stride_b, p->out_stride_b,
                          p->z ? p->z_stride_b : 0};
   int64_t st[6] = {p->x_stride_t, p->dt_stride_t, p->b_stride_t, p->c_stride_t, p->out_stride_t, p->z ? p->z_stride_t : 0};
@@ -191,18 +199,31 @@ gdn_status_t ssm_check(const gdn_ssm_problem_t* p, bool step, const void* x, con
   if (!r_o.fits() || !r_s.fits() || r_o.meets_itself()) return GDN_ERR_INVALID_ARGUMENT;
   const int64_t sbytes = state ? r_s.extent(r_s.dims) : 0;
   const Rows so(state_out, sbytes);
+  SsmPlan plan = {};
+  if (!step) plan = ssm_plan(B, T, D, N, G, off != nullptr);
+  const Rows ws(plan.split ? p->workspace : nullptr, (int64_t)plan.total_bytes);
+  if (plan.split) {
+    if (!p->workspace || !is_aligned(p->workspace, 256)) return GDN_ERR_INVALID_ARGUMENT;
+    if (p->workspace_bytes < plan.total_bytes) return GDN_ERR_WORKSPACE_TOO_SMALL;
+  }
   for (int i = 0; i < 6; ++i) {
     if (i == 4) continue;
     const Rows r = token_rows(typed[i], len[i], es, B, sb[i], T, st[i], off);
-    if (!r.fits() || meet(r_o, r) || meet(so, r)) return GDN_ERR_INVALID_ARGUMENT;
+    if (!r.fits() || meet(r_o, r) || meet(so, r) || meet(ws, r)) return GDN_ERR_INVALID_ARGUMENT;
   }
+  if (meet(ws, r_o) || meet(ws, so) || meet(ws, Rows(state_in, sbytes))) return GDN_ERR_INVALID_ARGUMENT;
   const Rows ins[] = {Rows(A, D * N * 4), Rows(p->dt_bias, D * 4), Rows(p->skip, D * 4), Rows(off, (B + 1) * 4),
                       Rows(p->state_index, B * 4)};
   for (const Rows& r : ins)
-    if (meet(r_o, r) || meet(so, r)) return GDN_ERR_INVALID_ARGUMENT;
+    if (meet(r_o, r) || meet(so, r) || meet(ws, r)) return GDN_ERR_INVALID_ARGUMENT;
   if (meet(r_o, Rows(state_in, sbytes)) || meet(r_o, so)) return GDN_ERR_INVALID_ARGUMENT;
   if (!state_pair_ok(state_in, state_out, sbytes)) return GDN_ERR_INVALID_ARGUMENT;
   memset(a, 0, sizeof(*a));
+  a->chunk = plan.chunk; a->chunks = plan.chunks;
+  if (plan.split) {
+    a->ends = static_cast<float*>(p->workspace);
+    a->steps = reinterpret_cast<float*>(static_cast<unsigned char*>(p->workspace) + plan.ends_bytes);
+  }
   a->x = x; a->dt = dt; a->A = A; a->Bm = Bm; a->Cm = Cm; a->z = p->z; a->dt_bias = p->dt_bias; a->skip = p->skip;
   a->state_in = state_in; a->state_out = const_cast<float*>(state_out); a->out = const_cast<void*>(out);
   a->off = off; a->index = p->state_index;
@@ -239,6 +260,11 @@ extern "C" gdn_status_t gdn_conv_step(const gdn_conv_problem_t* p, const void* x
   hipStream_t stream = static_cast<hipStream_t>(p->stream);
   return launched(p->dtype == GDN_DTYPE_BF16 ? launch_conv_step<bf16>(a, p->width, aligned, stream)
                                              : launch_conv_step<float>(a, p->width, aligned, stream));
+}
+
+extern "C" size_t gdn_ssm_workspace_bytes(const gdn_ssm_problem_t* p) {
+  if (ssm_sizes(p, false) != GDN_OK) return 0;
+  return ssm_plan(p->B, p->T, p->D, p->N, p->G, p->seq_offsets != nullptr).total_bytes;
 }
 
 extern "C" gdn_status_t gdn_ssm_forward(const gdn_ssm_problem_t* p, const void* x, const void* dt, const float* A,

@@ -15,306 +15,250 @@ __device__ __forceinline__ float step_size(const SsmArgs& a, float dt, float bia
 
 // ---- prompts ----
 // The decay depends on channel and state entry, so nothing here is a product
-// of matrices: per token, channel and entry a pass needs one exponential
-// (quarter rate), the products dt A and dt x B, the update and the readout --
-// bound by the vector units, not by memory.  What counts is to take that
-// exponential once although the scan over time has to be split over lanes:
+// of matrices: per token, channel and entry a pass takes one exponential (two
+// issue slots), the products dt A and dt x B, the update and the readout --
+// bound by the vector units, not by memory.
 //
-// A wave takes one channel; lane l takes K consecutive tokens of a tile of
-// 64 K.  For every state entry n in turn, it computes its K decays a and
-// inputs b (kept in registers), scans them from zero to the lane's end value
-// H with P = exp(A sum dt), combines (P, H) over the lanes by a wave-wide
-// prefix scan on data-parallel row shifts (the carried state enters through
-// lane 0), and runs through the same K registers again from the value that
-// enters its lane, adding C h to the K readouts.  The state leaves the tile in
-// lane 63.  Tokens behind the sequence's end have dt = 0 and B = C = 0:
-// decay 1, no input.
+// A lane owns a channel and NN state entries in registers and walks the tokens
+// in order, so rows of x, dt, z and out move in whole cache lines; the B and C
+// of kStage tokens wait in LDS as fp32 and reach every lane by broadcast
+// reads.  CT waves of a workgroup take neighbouring channel tiles of the same
+// tokens; more than NN entries are split over waves, whose partial readouts
+// meet in LDS.
 //
-// A workgroup takes CH neighbouring channels (CH waves), which share the B
-// and C of a tile: those are staged in LDS as fp32, four entries at a time,
-// double-buffered, each entry's tokens in the order the lanes read them (16
-// bytes a lane, neighbouring lanes in different banks).  Rows of x, dt and z
-// come in as CH channels of a token and are turned into a lane's K tokens of
-// one channel through whichever half of that buffer is free; the output goes
-// back the same way.
+// Too few channels to fill the GPU: sequences are cut into chunks and three
+// kernels run.  The first (STATES) finds each chunk's end state from a zero
+// start, and the sum of its step sizes: a chunk's whole decay is exp(A sum
+// dt).  The second (carry) turns those into the state that enters each chunk;
+// the third is the scan itself from there.  The first costs the exponentials
+// once more, about 0.7 of the scan; a sequence's last chunk, and with it a
+// sequence of one chunk, is spared it.
 
-constexpr int kMaxN = 256;
-constexpr int kGroup = 4;  // state entries staged at a time
+constexpr int kStage = 16;  // tokens whose B and C are staged at a time
+constexpr int kAhead = 4;   // tokens of x, dt and z in flight per lane
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float shifted(float old, float x) {
-  return __builtin_bit_cast(
-      float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, x), CTRL, ROWS, 0xF, false));
-}
-
-// (P, H) of each lane becomes that of all lanes up to it (P is spent)
-template <int CTRL, int ROWS>
-__device__ __forceinline__ void scan_step(float& P, float& H) {
-  H = fmaf(P, shifted<CTRL, ROWS>(0.0f, H), H);
-  P = P * shifted<CTRL, ROWS>(1.0f, P);
-}
-__device__ __forceinline__ float wave_scan(float P, float H) {
-  scan_step<0x111, 0xF>(P, H);  // from 1, 2, 4, 8 lanes back within a row of 16
-  scan_step<0x112, 0xF>(P, H);
-  scan_step<0x114, 0xF>(P, H);
-  scan_step<0x118, 0xF>(P, H);
-  scan_step<0x142, 0xA>(P, H);  // last lane of the row before, into rows 1 and 3
-  return fmaf(P, shifted<0x143, 0xC>(0.0f, H), H);  // lane 31, into rows 2 and 3
-}
-
-// Where token t of a tile lies in a staged entry: lanes read 16-byte pieces
-// j = 0 .. K / 4 - 1 of their K tokens, and a rotation of j by lane keeps the
-// 16 lanes of a bank cycle apart.
-template <int K>
-__device__ __forceinline__ int piece_of(int lane, int j) {
-  const int turn = K == 16 ? (lane >> 2) & 3 : K == 8 ? (lane >> 3) & 1 : 0;
-  return lane * (K / 4) + (j ^ turn);
-}
-template <int K>
-__device__ __forceinline__ int place_of(int t) {
-  return piece_of<K>(t / K, (t % K) / 4) * 4 + t % 4;
-}
-
-// CH neighbouring channels of one token row
-template <typename MT, int CH>
-struct __attribute__((aligned(CH * sizeof(MT) > 16 ? 16 : CH * sizeof(MT)))) Row {
-  MT e[CH];
+struct Chunk {
+  int64_t b;            // sequence
+  int64_t item;         // its place in the workspace
+  int64_t t0, t1, len;  // tokens of the sequence
+  int64_t row0;         // first row of a packed sequence
+  bool work;
 };
 
-template <typename MT, int K, int CH>
-__global__ __launch_bounds__(CH * 64, K == 16 ? 2 : 4) void ssm_kernel(SsmArgs a, int tiles_per_group, int row_vec, int bc_vec) {
-  constexpr int TT = 64 * K, THREADS = 64 * CH;
-  constexpr int ROWS = (TT + THREADS - 1) / THREADS;          // token rows a thread moves per tile and operand
-  constexpr int ITEMS = (2 * TT + THREADS - 1) / THREADS;     // (token, B or C) pieces a thread stages per group
-  constexpr int HALF = 2 * kGroup * TT;                       // floats of one staging buffer
-  static_assert(CH * TT * 4 <= HALF * 4, "a tile of one operand fits a free buffer");
-  __shared__ __align__(16) float lds[2 * HALF];               // [2][B, C][kGroup][TT]
-  __shared__ float carry[CH * kMaxN];                         // [CH][N]: the states between tiles
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
-  // Workgroups are dealt to the eight chiplets in turn; each chiplet takes a
-  // run of neighbouring channel tiles, whose rows share cache lines.
-  const unsigned nblk = gridDim.x, xcd = blockIdx.x & 7, pos = blockIdx.x >> 3;
-  const unsigned blk = xcd * (nblk / 8) + (xcd < (nblk & 7) ? xcd : nblk & 7) + pos;
-  const int64_t tiles = (int64_t)tiles_per_group * a.G;
-  const int64_t b = blk / tiles;
-  const int ct = (int)(blk % tiles), g = ct / tiles_per_group;
-  const int64_t per = a.D / a.G, d0 = g * per + (int64_t)(ct % tiles_per_group) * CH;
-  const int nch = (int)(g * per + per - d0 < CH ? g * per + per - d0 : CH);
-  const int N = (int)a.N;
-
-  int64_t r0 = 0, len = a.T;
+__device__ __forceinline__ Chunk chunk_of(const SsmArgs& a, int64_t item) {
+  Chunk c;
+  c.item = item;
+  int64_t k;
   if (a.off) {
-    r0 = clamp64(a.off[b], 0, a.T);
-    len = clamp64(a.off[b + 1], r0, a.T) - r0;
+    const SeqItem s = find_packed(a.off, a.B, a.T, a.chunk, item);
+    c.b = s.b;
+    c.len = s.len;
+    c.row0 = s.row0;
+    k = s.chunk;
+  } else {
+    c.b = item / a.chunks;
+    k = item - c.b * a.chunks;
+    c.len = a.T;
+    c.row0 = 0;
   }
-  auto base = [&](int64_t sb, int64_t st) { return a.off ? r0 * st : b * sb; };
+  c.t0 = k * a.chunk;
+  c.t1 = c.t0 + a.chunk < c.len ? c.t0 + a.chunk : c.len;
+  c.work = k >= 0 && (c.t0 < c.len || k == 0);
+  return c;
+}
+
+template <typename MT, int NN, int CT, bool STATES>
+__global__ __launch_bounds__(1024) void ssm_kernel(SsmArgs a, int NG, int tiles_per_group) {
+  extern __shared__ __align__(16) float lds[];  // [kStage][B, C][NG * NN], then partial readouts
+  const int NP = NG * NN, N = (int)a.N;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ng = wave / CT, ct = wave % CT;     // this wave's entries and channel tile
+  const unsigned tiles = (unsigned)tiles_per_group * (unsigned)a.G;
+  const Chunk c = chunk_of(a, blockIdx.x / tiles);
+  if (!c.work) return;
+  if (STATES && c.t1 >= c.len) return;  // nothing follows the last chunk
+  const unsigned tile = blockIdx.x % tiles, g = tile / (unsigned)tiles_per_group;
+  // the wave's first channel (uniform) and the lane's behind it; lanes without
+  // a channel repeat the group's last one and store nothing
+  const int64_t per = a.D / a.G, end = (g + 1) * per;
+  const int64_t want = g * per + ((int64_t)(tile % (unsigned)tiles_per_group) * CT + ct) * 64;
+  const int64_t d0 = want < end ? want : end - 1;
+  const bool live = want + lane < end;
+  const unsigned dl = live ? lane : (unsigned)(end - 1 - d0);
+  const int64_t d = d0 + dl;
+  const int64_t slot = slot_of(a.index, c.b, a.slots);
+
+  auto base = [&](int64_t sb, int64_t st) { return a.off ? c.row0 * st : c.b * sb; };
   const MT* x = static_cast<const MT*>(a.x) + base(a.x_sb, a.x_st) + d0;
   const MT* dt = static_cast<const MT*>(a.dt) + base(a.dt_sb, a.dt_st) + d0;
   const MT* z = a.z ? static_cast<const MT*>(a.z) + base(a.z_sb, a.z_st) + d0 : nullptr;
-  const MT* Bm = static_cast<const MT*>(a.Bm) + base(a.b_sb, a.b_st) + g * a.N;
-  const MT* Cm = static_cast<const MT*>(a.Cm) + base(a.c_sb, a.c_st) + g * a.N;
   MT* out = static_cast<MT*>(a.out) + base(a.o_sb, a.o_st) + d0;
-  const int64_t slot = slot_of(a.index, b, a.slots);
-
-  for (int i = tid; i < nch * N; i += THREADS)
-    carry[i] = a.state_in && slot >= 0 ? a.state_in[(slot * a.D + d0) * N + i] : 0.0f;
-
-  // ---- staging ----
-  auto load_rows = [&](const MT* p, int64_t st, int64_t t0, Row<MT, CH>* r) {
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const int t = tid + i * THREADS;
-      if (t < TT && t0 + t < len) {
-        if (row_vec) {
-          r[i] = *reinterpret_cast<const Row<MT, CH>*>(p + (t0 + t) * st);
-        } else {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) r[i].e[c] = c < nch ? p[(t0 + t) * st + c] : (MT)0.0f;
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) r[i].e[c] = (MT)0.0f;
-      }
-    }
-  };
-  // rows <-> a lane's tokens, through an LDS buffer of [CH][TT] elements
-  auto rows_to_lds = [&](MT* buf, const Row<MT, CH>* r) {
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const int t = tid + i * THREADS;
-      if (t < TT) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) buf[c * TT + (sizeof(MT) == 4 ? place_of<K>(t) : t)] = r[i].e[c];
-      }
-    }
-  };
-  auto own_tokens = [&](MT* buf, MT* v) {
-#pragma unroll
-    for (int j = 0; j < K / 4; ++j) {
-      MT* p = buf + wave * TT + (sizeof(MT) == 4 ? piece_of<K>(lane, j) * 4 : lane * K + j * 4);
-      __builtin_memcpy(v + j * 4, __builtin_assume_aligned(p, 4 * sizeof(MT)), 4 * sizeof(MT));
-    }
-  };
-  auto own_tokens_back = [&](MT* buf, const MT* v) {
-#pragma unroll
-    for (int j = 0; j < K / 4; ++j) {
-      MT* p = buf + wave * TT + (sizeof(MT) == 4 ? piece_of<K>(lane, j) * 4 : lane * K + j * 4);
-      __builtin_memcpy(__builtin_assume_aligned(p, 4 * sizeof(MT)), v + j * 4, 4 * sizeof(MT));
-    }
-  };
-  struct __attribute__((aligned(4 * sizeof(MT)))) Quad {
-    MT e[kGroup];
-  };
-  auto load_bc = [&](int64_t t0, int n0, Quad* q) {
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int it = tid + i * THREADS, t = it % TT;
-#pragma unroll
-      for (int e = 0; e < kGroup; ++e) q[i].e[e] = (MT)0.0f;
-      if (it < 2 * TT && t0 + t < len) {
-        const MT* p = (it < TT ? Bm + (t0 + t) * a.b_st : Cm + (t0 + t) * a.c_st) + n0;
-        if (bc_vec) {
-          q[i] = *reinterpret_cast<const Quad*>(p);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kGroup; ++e)
-            if (n0 + e < N) q[i].e[e] = p[e];
-        }
-      }
-    }
-  };
-  auto store_bc = [&](float* buf, const Quad* q) {
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int it = tid + i * THREADS, t = it % TT;
-      if (it < 2 * TT) {
-        float* p = buf + (it < TT ? 0 : kGroup * TT) + place_of<K>(t);
-#pragma unroll
-        for (int e = 0; e < kGroup; ++e) p[e * TT] = to_float(q[i].e[e]);
-      }
-    }
-  };
-
-  const int groups = (N + kGroup - 1) / kGroup;
-  const int64_t d = d0 + (wave < nch ? wave : 0);  // idle waves of a partial tile compute, but store nothing
   const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f, skip = a.skip ? a.skip[d] : 0.0f;
-  const float* A = a.A + d * N;
 
-  Quad q[ITEMS];
-  Row<MT, CH> rx[ROWS], rd[ROWS], rz[ROWS];
-  load_bc(0, 0, q);
-  load_rows(x, a.x_st, 0, rx);
-  load_rows(dt, a.dt_st, 0, rd);
-  store_bc(lds, q);
-  int s = 0;  // group s is staged in buffer s & 1
-  for (int64_t t0 = 0; t0 < len; t0 += TT) {
-    MT* turn = reinterpret_cast<MT*>(lds + ((s + 1) & 1) * HALF);  // the free buffer
-    float dts[K], u[K], y[K], total = 0.0f;
-    {
-      MT v[K];
-      rows_to_lds(turn, rx);
-      __syncthreads();
-      own_tokens(turn, v);
-      __syncthreads();
+  float A[NN], h[NN];
 #pragma unroll
-      for (int k = 0; k < K; ++k) u[k] = to_float(v[k]);
-      rows_to_lds(turn, rd);
-      __syncthreads();
-      own_tokens(turn, v);
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const bool in = t0 + lane * K + k < len;
-        dts[k] = in ? step_size(a, to_float(v[k]), bias) : 0.0f;
-        y[k] = skip * u[k];
-        u[k] *= dts[k];
-        total += dts[k];
-      }
+  for (int i = 0; i < NN; ++i) {
+    const int n = ng * NN + i;
+    const bool in = n < N;
+    A[i] = in ? a.A[d * N + n] * kLog2e : 0.0f;
+    h[i] = 0.0f;
+    if (!STATES && in) {
+      if (a.ends) h[i] = a.ends[(c.item * N + n) * a.D + d];
+      else if (a.state_in && slot >= 0) h[i] = a.state_in[(slot * a.D + d) * N + n];
     }
-    if (z) load_rows(z, a.z_st, t0, rz);
-    for (int gr = 0; gr < groups; ++gr, ++s) {
-      const bool last = gr + 1 == groups;
-      const float* buf = lds + (s & 1) * HALF;
-      load_bc(last ? t0 + TT : t0, last ? 0 : (gr + 1) * kGroup, q);  // behind the end: zeros
-      if (last) {
-        load_rows(x, a.x_st, t0 + TT, rx);
-        load_rows(dt, a.dt_st, t0 + TT, rd);
-      }
-      const int most = N - gr * kGroup < kGroup ? N - gr * kGroup : kGroup;
+  }
+
+  // B and C of kStage tokens: one element a thread and round; a round covers
+  // whole tokens, so a thread keeps its column
+  constexpr int STEP = CT * 64 / (2 * NN), ROUNDS = kStage / STEP;
+  static_assert(kStage % STEP == 0 && STEP > 0, "rounds cover the stage");
+  const int col = tid % (2 * NP), first = tid / (2 * NP);
+  const bool isC = col >= NP;
+  const int n_col = isC ? col - NP : col;
+  const bool stages = n_col < N && !(STATES && isC);
+  const int64_t bc_st = isC ? a.c_st : a.b_st;
+  const MT* bc = static_cast<const MT*>(isC ? a.Cm : a.Bm) + (isC ? base(a.c_sb, a.c_st) : base(a.b_sb, a.b_st)) +
+                 g * a.N + (n_col < N ? n_col : 0);
+  MT sv[ROUNDS];
+  auto load_bc = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int64_t u = t + first + i * STEP;
+      sv[i] = stages && u < c.t1 ? bc[u * bc_st] : (MT)0.0f;
+    }
+  };
+  // x, dt and z of kAhead tokens; past the end the last token repeats
+  MT xv[kAhead], dv[kAhead], zv[kAhead];
+  auto load_rows = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t u = t + i < c.t1 ? t + i : c.t1 - 1;
+      xv[i] = (x + u * a.x_st)[dl];
+      dv[i] = (dt + u * a.dt_st)[dl];
+      if (!STATES && NG == 1) zv[i] = z ? (z + u * a.z_st)[dl] : (MT)0.0f;
+    }
+  };
+
+  float total = 0.0f;
+  if (c.t0 < c.t1) {
+    load_bc(c.t0);
+    load_rows(c.t0);
+  }
+  for (int64_t tb = c.t0; tb < c.t1; tb += kStage) {
+    __syncthreads();  // the stage before is read
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) lds[(first + i * STEP) * 2 * NP + col] = to_float(sv[i]);
+    __syncthreads();
+    if (tb + kStage < c.t1) load_bc(tb + kStage);
 #pragma unroll 1
-      for (int e = 0; e < most; ++e) {
-        const int n = gr * kGroup + e;
-        const float A2 = A[n] * kLog2e, h0 = carry[wave * N + n];
-        float dec[K], in[K];
+    for (int part = 0; part < kStage && tb + part < c.t1; part += kAhead) {
+      const int64_t t = tb + part;
+      MT xc[kAhead], dc[kAhead], zc[kAhead];
 #pragma unroll
-        for (int j = 0; j < K / 4; ++j) {
-          const f32x4 B = *reinterpret_cast<const f32x4*>(buf + e * TT + piece_of<K>(lane, j) * 4);
+      for (int i = 0; i < kAhead; ++i) {
+        xc[i] = xv[i];
+        dc[i] = dv[i];
+        zc[i] = zv[i];
+      }
+      if (t + kAhead < c.t1) load_rows(t + kAhead);
+      float* partial = lds + kStage * 2 * NP + wave * kAhead * 64 + lane;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) in[j * 4 + i] = u[j * 4 + i] * B[i];
-        }
-        float H = 0.0f;
+      for (int i = 0; i < kAhead; ++i) {
+        const float xi = to_float(xc[i]);
+        const float s = t + i < c.t1 ? step_size(a, to_float(dc[i]), bias) : 0.0f;  // past the end: decay 1, no input
+        const float u = s * xi;
+        if (STATES) total += s;
+        const float* bcl = lds + (part + i) * 2 * NP + ng * NN;
+        float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          dec[k] = hw_exp2(dts[k] * A2);
-          H = fmaf(dec[k], H, in[k]);
-        }
-        const float P = hw_exp2(total * A2);
-        if (lane == 0) H = fmaf(P, h0, H);
-        H = wave_scan(P, H);
-        float h = shifted<0x138, 0xF>(h0, H);  // the lane before's; lane 0 starts from the carried state
-        if (lane == 63 && wave < nch) carry[wave * N + n] = H;
+        for (int j = 0; j < NN / 4; ++j) {
+          const f32x4 B = *reinterpret_cast<const f32x4*>(bcl + 4 * j);
+          f32x4 C = {0.f, 0.f, 0.f, 0.f};
+          if (!STATES) C = *reinterpret_cast<const f32x4*>(bcl + NP + 4 * j);
 #pragma unroll
-        for (int j = 0; j < K / 4; ++j) {
-          const f32x4 C = *reinterpret_cast<const f32x4*>(buf + (kGroup + e) * TT + piece_of<K>(lane, j) * 4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = j * 4 + i;
-            h = fmaf(dec[k], h, in[k]);
-            y[k] = fmaf(C[i], h, y[k]);
+          for (int m = 0; m < 4; ++m) {
+            const int n = 4 * j + m;
+            h[n] = fmaf(hw_exp2(s * A[n]), h[n], u * B[m]);
+            if (!STATES) {
+              if (m & 1) y1 = fmaf(h[n], C[m], y1);
+              else y0 = fmaf(h[n], C[m], y0);
+            }
           }
         }
-      }
-      store_bc(lds + ((s + 1) & 1) * HALF, q);
-      __syncthreads();
-    }
-    // readouts: gate, and back to rows
-    turn = reinterpret_cast<MT*>(lds + ((s + 1) & 1) * HALF);
-    MT v[K];
-    if (z) {
-      rows_to_lds(turn, rz);
-      __syncthreads();
-      own_tokens(turn, v);
-#pragma unroll
-      for (int k = 0; k < K; ++k) y[k] *= silu(to_float(v[k]));
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = (MT)y[k];
-    own_tokens_back(turn, v);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const int t = tid + i * THREADS;
-      if (t < TT && t0 + t < len) {
-        Row<MT, CH> r;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) r.e[c] = turn[c * TT + (sizeof(MT) == 4 ? place_of<K>(t) : t)];
-        MT* p = out + (t0 + t) * a.o_st;
-        if (row_vec) {
-          *reinterpret_cast<Row<MT, CH>*>(p) = r;
-        } else {
-#pragma unroll
-          for (int c = 0; c < CH; ++c)
-            if (c < nch) p[c] = r.e[c];
+        if (!STATES) {
+          if (NG == 1) {
+            float y = fmaf(skip, xi, y0 + y1);
+            if (z) y *= silu(to_float(zc[i]));
+            if (live && t + i < c.t1) (out + (t + i) * a.o_st)[dl] = (MT)y;
+          } else {
+            partial[i * 64] = y0 + y1;
+          }
         }
+        __builtin_amdgcn_sched_barrier(0);  // one token's operands in registers at a time
+      }
+      if (!STATES && NG > 1) {
+        // the waves of a channel tile share out the tokens' sums
+        __syncthreads();
+        for (int i = ng; i < kAhead; i += NG) {
+          const int64_t u = t + i;
+          if (u >= c.t1) break;
+          const float* p = lds + kStage * 2 * NP + (ct * kAhead + i) * 64 + lane;
+          float y = skip * to_float((x + u * a.x_st)[dl]);
+          for (int k = 0; k < NG; ++k) y += p[k * CT * kAhead * 64];
+          if (z) y *= silu(to_float((z + u * a.z_st)[dl]));
+          if (live) (out + u * a.o_st)[dl] = (MT)y;
+        }
+        __syncthreads();
       }
     }
-    __syncthreads();
   }
-  __syncthreads();
-  if (a.state_out && slot >= 0)
-    for (int i = tid; i < nch * N; i += THREADS) a.state_out[(slot * a.D + d0) * N + i] = carry[i];
+  if (STATES) {
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < NN; ++i)
+      if (ng * NN + i < N) a.ends[(c.item * N + ng * NN + i) * a.D + d] = h[i];
+    if (ng == 0) a.steps[c.item * a.D + d] = total;
+  } else if (a.state_out && slot >= 0 && live && c.t1 >= c.len) {
+#pragma unroll
+    for (int i = 0; i < NN; ++i)
+      if (ng * NN + i < N) a.state_out[(slot * a.D + d) * N + ng * NN + i] = h[i];
+  }
+}
+
+// Chunk end states become entering states, in place: a thread per channel and
+// state entry of a sequence walks its chunks.
+constexpr int kCarry = 8;  // chunks in flight
+
+__global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, DN = a.D * a.N;
+  if (i >= a.B * DN) return;
+  const int64_t b = i / DN, r = i - b * DN, n = r / a.D, d = r - n * a.D;
+  int64_t item0 = b * a.chunks, len = a.T;
+  if (a.off) {
+    const int64_t row0 = clamp64(a.off[b], 0, a.T);
+    item0 = row0 / a.chunk + b;
+    len = clamp64(a.off[b + 1], row0, a.T) - row0;
+  }
+  const int64_t chunks = len > a.chunk ? (len + a.chunk - 1) / a.chunk : 1;
+  const int64_t slot = slot_of(a.index, b, a.slots);
+  const float A = a.A[d * a.N + n] * kLog2e;
+  float h = a.state_in && slot >= 0 ? a.state_in[(slot * a.D + d) * a.N + n] : 0.0f;
+  float* ends = a.ends + (item0 * a.N + n) * a.D + d;
+  const float* steps = a.steps + item0 * a.D + d;
+  for (int64_t c = 0; c < chunks; c += kCarry) {
+    float e[kCarry], s[kCarry];
+#pragma unroll
+    for (int k = 0; k < kCarry; ++k) {
+      const bool in = c + k < chunks - 1;  // the last chunk has no end state here
+      e[k] = in ? ends[(c + k) * DN] : 0.0f;
+      s[k] = in ? steps[(c + k) * a.D] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < kCarry; ++k) {
+      if (c + k < chunks) ends[(c + k) * DN] = h;
+      h = fmaf(hw_exp2(s[k] * A), h, e[k]);
+    }
+  }
 }
 
 // One token per sequence: 1 << lanes_log2 lanes share a channel, each taking V
@@ -357,37 +301,61 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <typename MT, int K, int CH>
+template <typename MT, int NN, int CT>
 hipError_t ssm_launch(const SsmArgs& a, hipStream_t stream) {
-  const int64_t per = a.D / a.G, tiles = (per + CH - 1) / CH, blocks = a.B * a.G * tiles;
-  if (!grid_fits(blocks, CH * 64) || tiles * a.G > 0x7FFFFFFF) return hipErrorNotSupported;
-  auto rows_ok = [&](const void* p, int64_t sb, int64_t st, size_t bytes) {
-    return !p || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && st * sizeof(MT) % bytes == 0 &&
-                  (a.off || a.B == 1 || sb * sizeof(MT) % bytes == 0));
-  };
-  constexpr size_t row = CH * sizeof(MT) > 16 ? 16 : CH * sizeof(MT), quad = kGroup * sizeof(MT);
-  const int row_vec = per % CH == 0 && rows_ok(a.x, a.x_sb, a.x_st, row) && rows_ok(a.dt, a.dt_sb, a.dt_st, row) &&
-                      rows_ok(a.z, a.z_sb, a.z_st, row) && rows_ok(a.out, a.o_sb, a.o_st, row);
-  const int bc_vec = a.N % kGroup == 0 && rows_ok(a.Bm, a.b_sb, a.b_st, quad) && rows_ok(a.Cm, a.c_sb, a.c_st, quad);
-  hipLaunchKernelGGL((ssm_kernel<MT, K, CH>), dim3((unsigned)blocks), dim3(CH * 64), 0, stream, a, (int)tiles,
-                     row_vec, bc_vec);
+  const int64_t per = a.D / a.G, tiles = (per + 64 * CT - 1) / (64 * CT);
+  const int NG = (int)((a.N + NN - 1) / NN), threads = NG * CT * 64;
+  const int64_t items = a.off ? a.T / a.chunk + a.B : a.B * a.chunks, blocks = items * a.G * tiles;
+  const int64_t carries = (a.B * a.D * a.N + 255) / 256;
+  if (!grid_fits(blocks, threads) || !grid_fits(carries, 256) || tiles > 0x7FFFFFFF) return hipErrorNotSupported;
+  const size_t stage = (size_t)kStage * 2 * NG * NN * sizeof(float);
+  const size_t partials = NG > 1 ? (size_t)NG * CT * kAhead * 64 * sizeof(float) : 0;
+  if (a.ends) {
+    hipLaunchKernelGGL((ssm_kernel<MT, NN, CT, true>), dim3((unsigned)blocks), dim3(threads), (unsigned)stage, stream, a,
+                       NG, (int)tiles);
+    hipLaunchKernelGGL(ssm_carry_kernel, dim3((unsigned)carries), dim3(256), 0, stream, a);
+  }
+  hipLaunchKernelGGL((ssm_kernel<MT, NN, CT, false>), dim3((unsigned)blocks), dim3(threads), (unsigned)(stage + partials),
+                     stream, a, NG, (int)tiles);
   return hipGetLastError();
-}
-
-template <typename MT, int K>
-hipError_t ssm_for(const SsmArgs& a, hipStream_t stream) {
-  return ssm_launch<MT, K, 8>(a, stream);
 }
 
 }  // namespace
 
+SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool packed) {
+  SsmPlan p;
+  const int64_t waves = G * ((D / G + 63) / 64) * ((N + 15) / 16);  // of one sequence
+  const int64_t rows = packed ? T : B * T;
+  p.split = packed || B * waves < 768;
+  int64_t chunk = (rows * waves / 4096 + kStage - 1) / kStage * kStage;
+  if (chunk < 64) chunk = 64;
+  if (chunk < T / 128) chunk = (T / 128 + kStage) / kStage * kStage;
+  if (!p.split || chunk >= T) {
+    p.split = false;
+    chunk = T < 1 ? 1 : T;
+  }
+  p.chunk = chunk;
+  p.chunks = T < 1 ? 1 : (T + chunk - 1) / chunk;
+  p.ends_bytes = p.total_bytes = 0;
+  if (p.split) {
+    const int64_t items = packed ? T / chunk + B : B * p.chunks;
+    // (no overflow: a split leaves D N below 2^23)
+    const size_t entries = (size_t)(items * D);
+    p.ends_bytes = align_up(entries * N * 4, 256);
+    p.total_bytes = p.ends_bytes + align_up(entries * 4, 256);
+  }
+  return p;
+}
+
 template <typename MT>
 hipError_t launch_ssm(const SsmArgs& a, hipStream_t stream) {
-  // tokens per lane: the fewest whose tile holds an ordinary sequence
-  const int64_t T = a.off ? (a.T + a.B - 1) / a.B : a.T;
-  if (T <= 256) return ssm_for<MT, 4>(a, stream);
-  if (T <= 512) return ssm_for<MT, 8>(a, stream);
-  return ssm_for<MT, 16>(a, stream);
+  // channel tiles per workgroup: four waves' worth, fewer where the entries
+  // already split over waves or the group has fewer channels
+  const int64_t tiles = (a.D / a.G + 63) / 64;
+  if (a.N <= 8) return ssm_launch<MT, 8, 4>(a, stream);
+  if (a.N <= 16 && tiles > 2) return ssm_launch<MT, 16, 4>(a, stream);
+  if (a.N <= 32 && tiles > 1) return ssm_launch<MT, 16, 2>(a, stream);
+  return ssm_launch<MT, 16, 1>(a, stream);
 }
 
 template <typename MT>

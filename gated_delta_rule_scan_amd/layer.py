@@ -209,14 +209,15 @@ def _ssm_operands(x, dt, A, B, C, D, z, dt_bias) -> tuple:
 
 def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = True, state_in=None,
                    seq_offsets=None, state_index=None, out=None, state_out=None, want_state: bool = True,
-                   stream=None) -> Tuple:
+                   workspace=None, stream=None) -> Tuple:
     """Selective state space scan: per channel, with dt' = softplus(dt + dt_bias) (dt + dt_bias without
     ``dt_softplus``), h = exp(dt' A) h + dt' x B, y = h . C + D x, out = y silu(z).
 
     x, dt, z [B, T, Dch] (or [T, Dch] packed with ``seq_offsets``); A [Dch, N] float32 (<= 0), N <= 256; B, C
     [..., G, N] or [..., N], shared by groups of Dch / G channels; D, dt_bias [Dch] float32 or None.  States
     [slots, Dch, N] float32: ``state_in`` (None: zeros), ``state_out`` (may be ``state_in``), ``state_index`` as for
-    causal_conv.  Returns (out like x, state_out or None)."""
+    causal_conv.  ``workspace``: a uint8 tensor (``gdn_ssm_workspace_bytes``); a smaller one, or None, is replaced by
+    one allocated here.  Returns (out like x, state_out or None)."""
     kind, Dch, N, G, pA, pD, pbias = _ssm_operands(x, dt, A, B, C, D, z, dt_bias)
     S, T = _lead(x, seq_offsets)
     slots, new_state = _states(S, (Dch, N), torch.float32, x, state_in, state_out, state_index, want_state)
@@ -229,6 +230,14 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
                                    _ptr(z), pbias, pD)
     if state_out is None and new_state is not None:
         made += (new_state,)
+    size = _g.gdn_ssm_workspace_bytes(problem)
+    if size:
+        if workspace is None or workspace.numel() < size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+            made += (workspace,)
+        elif workspace.dtype != torch.uint8 or workspace.device != x.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {x.device}")
+        problem.workspace, problem.workspace_bytes = workspace.data_ptr(), workspace.numel()
     _call(_g.gdn_ssm_forward, problem, x.device, stream, made, x.data_ptr(), dt.data_ptr(), pA, B.data_ptr(),
           C.data_ptr(), _ptr(state_in), _ptr(new_state), out.data_ptr())
     return out, new_state

@@ -303,9 +303,10 @@ gdn_status_t gdn_vda_forward(const gdn_vda_problem_t* p,
  *
  * The short causal convolution in front of the scan, rotary positions on q
  * and k, the other common recurrent scan (a selective state space), and the
- * single-token steps of all three recurrences.  Everything below runs on the
+ * single-token steps of these recurrences.  Everything below runs on the
  * problem's `stream`, allocates nothing, does not synchronise, can be captured
  * into a graph, and uses no atomics: results are bitwise deterministic.
+ * Calls whose workspaces or states overlap must be ordered by the caller.
  * Errors as for gdn_forward: a rejected call leaves every buffer untouched.
  *
  * Rows and strides.  An operand described with strides holds, for sequence b
@@ -400,8 +401,15 @@ typedef struct {
   const void* z;
   const float* dt_bias;
   const float* skip;
+  void* workspace;           /* gdn_ssm_forward: caller-owned device memory, 256-byte aligned */
+  size_t workspace_bytes;
   void* stream;
 } gdn_ssm_problem_t;
+
+/* Workspace bytes of gdn_ssm_forward (0 if invalid or unsupported, or where
+ * none is needed: enough sequences and channels to fill the GPU, or short
+ * sequences).  It depends on the sizes and on whether seq_offsets is given. */
+size_t gdn_ssm_workspace_bytes(const gdn_ssm_problem_t* p);
 
 gdn_status_t gdn_ssm_forward(const gdn_ssm_problem_t* p, const void* x, const void* dt, const float* A,
                              const void* Bm, const void* Cm, const float* state_in, float* state_out, void* out);

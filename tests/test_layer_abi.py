@@ -60,7 +60,7 @@ def conv(step=False, **over):
 
 def ssm(step=False, **over):
     f = dict(B=2, T=300, D=64, N=16, G=2, slots=2, dtype=gdn.GDN_DTYPE_BF16, options=1, z=addr(6), dt_bias=addr(7),
-             skip=addr(8))
+             skip=addr(8), workspace=addr(12), workspace_bytes=1 << 30)
     for r in ("x", "dt", "z", "out"):
         f[r + "_stride_b"], f[r + "_stride_t"] = (64, 0) if step else (300 * 64, 64)
     for r in ("b", "c"):
@@ -176,9 +176,25 @@ def test_ssm_rejects(over, status):
 
 
 @pytest.mark.parametrize("over", [dict(T=-1), dict(T=1 << 31), dict(x_stride_t=-1), dict(state_in=addr(10) + 128),
-                                  dict(state_in=addr(5)), dict(out_stride_t=32), dict(seq_offsets=addr(11) + 2)])
+                                  dict(state_in=addr(5)), dict(out_stride_t=32), dict(seq_offsets=addr(11) + 2), dict(workspace=None),
+                                  dict(workspace=addr(12) + 128), dict(workspace=addr(0)), dict(workspace=addr(5)),
+                                  dict(workspace=addr(9)), dict(workspace=addr(10)), dict(workspace=addr(2))])
 def test_ssm_forward_rejects(over):
     assert ssm(**over) == INVALID
+
+
+def test_ssm_workspace():
+    def size(packed=False, **k):
+        p = gdn.gdn_ssm_problem_t(**dict(dict(B=1, T=4096, D=2048, N=16, G=1, dtype=1), **k))
+        p.seq_offsets = addr(0) if packed else None
+        return gdn.gdn_ssm_workspace_bytes(p)
+
+    small = size()
+    assert 0 < small and size(T=8192) >= small and size(packed=True) > 0
+    assert size(T=0) == 0 and size(T=1) == 0 and size(T=64) == 0       # one chunk
+    assert size(B=64) == 0                                             # enough sequences
+    assert size(N=257) == 0 and size(dtype=7) == 0 and size(G=3) == 0  # unsupported, invalid
+    assert ssm(workspace_bytes=4096) == gdn.GDN_ERR_WORKSPACE_TOO_SMALL
 
 
 @no_gpu
