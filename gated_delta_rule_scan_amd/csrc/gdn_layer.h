@@ -43,9 +43,10 @@ struct SsmArgs {
   int64_t B, T, D, N, G, slots;
   int64_t x_sb, x_st, dt_sb, dt_st, z_sb, z_st, b_sb, b_st, c_sb, c_st, o_sb, o_st;
   int softplus;
+  int vec4;  // entries of A and of the states come in whole, aligned 16-byte pieces
   // prompts: tokens per chunk, chunks of an unpacked sequence, and where
   // sequences are split (else null) the workspace: chunk end states, then
-  // entering states [item][N][D], and sums of step sizes [item][D]
+  // entering states [item][D][N], and sums of step sizes [item][D]
   int64_t chunk, chunks;
   float* ends;
   float* steps;
@@ -128,21 +129,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float silu(float x) { return x * hw_rcp(1.0f + hw_exp2(-kLog2e * x)); }
 
 // log(1 + e^x) = max(x, 0) + log1p(t), t = e^-|x| in (0, 1].  log1p(t) =
-// 2 atanh(s), s = t / (2 + t) <= 1/3, by the series s + s^3/3 + ... + s^13/13
-// (the rest is below s^15/15 / s < 3e-8 relative): no cancellation, so small
-// steps keep their relative precision.
+// 2 atanh(s), s = t / (2 + t) <= 1/3: no cancellation, so small steps keep
+// their relative precision.  2 atanh(s) / s as a polynomial of degree four in
+// s^2, the one of least relative error on [0, 1/9] (8e-9, found by exchange).
 __device__ __forceinline__ float softplus(float x) {
   const float t = hw_exp2(-kLog2e * fabsf(x));
   const float s = t * hw_rcp(2.0f + t);
   const float w = s * s;
-  float p = 1.0f / 13;
-  p = fmaf(p, w, 1.0f / 11);
-  p = fmaf(p, w, 1.0f / 9);
-  p = fmaf(p, w, 1.0f / 7);
-  p = fmaf(p, w, 1.0f / 5);
-  p = fmaf(p, w, 1.0f / 3);
-  p = fmaf(p, w, 1.0f);
-  return fmaxf(x, 0.0f) + 2.0f * s * p;
+  float p = 0.28178334f;
+  p = fmaf(p, w, 0.27960601f);
+  p = fmaf(p, w, 0.40024909f);
+  p = fmaf(p, w, 0.66666317f);
+  p = fmaf(p, w, 2.0f);
+  return fmaf(s, p, fmaxf(x, 0.0f));
 }
 
 // Slot of sequence b, or -1 (no state): an index outside 0..slots-1 is no slot.

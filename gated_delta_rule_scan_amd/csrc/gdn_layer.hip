@@ -182,6 +182,7 @@ gdn_status_t ssm_check(const gdn_ssm_problem_t* p, bool step, const void* x, con
   for (int i = 0; i < 6; ++i) {
     if (step) st[i] = 0;
     if (!stride_ok(sb[i]) || !stride_ok(st[i])) return GDN_ERR_INVALID_ARGUMENT;
+    if (st[i] >= (int64_t)1 << 26) return GDN_ERR_UNSUPPORTED;  // some tokens' rows within 32-bit byte offsets
   }
   const bool state = step || state_in || state_out;
   if (state ? !slots_ok(p->slots, p->state_index, B) : !is_aligned(p->state_index, 4)) return GDN_ERR_INVALID_ARGUMENT;
@@ -231,6 +232,7 @@ gdn_status_t ssm_check(const gdn_ssm_problem_t* p, bool step, const void* x, con
   a->x_sb = sb[0]; a->dt_sb = sb[1]; a->b_sb = sb[2]; a->c_sb = sb[3]; a->o_sb = sb[4]; a->z_sb = sb[5];
   a->x_st = st[0]; a->dt_st = st[1]; a->b_st = st[2]; a->c_st = st[3]; a->o_st = st[4]; a->z_st = st[5];
   a->softplus = (p->options & GDN_SSM_OPT_SOFTPLUS) != 0;
+  a->vec4 = N % 4 == 0 && is_aligned(A, 16) && is_aligned(state_in, 16) && is_aligned(state_out, 16);
   return GDN_OK;
 }
 

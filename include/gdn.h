@@ -382,7 +382,7 @@ gdn_status_t gdn_conv_step(const gdn_conv_problem_t* p, const void* x, const flo
  *   dt_bias, skip  [D] fp32, or NULL
  *   state_in       [slots, D, N] fp32, or NULL for zeros
  *   state_out      the same, or NULL; may be state_in (an in-place carry)
- * Supported: 1 <= N <= 256, G divides D. */
+ * Supported: 1 <= N <= 256, G divides D, stride_t < 2^26. */
 typedef enum { GDN_SSM_OPT_SOFTPLUS = 1 } gdn_ssm_option_t;
 
 typedef struct {

@@ -183,6 +183,11 @@ def test_ssm_forward_rejects(over):
     assert ssm(**over) == INVALID
 
 
+@pytest.mark.parametrize("name", ["x", "dt", "z", "b", "c", "out"])
+def test_ssm_token_strides_are_bounded(name):
+    assert ssm(T=300, **{name + "_stride_t": 1 << 26, name + "_stride_b": 1 << 36}) == UNSUPPORTED
+
+
 def test_ssm_workspace():
     def size(packed=False, **k):
         p = gdn.gdn_ssm_problem_t(**dict(dict(B=1, T=4096, D=2048, N=16, G=1, dtype=1), **k))
@@ -191,7 +196,7 @@ def test_ssm_workspace():
 
     small = size()
     assert 0 < small and size(T=8192) >= small and size(packed=True) > 0
-    assert size(T=0) == 0 and size(T=1) == 0 and size(T=64) == 0       # one chunk
+    assert size(T=0) == 0 and size(T=1) == 0 and size(T=32) == 0       # one chunk
     assert size(B=64) == 0                                             # enough sequences
     assert size(N=257) == 0 and size(dtype=7) == 0 and size(G=3) == 0  # unsupported, invalid
     assert ssm(workspace_bytes=4096) == gdn.GDN_ERR_WORKSPACE_TOO_SMALL
