@@ -7,8 +7,8 @@
 // W - 1 input rows).  Memory-bound: 2 W flops per element against one read
 // and one write of it.
 //
-// Prompt split: a thread owns V neighbouring channels (16 bytes of a row, or
-// one channel where rows are not 16-byte aligned) and a run of tokens, which
+// Prompt split: a thread owns V neighbouring channels (16 bytes of a row) and a
+// run of tokens, which
 // it walks in batches of kConvRows.  A batch's rows are all in flight at once,
 // the last W - 1 rows of the batch before stay in registers, and the next
 // batch's loads are issued before the current one is computed; a run re-reads
@@ -19,52 +19,55 @@
 namespace gdn {
 namespace {
 
-constexpr int kConvRows = 8;  // tokens in flight per thread
+constexpr int kConvRows = 8;   // tokens in flight per thread
+constexpr int kUnaligned = 4;  // bytes of a row that a thread takes where rows are not 16-byte aligned
 
-// V channels as stored: 16 aligned bytes, or a single element
+// V neighbouring channels as stored.  WHOLE: 16 bytes, and rows lie on 16 bytes
+// and hold whole packs; else a pack may start at any element (unaligned
+// accesses) and a row's last one may hold only `m` channels.
 template <typename MT, int V>
 struct Pack {
   MT e[V];
 };
-template <typename MT, int V>
-__device__ __forceinline__ Pack<MT, V> load_pack(const MT* p) {
+template <typename MT, int V, bool WHOLE>
+__device__ __forceinline__ Pack<MT, V> load_pack(const MT* p, int m) {
   Pack<MT, V> r;
-  if constexpr (V == 1) {
-    r.e[0] = *p;
+  if constexpr (WHOLE) {
+    __builtin_memcpy(&r, __builtin_assume_aligned(p, 16), 16);
+  } else if (m >= V) {
+    __builtin_memcpy(&r, p, sizeof(r));
   } else {
-    const f32x4 raw = *reinterpret_cast<const f32x4*>(p);
-    __builtin_memcpy(&r, &raw, 16);
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.e[e] = e < m ? p[e] : (MT)0.0f;
   }
   return r;
 }
-template <typename MT, int V>
-__device__ __forceinline__ void store_pack(MT* p, const Pack<MT, V>& v) {
-  if constexpr (V == 1) {
-    *p = v.e[0];
+template <typename MT, int V, bool WHOLE>
+__device__ __forceinline__ void store_pack(MT* p, const Pack<MT, V>& v, int m) {
+  if constexpr (WHOLE) {
+    __builtin_memcpy(__builtin_assume_aligned(p, 16), &v, 16);
+  } else if (m >= V) {
+    __builtin_memcpy(p, &v, sizeof(v));
   } else {
-    f32x4 raw;
-    __builtin_memcpy(&raw, &v, 16);
-    *reinterpret_cast<f32x4*>(p) = raw;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < m) p[e] = v.e[e];
   }
 }
-template <typename MT, int V>
-__device__ __forceinline__ Pack<MT, V> zero_pack() {
+
+// row `pos` of a sequence: its own rows from `x`, the W - 1 before them from
+// the state (zeros without one)
+template <typename MT, int W, int V, bool WHOLE>
+__device__ __forceinline__ Pack<MT, V> load_row(const MT* x, int64_t st, const MT* state, int64_t D, int64_t pos, int m) {
+  if (pos >= 0) return load_pack<MT, V, WHOLE>(x + pos * st, m);
+  if (state) return load_pack<MT, V, WHOLE>(state + (W - 1 + pos) * D, m);
   Pack<MT, V> r;
 #pragma unroll
   for (int e = 0; e < V; ++e) r.e[e] = (MT)0.0f;
   return r;
 }
 
-// row `pos` of a sequence: its own rows from `x`, the W - 1 before them from
-// the state (zeros without one)
-template <typename MT, int W, int V>
-__device__ __forceinline__ Pack<MT, V> load_row(const MT* x, int64_t st, const MT* state, int64_t D, int64_t pos) {
-  if (pos >= 0) return load_pack<MT, V>(x + pos * st);
-  if (state) return load_pack<MT, V>(state + (W - 1 + pos) * D);
-  return zero_pack<MT, V>();
-}
-
-template <typename MT, int W, int V>
+template <typename MT, int W, int V, bool WHOLE>
 __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int channel_tiles, int64_t chunks) {
   const int TX = 1 << tx_log2, TY = 256 >> tx_log2;
   const int tx = threadIdx.x & (TX - 1), ty = threadIdx.x >> tx_log2;
@@ -85,6 +88,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int 
     o0 = s.b * a.o_sb;
   }
   if (d >= a.D || s.chunk < 0) return;
+  const int m = a.D - d < V ? (int)(a.D - d) : V;  // channels of this pack
   const int64_t t0 = s.chunk * C + ty * run;
   const bool writes_state = s.chunk == 0 && ty == 0 && a.state_out;
   if (t0 >= s.len && !writes_state) return;
@@ -97,17 +101,18 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int 
     float w[V][W], bias[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      bias[e] = a.bias ? a.bias[d + e] : 0.0f;
+      const int64_t c = d + (e < m ? e : m - 1);
+      bias[e] = a.bias ? a.bias[c] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < W; ++j) w[e][j] = a.weight[(d + e) * W + j];
+      for (int j = 0; j < W; ++j) w[e][j] = a.weight[c * W + j];
     }
     Pack<MT, V> r[kConvRows + W - 1], nx[kConvRows];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) r[j] = load_row<MT, W, V>(x, a.x_st, state, a.D, t0 - (W - 1) + j);
+    for (int j = 0; j < W - 1; ++j) r[j] = load_row<MT, W, V, WHOLE>(x, a.x_st, state, a.D, t0 - (W - 1) + j, m);
     const int64_t tend = t0 + run < s.len ? t0 + run : s.len;
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i)  // rows past the end repeat the last one; they are not stored
-      nx[i] = load_pack<MT, V>(x + (t0 + i < tend ? t0 + i : tend - 1) * a.x_st);
+      nx[i] = load_pack<MT, V, WHOLE>(x + (t0 + i < tend ? t0 + i : tend - 1) * a.x_st, m);
     for (int64_t t = t0; t < tend; t += kConvRows) {
 #pragma unroll
       for (int i = 0; i < kConvRows; ++i) r[W - 1 + i] = nx[i];
@@ -115,7 +120,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int 
 #pragma unroll
         for (int i = 0; i < kConvRows; ++i) {
           const int64_t u = t + kConvRows + i;
-          nx[i] = load_pack<MT, V>(x + (u < tend ? u : tend - 1) * a.x_st);
+          nx[i] = load_pack<MT, V, WHOLE>(x + (u < tend ? u : tend - 1) * a.x_st, m);
         }
       }
 #pragma unroll
@@ -128,7 +133,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int 
           for (int j = 0; j < W; ++j) acc = fmaf(w[e][j], to_float(r[i + j].e[e]), acc);
           y.e[e] = (MT)(a.silu ? silu(acc) : acc);
         }
-        if (t + i < tend) store_pack<MT, V>(out + (t + i) * a.o_st, y);
+        if (t + i < tend) store_pack<MT, V, WHOLE>(out + (t + i) * a.o_st, y, m);
       }
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) r[j] = r[kConvRows + j];
@@ -140,37 +145,39 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int 
   if (writes_state && slot >= 0) {
     Pack<MT, V> keep[W - 1];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) keep[j] = load_row<MT, W, V>(x, a.x_st, state, a.D, s.len - (W - 1) + j);
+    for (int j = 0; j < W - 1; ++j) keep[j] = load_row<MT, W, V, WHOLE>(x, a.x_st, state, a.D, s.len - (W - 1) + j, m);
     MT* so = static_cast<MT*>(a.state_out) + slot * (W - 1) * a.D + d;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) store_pack<MT, V>(so + j * a.D, keep[j]);
+    for (int j = 0; j < W - 1; ++j) store_pack<MT, V, WHOLE>(so + j * a.D, keep[j], m);
   }
 }
 
 // One token per sequence: a thread takes V channels of one sequence.
-template <typename MT, int W, int V>
+template <typename MT, int W, int V, bool WHOLE>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int tx_log2, int channel_tiles) {
   const int TX = 1 << tx_log2, TY = 256 >> tx_log2;
   const int64_t b = (int64_t)(blockIdx.x / channel_tiles) * TY + (threadIdx.x >> tx_log2);
   const int64_t d = ((int64_t)(blockIdx.x % channel_tiles) * TX + (threadIdx.x & (TX - 1))) * V;
   if (b >= a.B || d >= a.D) return;
+  const int m = a.D - d < V ? (int)(a.D - d) : V;  // channels of this pack
   const int64_t slot = slot_of(a.index, b, a.slots);
   if (slot < 0) return;
   MT* state = static_cast<MT*>(a.state_out) + slot * (W - 1) * a.D + d;
   Pack<MT, V> r[W], y;
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) r[j] = load_pack<MT, V>(state + j * a.D);
-  r[W - 1] = load_pack<MT, V>(static_cast<const MT*>(a.x) + b * a.x_sb + d);
+  for (int j = 0; j < W - 1; ++j) r[j] = load_pack<MT, V, WHOLE>(state + j * a.D, m);
+  r[W - 1] = load_pack<MT, V, WHOLE>(static_cast<const MT*>(a.x) + b * a.x_sb + d, m);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    float acc = a.bias ? a.bias[d + e] : 0.0f;
+    const int64_t c = d + (e < m ? e : m - 1);
+    float acc = a.bias ? a.bias[c] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) acc = fmaf(a.weight[(d + e) * W + j], to_float(r[j].e[e]), acc);
+    for (int j = 0; j < W; ++j) acc = fmaf(a.weight[c * W + j], to_float(r[j].e[e]), acc);
     y.e[e] = (MT)(a.silu ? silu(acc) : acc);
   }
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_pack<MT, V>(state + j * a.D, r[j + 1]);
-  store_pack<MT, V>(static_cast<MT*>(a.out) + b * a.o_sb + d, y);
+  for (int j = 0; j < W - 1; ++j) store_pack<MT, V, WHOLE>(state + j * a.D, r[j + 1], m);
+  store_pack<MT, V, WHOLE>(static_cast<MT*>(a.out) + b * a.o_sb + d, y, m);
 }
 
 // lanes across channels: enough for the row, at most a wave
@@ -180,7 +187,7 @@ int lanes_log2(int64_t lanes) {
   return l;
 }
 
-template <typename MT, int W, int V>
+template <typename MT, int W, int V, bool WHOLE>
 hipError_t conv_launch(ConvArgs a, hipStream_t stream) {
   const int64_t lanes = (a.D + V - 1) / V;
   const int txl = lanes_log2(lanes), TY = 256 >> txl;
@@ -193,18 +200,18 @@ hipError_t conv_launch(ConvArgs a, hipStream_t stream) {
   const int64_t chunks = (a.T + C - 1) / C > 0 ? (a.T + C - 1) / C : 1;
   const int64_t items = a.off ? a.T / C + a.B : a.B * chunks;
   if (!grid_fits(items * ctiles, 256)) return hipErrorNotSupported;
-  hipLaunchKernelGGL((conv_kernel<MT, W, V>), dim3((unsigned)(items * ctiles)), dim3(256), 0, stream, a, txl, (int)ctiles,
+  hipLaunchKernelGGL((conv_kernel<MT, W, V, WHOLE>), dim3((unsigned)(items * ctiles)), dim3(256), 0, stream, a, txl, (int)ctiles,
                      chunks);
   return hipGetLastError();
 }
 
-template <typename MT, int W, int V>
+template <typename MT, int W, int V, bool WHOLE>
 hipError_t conv_step_launch(const ConvArgs& a, hipStream_t stream) {
   const int64_t lanes = (a.D + V - 1) / V;
   const int txl = lanes_log2(lanes), TY = 256 >> txl;
   const int64_t ctiles = (lanes + ((int64_t)1 << txl) - 1) >> txl, items = (a.B + TY - 1) / TY;
   if (!grid_fits(items * ctiles, 256)) return hipErrorNotSupported;
-  hipLaunchKernelGGL((conv_step_kernel<MT, W, V>), dim3((unsigned)(items * ctiles)), dim3(256), 0, stream, a, txl,
+  hipLaunchKernelGGL((conv_step_kernel<MT, W, V, WHOLE>), dim3((unsigned)(items * ctiles)), dim3(256), 0, stream, a, txl,
                      (int)ctiles);
   return hipGetLastError();
 }
@@ -213,18 +220,18 @@ hipError_t conv_step_launch(const ConvArgs& a, hipStream_t stream) {
 
 template <typename MT>
 hipError_t launch_conv(const ConvArgs& a, int width, bool aligned, hipStream_t stream) {
-  constexpr int V = 16 / sizeof(MT);
-  if (width == 2) return aligned ? conv_launch<MT, 2, V>(a, stream) : conv_launch<MT, 2, 1>(a, stream);
-  if (width == 3) return aligned ? conv_launch<MT, 3, V>(a, stream) : conv_launch<MT, 3, 1>(a, stream);
-  return aligned ? conv_launch<MT, 4, V>(a, stream) : conv_launch<MT, 4, 1>(a, stream);
+  constexpr int V = 16 / sizeof(MT), U = kUnaligned / (int)sizeof(MT);
+  if (width == 2) return aligned ? conv_launch<MT, 2, V, true>(a, stream) : conv_launch<MT, 2, U, false>(a, stream);
+  if (width == 3) return aligned ? conv_launch<MT, 3, V, true>(a, stream) : conv_launch<MT, 3, U, false>(a, stream);
+  return aligned ? conv_launch<MT, 4, V, true>(a, stream) : conv_launch<MT, 4, U, false>(a, stream);
 }
 
 template <typename MT>
 hipError_t launch_conv_step(const ConvArgs& a, int width, bool aligned, hipStream_t stream) {
-  constexpr int V = 16 / sizeof(MT);
-  if (width == 2) return aligned ? conv_step_launch<MT, 2, V>(a, stream) : conv_step_launch<MT, 2, 1>(a, stream);
-  if (width == 3) return aligned ? conv_step_launch<MT, 3, V>(a, stream) : conv_step_launch<MT, 3, 1>(a, stream);
-  return aligned ? conv_step_launch<MT, 4, V>(a, stream) : conv_step_launch<MT, 4, 1>(a, stream);
+  constexpr int V = 16 / sizeof(MT), U = kUnaligned / (int)sizeof(MT);
+  if (width == 2) return aligned ? conv_step_launch<MT, 2, V, true>(a, stream) : conv_step_launch<MT, 2, U, false>(a, stream);
+  if (width == 3) return aligned ? conv_step_launch<MT, 3, V, true>(a, stream) : conv_step_launch<MT, 3, U, false>(a, stream);
+  return aligned ? conv_step_launch<MT, 4, V, true>(a, stream) : conv_step_launch<MT, 4, U, false>(a, stream);
 }
 
 template hipError_t launch_conv<float>(const ConvArgs&, int, bool, hipStream_t);

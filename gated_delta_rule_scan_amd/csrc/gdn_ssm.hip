@@ -344,40 +344,115 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a) {
 }
 
 // One token per sequence: 1 << lanes_log2 lanes share a channel, each taking V
-// neighbouring state entries at a time, so a wave's state accesses are
-// contiguous.  Memory-bound on the state, read and written once.
+// neighbouring state entries (with V = 1 up to four of them, 64 apart), so a
+// wave's state accesses are contiguous; a thread takes kChannels channels.
+// Memory-bound on the state, read and written once, and on the latency of
+// what comes before: only the state's address waits for the slot index, and
+// everything else is on its way by then.
+constexpr int kChannels = 2;
+
 template <typename MT, int V>
-__global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2, int channel_tiles) {
-  const int L = 1 << lanes_log2;
-  const int64_t b = blockIdx.x / channel_tiles;
-  const int64_t d = (int64_t)(blockIdx.x % channel_tiles) * (256 >> lanes_log2) + (threadIdx.x >> lanes_log2);
-  const int l = threadIdx.x & (L - 1);
+struct __attribute__((aligned(V * sizeof(MT)))) Entries {
+  MT e[V];
+};
+
+template <typename MT, int V>
+__global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2, int tiles_per_group, int bc_vec) {
+  constexpr int PARTS = V == 4 ? 1 : 4;  // V = 4: 64 lanes hold the 256 entries there can be
+  const int L = 1 << lanes_log2, rows = 256 >> lanes_log2, N = (int)a.N;
+  const unsigned tiles = (unsigned)tiles_per_group * (unsigned)a.G;
+  const int64_t b = blockIdx.x / tiles;
+  const unsigned tile = blockIdx.x % tiles, g = tile / (unsigned)tiles_per_group;
+  const int64_t per = a.D / a.G, end = (g + 1) * per;
+  // the workgroup's first channel (uniform), and this thread's behind it;
+  // channels behind the group's last repeat it and store nothing
+  const int64_t base = g * per + (int64_t)(tile % (unsigned)tiles_per_group) * rows * kChannels;
+  const int l = threadIdx.x & (L - 1), left = end - base < 0x10000 ? (int)(end - base) : 0x10000;
   const int64_t slot = slot_of(a.index, b, a.slots);
-  if (slot < 0 || d >= a.D) return;
-  const int64_t g = d / (a.D / a.G);
-  const float x = to_float(static_cast<const MT*>(a.x)[b * a.x_sb + d]);
-  const float dt =
-      step_size(a, to_float(static_cast<const MT*>(a.dt)[b * a.dt_sb + d]), a.dt_bias ? a.dt_bias[d] : 0.0f);
-  const MT* Bm = static_cast<const MT*>(a.Bm) + b * a.b_sb + g * a.N;
-  const MT* Cm = static_cast<const MT*>(a.Cm) + b * a.c_sb + g * a.N;
-  float* st = a.state_out + (slot * a.D + d) * a.N;
-  float y = 0.0f;
-  for (int n = l * V; n < a.N; n += L * V) {
-    float h[V], A[V];
-    __builtin_memcpy(h, __builtin_assume_aligned(st + n, V * 4), V * 4);
-    __builtin_memcpy(A, __builtin_assume_aligned(a.A + d * a.N + n, V * 4), V * 4);
+  unsigned c[kChannels];
+  bool live[kChannels];
+  float x[kChannels], dt[kChannels];
+  Entries<float, V> A[PARTS][kChannels], h[PARTS][kChannels];
+  Entries<MT, V> B[PARTS], C[PARTS];
+  const MT* px = static_cast<const MT*>(a.x) + b * a.x_sb + base;
+  const MT* pd = static_cast<const MT*>(a.dt) + b * a.dt_sb + base;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      h[e] = fmaf(hw_exp2(dt * A[e] * kLog2e), h[e], dt * x * to_float(Bm[n + e]));
-      y = fmaf(h[e], to_float(Cm[n + e]), y);
-    }
-    __builtin_memcpy(__builtin_assume_aligned(st + n, V * 4), h, V * 4);
+  for (int i = 0; i < kChannels; ++i) {
+    const int ch = (threadIdx.x >> lanes_log2) + i * rows;
+    live[i] = ch < left;
+    c[i] = live[i] ? ch : left - 1;
+    x[i] = to_float(px[c[i]]);
+    dt[i] = to_float(pd[c[i]]) + (a.dt_bias ? (a.dt_bias + base)[c[i]] : 0.0f);
   }
-  for (int m = L >> 1; m >= 1; m >>= 1) y += __shfl_xor(y, m, 64);
-  if (l == 0) {
-    if (a.skip) y = fmaf(a.skip[d], x, y);
-    if (a.z) y *= silu(to_float(static_cast<const MT*>(a.z)[b * a.z_sb + d]));
-    static_cast<MT*>(a.out)[b * a.o_sb + d] = (MT)y;
+  // this thread finishes one of its channels (or all, with fewer lanes than channels)
+  const int mine = L >= kChannels ? l % kChannels : 0;
+  unsigned cf = c[0];
+#pragma unroll
+  for (int i = 1; i < kChannels; ++i) cf = mine == i ? c[i] : cf;
+  const float zf = a.z ? to_float((static_cast<const MT*>(a.z) + b * a.z_sb + base)[cf]) : 0.0f;
+  const float skipf = a.skip ? (a.skip + base)[cf] : 0.0f;
+  const MT* Bm = static_cast<const MT*>(a.Bm) + b * a.b_sb + (int64_t)g * N;
+  const MT* Cm = static_cast<const MT*>(a.Cm) + b * a.c_sb + (int64_t)g * N;
+  const float* Ab = a.A + base * N;
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) {
+    const int n = (q * L + l) * V;
+    const bool in = n < N;
+#pragma unroll
+    for (int e = 0; e < V; ++e) B[q].e[e] = C[q].e[e] = (MT)0.0f;
+    if (in) {
+      if (bc_vec) {
+        B[q] = *reinterpret_cast<const Entries<MT, V>*>(Bm + n);
+        C[q] = *reinterpret_cast<const Entries<MT, V>*>(Cm + n);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          B[q].e[e] = Bm[n + e];
+          C[q].e[e] = Cm[n + e];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kChannels; ++i) A[q][i] = *reinterpret_cast<const Entries<float, V>*>(Ab + c[i] * (unsigned)N + (in ? n : 0));
+  }
+  if (slot < 0) return;  // the whole workgroup
+  float* S = a.state_out + (slot * a.D + base) * N;
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) {
+    const int n = (q * L + l) * V;
+#pragma unroll
+    for (int i = 0; i < kChannels; ++i)
+      h[q][i] = *reinterpret_cast<const Entries<float, V>*>(S + c[i] * (unsigned)N + (n < N ? n : 0));
+  }
+  float y[kChannels];
+#pragma unroll
+  for (int i = 0; i < kChannels; ++i) {
+    const float s = step_size(a, dt[i], 0.0f), u = s * x[i];
+    y[i] = 0.0f;
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      const int n = (q * L + l) * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        h[q][i].e[e] = fmaf(hw_exp2(s * (A[q][i].e[e] * kLog2e)), h[q][i].e[e], u * to_float(B[q].e[e]));
+        y[i] = fmaf(h[q][i].e[e], n < N ? to_float(C[q].e[e]) : 0.0f, y[i]);
+      }
+      if (live[i] && n < N) *reinterpret_cast<Entries<float, V>*>(S + c[i] * (unsigned)N + n) = h[q][i];
+    }
+  }
+  for (int m = L >> 1; m >= 1; m >>= 1) {
+#pragma unroll
+    for (int i = 0; i < kChannels; ++i) y[i] += __shfl_xor(y[i], m, 64);
+  }
+  MT* po = static_cast<MT*>(a.out) + b * a.o_sb + base;
+#pragma unroll
+  for (int i = 0; i < kChannels; ++i) {
+    if (!live[i] || l != (L >= kChannels ? i : 0)) continue;
+    const bool own = L >= kChannels || i == 0;  // whose gate and skip this thread holds
+    const float sk = own ? skipf : a.skip ? (a.skip + base)[c[i]] : 0.0f;
+    const float zi = own ? zf : a.z ? to_float((static_cast<const MT*>(a.z) + b * a.z_sb + base)[c[i]]) : 0.0f;
+    const float v = fmaf(sk, x[i], y[i]);
+    po[c[i]] = (MT)(a.z ? v * silu(zi) : v);
   }
 }
 
@@ -445,16 +520,21 @@ hipError_t launch_ssm(const SsmArgs& a, hipStream_t stream) {
 
 template <typename MT>
 hipError_t launch_ssm_step(const SsmArgs& a, hipStream_t stream) {
-  const bool v4 = a.vec4;
-  const int64_t lanes = v4 ? a.N / 4 : a.N;
+  const int64_t lanes = a.vec4 ? a.N / 4 : a.N;
   int l = 0;
   while (l < 6 && ((int64_t)1 << l) < lanes) ++l;
-  const int64_t ctiles = (a.D + (256 >> l) - 1) / (256 >> l);
-  if (!grid_fits(a.B * ctiles, 256)) return hipErrorNotSupported;
-  if (v4)
-    hipLaunchKernelGGL((ssm_step_kernel<MT, 4>), dim3((unsigned)(a.B * ctiles)), dim3(256), 0, stream, a, l, (int)ctiles);
+  const int64_t rows = (256 >> l) * kChannels, ctiles = (a.D / a.G + rows - 1) / rows;
+  if (!grid_fits(a.B * a.G * ctiles, 256)) return hipErrorNotSupported;
+  auto quads = [&](const void* p, int64_t sb) {
+    return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(MT)) == 0 && (a.B == 1 || sb % 4 == 0);
+  };
+  const int bc_vec = a.vec4 && quads(a.Bm, a.b_sb) && quads(a.Cm, a.c_sb);
+  if (a.vec4)
+    hipLaunchKernelGGL((ssm_step_kernel<MT, 4>), dim3((unsigned)(a.B * a.G * ctiles)), dim3(256), 0, stream, a, l, (int)ctiles,
+                       bc_vec);
   else
-    hipLaunchKernelGGL((ssm_step_kernel<MT, 1>), dim3((unsigned)(a.B * ctiles)), dim3(256), 0, stream, a, l, (int)ctiles);
+    hipLaunchKernelGGL((ssm_step_kernel<MT, 1>), dim3((unsigned)(a.B * a.G * ctiles)), dim3(256), 0, stream, a, l, (int)ctiles,
+                       1);
   return hipGetLastError();
 }
 

@@ -11,6 +11,7 @@ dimension is contiguous (the halves of one projection, say).
 """
 from __future__ import annotations
 
+import ctypes
 import math
 from typing import Optional, Sequence, Tuple
 
@@ -18,36 +19,38 @@ import torch
 
 import gated_delta_rule_scan_amd as _g
 
+_F32 = torch.float32
+_byref = ctypes.byref
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _TYPES = {torch.bfloat16: _g.GDN_DTYPE_BF16, torch.float32: _g.GDN_DTYPE_F32}
 
 
 def _type(x, name: str) -> int:
-    if x.dtype not in _TYPES:
+    kind = _TYPES.get(x.dtype)
+    if kind is None:
         raise TypeError(f"{name} must be float32 or bfloat16")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return _TYPES[x.dtype]
+    return kind
 
 
-def _param(t, shape: tuple, like, name: str, dtype=torch.float32) -> Optional[int]:
+def _param(t, shape: tuple, like, name: str, dtype=_F32) -> Optional[int]:
     """Address of an optional contiguous parameter of the given shape and type."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
         raise ValueError(f"{name} must be contiguous {str(dtype)[6:]} {list(shape)} on {like.device}")
     return t.data_ptr()
 
 
-def _rows(t, x, last: tuple, name: str) -> None:
-    """Checks that t is rows like x's (same leading dimensions, type, device) of contiguous trailing dimensions."""
-    lead = x.dim() - 1
-    if t.dtype != x.dtype or t.device != x.device or t.shape[:lead] != x.shape[:lead] or t.shape[lead:] != last:
-        raise ValueError(f"{name} must be {list(x.shape[:lead]) + list(last)} of the type and on the device of x")
-    step = 1
-    for i in range(t.dim() - 1, lead - 1, -1):
-        if t.shape[i] != 1 and t.stride(i) != step and t.numel():
-            raise ValueError(f"{name}: the last dimension(s) must be contiguous")
-        step *= t.shape[i]
+def _rows(t, shape, dtype, dev, name: str) -> None:
+    """Checks that t is rows of the given shape, type and device whose last dimension is contiguous."""
+    if t.shape == shape and t.dtype is dtype and t.device == dev and t.stride(-1) == 1:
+        return
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+        raise ValueError(f"{name} must be {str(dtype)[6:]} {list(shape)} on {dev}")
+    if t.shape[-1] != 1 and t.numel():
+        raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
 def _lead(x, offsets) -> tuple:
@@ -91,7 +94,7 @@ def _call(fn, problem, device, stream, made, *pointers) -> None:
     """One library call on `device`; `made`: tensors allocated here, which work on another stream than the
     current one keeps alive."""
     index = device.index
-    current = torch._C._cuda_getCurrentRawStream(index)
+    current = _raw_stream(index)
     if stream is None:
         problem.stream = current or None
     else:
@@ -101,22 +104,22 @@ def _call(fn, problem, device, stream, made, *pointers) -> None:
         if stream.cuda_stream != current:
             for t in made:
                 t.record_stream(stream)
-    if torch._C._cuda_getDevice() == index:
-        st = fn(problem, *pointers)
+    if _current_device() == index:
+        st = fn(_byref(problem), *pointers)
     else:
         with torch.cuda.device(device):
-            st = fn(problem, *pointers)
-    if st != _g.GDN_OK:
+            st = fn(_byref(problem), *pointers)
+    if st:
         raise _g.GdnError(st)
 
 
-def _output(out, shape, like, dtype, name="out"):
-    """(out, made): a new contiguous tensor, or the caller's, checked."""
+def _output(out, like, name="out"):
+    """(out, made): a new contiguous tensor like `like`, or the caller's, checked."""
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=like.device)
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
         return out, (out,)
-    if out.dtype != dtype or out.shape != shape or out.device != like.device:
-        raise ValueError(f"{name} must be {str(dtype)[6:]} {list(shape)} on {like.device}")
+    if out.dtype != like.dtype or out.shape != like.shape or out.device != like.device:
+        raise ValueError(f"{name} must be {str(like.dtype)[6:]} {list(like.shape)} on {like.device}")
     if out.shape[-1] != 1 and out.stride(-1) != 1 and out.numel():
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return out, ()
@@ -138,18 +141,18 @@ def causal_conv(x, weight, bias=None, state_in=None, activation: str = "silu", s
     dt = _type(x, "x")
     B, T = _lead(x, seq_offsets)
     D, W = x.shape[-1], weight.shape[-1]
-    _rows(x, x, (D,), "x")
+    _rows(x, x.shape, x.dtype, x.device, "x")
     if activation not in _g.ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_g.ACTIVATIONS)}")
     w, b = _param(weight, (D, W), x, "weight"), _param(bias, (D,), x, "bias")
     slots, new_state = _states(B, (W - 1, D), x.dtype, x, state_in, state_out, state_index, want_state)
-    out, made = _output(out, x.shape, x, x.dtype)
+    out, made = _output(out, x)
     packed = seq_offsets is not None
     problem = _g.gdn_conv_problem_t(B, T, D, *_strides(x, packed), *_strides(out, packed), slots, dt, W,
                                     _g.ACTIVATIONS[activation], _ptr(seq_offsets), _ptr(state_index))
     if state_out is None and new_state is not None:
         made += (new_state,)
-    _call(_g.gdn_conv_forward, problem, x.device, stream, made, x.data_ptr(), w, b, _ptr(state_in), _ptr(new_state),
+    _call(_g.lib().gdn_conv_forward, problem, x.device, stream, made, x.data_ptr(), w, b, _ptr(state_in), _ptr(new_state),
           out.data_ptr())
     return out, new_state
 
@@ -164,46 +167,56 @@ def causal_conv_step(x, weight, bias=None, state=None, activation: str = "silu",
         raise ValueError("x must be [B, D]")
     B, D = x.shape
     W = weight.shape[-1]
-    _rows(x, x, (D,), "x")
+    _rows(x, x.shape, x.dtype, x.device, "x")
     if activation not in _g.ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_g.ACTIVATIONS)}")
     w, b = _param(weight, (D, W), x, "weight"), _param(bias, (D,), x, "bias")
-    slots = _step_state(state, (W - 1, D), x.dtype, x, state_index, B)
-    out, made = _output(out, x.shape, x, x.dtype)
+    slots, ps, pi = _step_state(state, (W - 1, D), x.dtype, x.device, state_index, B)
+    out, made = _output(out, x)
     problem = _g.gdn_conv_problem_t(B, 1, D, x.stride(0), 0, out.stride(0), 0, slots, dt, W,
-                                    _g.ACTIVATIONS[activation], None, _ptr(state_index))
-    _call(_g.gdn_conv_step, problem, x.device, stream, made, x.data_ptr(), w, b, state.data_ptr(), out.data_ptr())
+                                    _g.ACTIVATIONS[activation], None, pi)
+    _call(_g.lib().gdn_conv_step, problem, x.device, stream, made, x.data_ptr(), w, b, ps, out.data_ptr())
     return out
 
 
-def _step_state(state, tail: tuple, dtype, x, index, B) -> int:
+def _step_state(state, tail: tuple, dtype, dev, index, B) -> tuple:
+    """(slots, address of the state, address of the index) of a step."""
     if state is None:
         raise ValueError("state must be given")
-    slots = state.shape[0]
-    _param(state, (slots,) + tail, x, "state", dtype)
-    _param(index, (B,), x, "state_index", torch.int32)
-    if index is None and slots != B:
-        raise ValueError(f"a state of {slots} slots needs state_index for {B} sequences")
-    return slots
+    ss = state.shape
+    if ss[1:] != tail or state.dtype is not dtype or state.device != dev or not state.is_contiguous():
+        raise ValueError(f"state must be contiguous {str(dtype)[6:]} {['slots', *tail]} on {dev}")
+    if index is None:
+        if ss[0] != B:
+            raise ValueError(f"a state of {ss[0]} slots needs state_index for {B} sequences")
+        return B, state.data_ptr(), None
+    if index.dtype is not torch.int32 or index.shape != (B,) or index.device != dev or not index.is_contiguous():
+        raise ValueError(f"state_index must be contiguous int32 {[B]} on {dev}")
+    return ss[0], state.data_ptr(), index.data_ptr()
 
 
 def _ssm_operands(x, dt, A, B, C, D, z, dt_bias) -> tuple:
     """Checks a selective scan's operands; (type, channels, N, G, addresses of A, D and dt_bias)."""
     kind = _type(x, "x")
-    Dch = x.shape[-1]
+    xs, dtype, dev = x.shape, x.dtype, x.device
+    Dch = xs[-1]
     if A.dim() != 2:
         raise ValueError("A must be [D, N]")
-    N = A.shape[1]
-    G = B.shape[-2] if B.dim() == x.dim() + 1 else 1
-    tail = (G, N) if B.dim() == x.dim() + 1 else (N,)
-    _rows(x, x, (Dch,), "x")
-    _rows(dt, x, (Dch,), "dt")
-    _rows(B, x, tail, "B")
-    _rows(C, x, tail, "C")
+    N, bs = A.shape[1], B.shape
+    grouped = len(bs) == len(xs) + 1
+    G = bs[-2] if grouped else 1
+    want = xs[:-1] + ((G, N) if grouped else (N,))
+    _rows(x, xs, dtype, dev, "x")
+    _rows(dt, xs, dtype, dev, "dt")
+    _rows(B, want, dtype, dev, "B")
+    _rows(C, want, dtype, dev, "C")
     if z is not None:
-        _rows(z, x, (Dch,), "z")
-    if G < 1 or Dch % G:
-        raise ValueError(f"{G} groups do not divide {Dch} channels")
+        _rows(z, xs, dtype, dev, "z")
+    if G != 1:
+        if G < 1 or Dch % G:
+            raise ValueError(f"{G} groups do not divide {Dch} channels")
+        if (B.stride(-2) != N or C.stride(-2) != N) and B.numel():
+            raise ValueError("B, C: the last two dimensions must be contiguous")
     return kind, Dch, N, G, _param(A, (Dch, N), x, "A"), _param(D, (Dch,), x, "D"), _param(dt_bias, (Dch,), x, "dt_bias")
 
 
@@ -221,7 +234,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
     kind, Dch, N, G, pA, pD, pbias = _ssm_operands(x, dt, A, B, C, D, z, dt_bias)
     S, T = _lead(x, seq_offsets)
     slots, new_state = _states(S, (Dch, N), torch.float32, x, state_in, state_out, state_index, want_state)
-    out, made = _output(out, x.shape, x, x.dtype)
+    out, made = _output(out, x)
     packed = seq_offsets is not None
     zs = (0, 0) if z is None else _strides(z, packed)
     problem = _g.gdn_ssm_problem_t(S, T, Dch, N, G, *_strides(x, packed), *_strides(dt, packed), *zs,
@@ -238,7 +251,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
         elif workspace.dtype != torch.uint8 or workspace.device != x.device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {x.device}")
         problem.workspace, problem.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    _call(_g.gdn_ssm_forward, problem, x.device, stream, made, x.data_ptr(), dt.data_ptr(), pA, B.data_ptr(),
+    _call(_g.lib().gdn_ssm_forward, problem, x.device, stream, made, x.data_ptr(), dt.data_ptr(), pA, B.data_ptr(),
           C.data_ptr(), _ptr(state_in), _ptr(new_state), out.data_ptr())
     return out, new_state
 
@@ -252,14 +265,13 @@ def selective_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
         raise ValueError("x must be [S, D]")
     kind, Dch, N, G, pA, pD, pbias = _ssm_operands(x, dt, A, B, C, D, z, dt_bias)
     S = x.shape[0]
-    slots = _step_state(state, (Dch, N), torch.float32, x, state_index, S)
-    out, made = _output(out, x.shape, x, x.dtype)
+    slots, ps, pi = _step_state(state, (Dch, N), _F32, x.device, state_index, S)
+    out, made = _output(out, x)
     problem = _g.gdn_ssm_problem_t(S, 1, Dch, N, G, x.stride(0), 0, dt.stride(0), 0, 0 if z is None else z.stride(0),
                                    0, B.stride(0), 0, C.stride(0), 0, out.stride(0), 0, slots, kind,
-                                   _g.GDN_SSM_OPT_SOFTPLUS if dt_softplus else 0, None, _ptr(state_index), _ptr(z),
-                                   pbias, pD)
-    _call(_g.gdn_ssm_step, problem, x.device, stream, made, x.data_ptr(), dt.data_ptr(), pA, B.data_ptr(), C.data_ptr(),
-          state.data_ptr(), out.data_ptr())
+                                   _g.GDN_SSM_OPT_SOFTPLUS if dt_softplus else 0, None, pi, _ptr(z), pbias, pD)
+    _call(_g.lib().gdn_ssm_step, problem, x.device, stream, made, x.data_ptr(), dt.data_ptr(), pA, B.data_ptr(), C.data_ptr(),
+          ps, out.data_ptr())
     return out
 
 
@@ -325,10 +337,10 @@ def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, sections: 
             raise ValueError(f"{name} must be [{B}, {T}, H, {d}] of the type and on the device of q")
         if d != 1 and t.stride(3) != 1 and t.numel():
             raise ValueError(f"{name}: the last dimension must be contiguous")
-    q_out, made = _output(q_out, q.shape, q, q.dtype, "q_out")
+    q_out, made = _output(q_out, q, "q_out")
     if k is not None:
         Hk = k.shape[2]
-        k_out, mk = _output(k_out, k.shape, k, k.dtype, "k_out")
+        k_out, mk = _output(k_out, k, "k_out")
         made += mk
     elif k_out is not None:
         raise ValueError("k_out without k")
@@ -353,7 +365,7 @@ def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, sections: 
                                       *((0, 0, 0) if k is None else k_out.stride()[:3]), position0, dt,
                                       (_g.GDN_ROTARY_OPT_INTERLEAVED if interleaved else 0)
                                       | (_g.GDN_ROTARY_OPT_INVERSE if inverse else 0), bits, axes, tuple(sections), scale)
-    _call(_g.gdn_rotary, problem, q.device, stream, made, q.data_ptr(), _ptr(k), pf, _ptr(positions), q_out.data_ptr(),
+    _call(_g.lib().gdn_rotary, problem, q.device, stream, made, q.data_ptr(), _ptr(k), pf, _ptr(positions), q_out.data_ptr(),
           None if k is None else k_out.data_ptr())
     return q_out, k_out
 
@@ -365,32 +377,35 @@ def delta_step(q, k, v, log_alpha, beta, state, state_index=None, erase: bool = 
     slot ``state_index[b]`` (None: slot b; out of range: the row is skipped).  ``erase``, ``exclusive`` (o read
     before the token's own write), ``gate`` [B, H, dv], ``norm_weight`` [dv] and ``norm_eps`` as for ``forward``.
     Returns out [B, H, dv] float32."""
+    dtype, dev, qs = q.dtype, q.device, q.shape
     dt = _type(q, "q")
-    if q.dim() != 3 or v.dim() != 3:
+    if len(qs) != 3 or v.dim() != 3:
         raise ValueError("q, k must be [B, H, dk] and v [B, H, dv]")
-    B, H, dk = q.shape
+    B, H, dk = qs
     dv = v.shape[2]
-    pk, pv = _param(k, (B, H, dk), q, "k", q.dtype), _param(v, (B, H, dv), q, "v", q.dtype)
-    pq = _param(q, (B, H, dk), q, "q", q.dtype)
-    pa, pb = _param(log_alpha, (B, H), q, "log_alpha"), _param(beta, (B, H), q, "beta")
-    if pa is None or pb is None or pk is None:
-        raise ValueError("k, log_alpha and beta must be given")
-    slots = _step_state(state, (H, dv, dk), torch.float32, q, state_index, B)
+    vs, gs = (B, H, dv), (B, H)
+    if not (k.shape == qs and v.shape == vs and k.dtype is dtype and v.dtype is dtype and k.device == dev
+            and v.device == dev and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        raise ValueError(f"q, k, v must be contiguous {str(dtype)[6:]} {list(qs)}, {list(qs)}, {list(vs)} on {dev}")
+    if not (log_alpha.shape == gs and beta.shape == gs and log_alpha.dtype is _F32 and beta.dtype is _F32
+            and log_alpha.device == dev and beta.device == dev and log_alpha.is_contiguous() and beta.is_contiguous()):
+        raise ValueError(f"log_alpha and beta must be contiguous float32 {list(gs)} on {dev}")
+    slots, ps, pi = _step_state(state, (H, dv, dk), _F32, dev, state_index, B)
     pg, pw = None, None
     if gate is not None:
-        pg, pw = _param(gate, (B, H, dv), q, "gate", q.dtype), _param(norm_weight, (dv,), q, "norm_weight")
+        pg, pw = _param(gate, (B, H, dv), q, "gate", dtype), _param(norm_weight, (dv,), q, "norm_weight")
         if pw is None:
             raise ValueError(f"norm_weight must be float32 [{dv}] when gate is given")
     made = ()
     if out is None:
-        out = torch.empty((B, H, dv), dtype=torch.float32, device=q.device)
+        out = torch.empty_like(v, dtype=_F32)
         made = (out,)
     else:
         _param(out, (B, H, dv), q, "out")
     problem = _g.gdn_step_problem_t(B, H, dk, dv, slots, dt, (0 if erase else _g.GDN_OPT_NO_ERASE)
-                                    | (_g.GDN_OPT_EXCLUSIVE_FORWARD if exclusive else 0), _ptr(state_index), pg, pw,
-                                    norm_eps)
-    _call(_g.gdn_step, problem, q.device, stream, made, pq, pk, pv, pa, pb, state.data_ptr(), out.data_ptr())
+                                    | (_g.GDN_OPT_EXCLUSIVE_FORWARD if exclusive else 0), pi, pg, pw, norm_eps)
+    _call(_g.lib().gdn_step, problem, dev, stream, made, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(),
+          beta.data_ptr(), ps, out.data_ptr())
     return out
 
 
