@@ -20,7 +20,6 @@ namespace gdn {
 namespace {
 
 constexpr int kConvRows = 8;   // tokens in flight per thread
-constexpr int kUnaligned = 4;  // bytes of a row that a thread takes where rows are not 16-byte aligned
 
 // V neighbouring channels as stored.  WHOLE: 16 bytes, and rows lie on 16 bytes
 // and hold whole packs; else a pack may start at any element (unaligned
@@ -109,20 +108,26 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int 
     Pack<MT, V> r[kConvRows + W - 1], nx[kConvRows];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) r[j] = load_row<MT, W, V, WHOLE>(x, a.x_st, state, a.D, t0 - (W - 1) + j, m);
-    const int64_t tend = t0 + run < s.len ? t0 + run : s.len;
+    // tokens of the run, counted down; pointers at the rows to be loaded and
+    // stored next
+    int left = (int)(s.len - t0 < run ? s.len - t0 : run);
+    const MT* px = x + t0 * a.x_st;
+    MT* po = out + t0 * a.o_st;
+    auto load = [&](int n) {  // the next kConvRows rows, of which n are there; the last one repeats
+      if (n >= kConvRows) {
 #pragma unroll
-    for (int i = 0; i < kConvRows; ++i)  // rows past the end repeat the last one; they are not stored
-      nx[i] = load_pack<MT, V, WHOLE>(x + (t0 + i < tend ? t0 + i : tend - 1) * a.x_st, m);
-    for (int64_t t = t0; t < tend; t += kConvRows) {
+        for (int i = 0; i < kConvRows; ++i) nx[i] = load_pack<MT, V, WHOLE>(px + i * a.x_st, m);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kConvRows; ++i) nx[i] = load_pack<MT, V, WHOLE>(px + (i < n ? i : n - 1) * a.x_st, m);
+      }
+      px += kConvRows * a.x_st;
+    };
+    load(left);
+    while (left > 0) {
 #pragma unroll
       for (int i = 0; i < kConvRows; ++i) r[W - 1 + i] = nx[i];
-      if (t + kConvRows < tend) {
-#pragma unroll
-        for (int i = 0; i < kConvRows; ++i) {
-          const int64_t u = t + kConvRows + i;
-          nx[i] = load_pack<MT, V, WHOLE>(x + (u < tend ? u : tend - 1) * a.x_st, m);
-        }
-      }
+      if (left > kConvRows) load(left - kConvRows);
 #pragma unroll
       for (int i = 0; i < kConvRows; ++i) {
         Pack<MT, V> y;
@@ -133,10 +138,12 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int 
           for (int j = 0; j < W; ++j) acc = fmaf(w[e][j], to_float(r[i + j].e[e]), acc);
           y.e[e] = (MT)(a.silu ? silu(acc) : acc);
         }
-        if (t + i < tend) store_pack<MT, V, WHOLE>(out + (t + i) * a.o_st, y, m);
+        if (i < left) store_pack<MT, V, WHOLE>(po + i * a.o_st, y, m);
       }
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) r[j] = r[kConvRows + j];
+      po += kConvRows * a.o_st;
+      left -= kConvRows;
     }
   }
   // The final state: written by the thread that alone reads this sequence's
@@ -195,7 +202,7 @@ hipError_t conv_launch(ConvArgs a, hipStream_t stream) {
   // four batches a run where that still gives every compute unit eight waves
   // (2048 in all); shorter work takes one batch, for more threads
   const int64_t rows = a.off ? a.T : a.B * a.T;
-  a.batches = ((rows * ctiles) << txl) >= (int64_t)2048 * 64 * 4 * kConvRows ? 4 : 1;
+  a.batches = ((rows * ctiles) << txl) >= (int64_t)2048 * 64 * 4 * kConvRows ? (WHOLE ? 4 : 2) : 1;
   const int64_t C = (int64_t)a.batches * kConvRows * TY;
   const int64_t chunks = (a.T + C - 1) / C > 0 ? (a.T + C - 1) / C : 1;
   const int64_t items = a.off ? a.T / C + a.B : a.B * chunks;
@@ -220,7 +227,7 @@ hipError_t conv_step_launch(const ConvArgs& a, hipStream_t stream) {
 
 template <typename MT>
 hipError_t launch_conv(const ConvArgs& a, int width, bool aligned, hipStream_t stream) {
-  constexpr int V = 16 / sizeof(MT), U = kUnaligned / (int)sizeof(MT);
+  constexpr int V = 16 / sizeof(MT), U = sizeof(MT) == 4 ? 2 : 1;
   if (width == 2) return aligned ? conv_launch<MT, 2, V, true>(a, stream) : conv_launch<MT, 2, U, false>(a, stream);
   if (width == 3) return aligned ? conv_launch<MT, 3, V, true>(a, stream) : conv_launch<MT, 3, U, false>(a, stream);
   return aligned ? conv_launch<MT, 4, V, true>(a, stream) : conv_launch<MT, 4, U, false>(a, stream);
@@ -228,7 +235,7 @@ hipError_t launch_conv(const ConvArgs& a, int width, bool aligned, hipStream_t s
 
 template <typename MT>
 hipError_t launch_conv_step(const ConvArgs& a, int width, bool aligned, hipStream_t stream) {
-  constexpr int V = 16 / sizeof(MT), U = kUnaligned / (int)sizeof(MT);
+  constexpr int V = 16 / sizeof(MT), U = sizeof(MT) == 4 ? 2 : 1;
   if (width == 2) return aligned ? conv_step_launch<MT, 2, V, true>(a, stream) : conv_step_launch<MT, 2, U, false>(a, stream);
   if (width == 3) return aligned ? conv_step_launch<MT, 3, V, true>(a, stream) : conv_step_launch<MT, 3, U, false>(a, stream);
   return aligned ? conv_step_launch<MT, 4, V, true>(a, stream) : conv_step_launch<MT, 4, U, false>(a, stream);
