@@ -496,7 +496,11 @@ SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool pac
   if (pieces < 1) pieces = 1;
   int64_t chunk = ((T + pieces - 1) / pieces + kAhead - 1) / kAhead * kAhead;
   if (chunk < kShortest) chunk = kShortest;
-  p.split = chunk < T && (packed || B * waves < 768);
+  // One kernel where every SIMD has a wave anyway (16 sequences of 512 tokens
+  // and 4096 channels: 262 us against 256 us split; 12: 260 and 210; 24: 335
+  // and 395), or few tokens (0.4 us each at a wave a SIMD; three kernels take
+  // 32 us: 64 tokens 29 us, 96 tokens 41 us).
+  p.split = T > 72 && chunk < T && (packed || B * waves < 1024);
   if (!p.split) chunk = T < 1 ? 1 : T;
   p.chunk = chunk;
   p.chunks = T < 1 ? 1 : (T + chunk - 1) / chunk;
