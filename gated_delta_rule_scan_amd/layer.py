@@ -2,8 +2,10 @@
 short causal convolution, selective state space scan, rotary positions, and the
 single-token steps (layouts and rules of ``include/gdn.h``).
 
-Argument checks and marshalling only, as in the package's other calls; imported
-by the package, whose names these are.  Every call takes ``stream`` (a
+Argument checks and marshalling only, as in the package's other calls, here in
+native code (``csrc/gdn_binding.cpp``): the steps run a few microseconds, and
+the same checks in Python took longer than the launch.  Imported by the
+package, whose names these are.  Every call takes ``stream`` (a
 ``torch.cuda.Stream``; the current one of the tensors' device by default).
 Prompts come as equal sequences ([B, T, ...]) or packed ([T, ...] with
 ``seq_offsets`` [B + 1] int32); operands may be strided views whose last
@@ -19,114 +21,33 @@ import torch
 
 import gated_delta_rule_scan_amd as _g
 
-_F32 = torch.float32
-_byref = ctypes.byref
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-_TYPES = {torch.bfloat16: _g.GDN_DTYPE_BF16, torch.float32: _g.GDN_DTYPE_F32}
+_bound = None
 
 
-def _type(x, name: str) -> int:
-    kind = _TYPES.get(x.dtype)
-    if kind is None:
-        raise TypeError(f"{name} must be float32 or bfloat16")
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return kind
+def _native():
+    """The native binding, with the entry points of the loaded library."""
+    global _bound
+    if _bound is not _g._lib or _bound is None:
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the native binding is missing: build it with `python -m gated_delta_rule_scan_amd.build`") \
+                from e
+
+        lib = _g.lib()
+        address = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+        _binding.init(_g.GdnError, *(address(n) for n in (
+            "gdn_conv_forward", "gdn_conv_step", "gdn_ssm_workspace_bytes", "gdn_ssm_forward", "gdn_ssm_step",
+            "gdn_rotary", "gdn_step")))
+        _native.binding, _bound = _binding, lib
+    return _native.binding
 
 
-def _param(t, shape: tuple, like, name: str, dtype=_F32) -> Optional[int]:
-    """Address of an optional contiguous parameter of the given shape and type."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"{name} must be contiguous {str(dtype)[6:]} {list(shape)} on {like.device}")
-    return t.data_ptr()
-
-
-def _rows(t, shape, dtype, dev, name: str) -> None:
-    """Checks that t is rows of the given shape, type and device whose last dimension is contiguous."""
-    if t.shape == shape and t.dtype is dtype and t.device == dev and t.stride(-1) == 1:
-        return
-    if t.shape != shape or t.dtype is not dtype or t.device != dev:
-        raise ValueError(f"{name} must be {str(dtype)[6:]} {list(shape)} on {dev}")
-    if t.shape[-1] != 1 and t.numel():
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-
-
-def _lead(x, offsets) -> tuple:
-    """(sequences, tokens): x is [B, T, D], or [T, D] with offsets."""
-    if offsets is None:
-        if x.dim() != 3:
-            raise ValueError("x must be [B, T, D] (or [T, D] with seq_offsets)")
-        return x.shape[0], x.shape[1]
-    if x.dim() != 2:
-        raise ValueError("x must be [T, D] with seq_offsets")
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous() \
-            or offsets.device != x.device:
-        raise ValueError(f"seq_offsets must be contiguous int32 [B + 1] on {x.device}")
-    return offsets.shape[0] - 1, x.shape[0]
-
-
-def _strides(t, packed: bool) -> tuple:
-    """(sequence stride, token stride) of rows."""
-    return (0, t.stride(0)) if packed else (t.stride(0), t.stride(1))
-
-
-def _states(B, tail: tuple, dtype, x, state_in, state_out, index, want) -> tuple:
-    """Checks the state buffers of a prompt and allocates a final state if one is wanted; (slots, state_out)."""
-    _param(index, (B,), x, "state_index", torch.int32)
-    slots = B
-    given = state_in if state_in is not None else state_out
-    if given is not None:
-        slots = given.shape[0]
-        if index is None and slots != B:
-            raise ValueError(f"a state of {slots} slots needs state_index for {B} sequences")
-    for t, name in ((state_in, "state_in"), (state_out, "state_out")):
-        _param(t, (slots,) + tail, x, name, dtype)
-    if state_out is None and want:
-        if index is not None:
-            raise ValueError("state_out must be given with state_index (or want_state=False)")
-        state_out = torch.empty((B,) + tail, dtype=dtype, device=x.device)
-    return slots, state_out
-
-
-def _call(fn, problem, device, stream, made, *pointers) -> None:
-    """One library call on `device`; `made`: tensors allocated here, which work on another stream than the
-    current one keeps alive."""
-    index = device.index
-    current = _raw_stream(index)
-    if stream is None:
-        problem.stream = current or None
-    else:
-        if stream.device != device:
-            raise ValueError(f"stream must be one of {device}")
-        problem.stream = stream.cuda_stream or None
-        if stream.cuda_stream != current:
-            for t in made:
-                t.record_stream(stream)
-    if _current_device() == index:
-        st = fn(_byref(problem), *pointers)
-    else:
-        with torch.cuda.device(device):
-            st = fn(_byref(problem), *pointers)
-    if st:
-        raise _g.GdnError(st)
-
-
-def _output(out, like, name="out"):
-    """(out, made): a new contiguous tensor like `like`, or the caller's, checked."""
-    if out is None:
-        out = torch.empty_like(like, memory_format=torch.contiguous_format)
-        return out, (out,)
-    if out.dtype != like.dtype or out.shape != like.shape or out.device != like.device:
-        raise ValueError(f"{name} must be {str(like.dtype)[6:]} {list(like.shape)} on {like.device}")
-    if out.shape[-1] != 1 and out.stride(-1) != 1 and out.numel():
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return out, ()
-
-
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+def _activation(name: str) -> int:
+    act = _g.ACTIVATIONS.get(name)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(_g.ACTIVATIONS)}")
+    return act
 
 
 def causal_conv(x, weight, bias=None, state_in=None, activation: str = "silu", seq_offsets=None, state_index=None,
@@ -138,23 +59,8 @@ def causal_conv(x, weight, bias=None, state_in=None, activation: str = "silu", s
     sequence (None: zeros), ``state_out`` receives the last W - 1 and may be ``state_in``; sequence b uses slot
     ``state_index[b]`` (None: slot b; out of range: no state).
     Returns (out like x, state_out or None)."""
-    dt = _type(x, "x")
-    B, T = _lead(x, seq_offsets)
-    D, W = x.shape[-1], weight.shape[-1]
-    _rows(x, x.shape, x.dtype, x.device, "x")
-    if activation not in _g.ACTIVATIONS:
-        raise ValueError(f"activation must be one of {sorted(_g.ACTIVATIONS)}")
-    w, b = _param(weight, (D, W), x, "weight"), _param(bias, (D,), x, "bias")
-    slots, new_state = _states(B, (W - 1, D), x.dtype, x, state_in, state_out, state_index, want_state)
-    out, made = _output(out, x)
-    packed = seq_offsets is not None
-    problem = _g.gdn_conv_problem_t(B, T, D, *_strides(x, packed), *_strides(out, packed), slots, dt, W,
-                                    _g.ACTIVATIONS[activation], _ptr(seq_offsets), _ptr(state_index))
-    if state_out is None and new_state is not None:
-        made += (new_state,)
-    _call(_g.lib().gdn_conv_forward, problem, x.device, stream, made, x.data_ptr(), w, b, _ptr(state_in), _ptr(new_state),
-          out.data_ptr())
-    return out, new_state
+    return _native().causal_conv(x, weight, bias, state_in, _activation(activation), seq_offsets, state_index, out,
+                                 state_out, bool(want_state), stream)
 
 
 def causal_conv_step(x, weight, bias=None, state=None, activation: str = "silu", state_index=None, out=None,
@@ -162,62 +68,7 @@ def causal_conv_step(x, weight, bias=None, state=None, activation: str = "silu",
     """The convolution of one new token per sequence: x [B, D]; ``state`` [slots, W - 1, D] is read and advanced in
     place.  A row whose ``state_index`` is out of range is skipped: its output row and every state stay as they
     were.  Returns out [B, D]."""
-    dt = _type(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [B, D]")
-    B, D = x.shape
-    W = weight.shape[-1]
-    _rows(x, x.shape, x.dtype, x.device, "x")
-    if activation not in _g.ACTIVATIONS:
-        raise ValueError(f"activation must be one of {sorted(_g.ACTIVATIONS)}")
-    w, b = _param(weight, (D, W), x, "weight"), _param(bias, (D,), x, "bias")
-    slots, ps, pi = _step_state(state, (W - 1, D), x.dtype, x.device, state_index, B)
-    out, made = _output(out, x)
-    problem = _g.gdn_conv_problem_t(B, 1, D, x.stride(0), 0, out.stride(0), 0, slots, dt, W,
-                                    _g.ACTIVATIONS[activation], None, pi)
-    _call(_g.lib().gdn_conv_step, problem, x.device, stream, made, x.data_ptr(), w, b, ps, out.data_ptr())
-    return out
-
-
-def _step_state(state, tail: tuple, dtype, dev, index, B) -> tuple:
-    """(slots, address of the state, address of the index) of a step."""
-    if state is None:
-        raise ValueError("state must be given")
-    ss = state.shape
-    if ss[1:] != tail or state.dtype is not dtype or state.device != dev or not state.is_contiguous():
-        raise ValueError(f"state must be contiguous {str(dtype)[6:]} {['slots', *tail]} on {dev}")
-    if index is None:
-        if ss[0] != B:
-            raise ValueError(f"a state of {ss[0]} slots needs state_index for {B} sequences")
-        return B, state.data_ptr(), None
-    if index.dtype is not torch.int32 or index.shape != (B,) or index.device != dev or not index.is_contiguous():
-        raise ValueError(f"state_index must be contiguous int32 {[B]} on {dev}")
-    return ss[0], state.data_ptr(), index.data_ptr()
-
-
-def _ssm_operands(x, dt, A, B, C, D, z, dt_bias) -> tuple:
-    """Checks a selective scan's operands; (type, channels, N, G, addresses of A, D and dt_bias)."""
-    kind = _type(x, "x")
-    xs, dtype, dev = x.shape, x.dtype, x.device
-    Dch = xs[-1]
-    if A.dim() != 2:
-        raise ValueError("A must be [D, N]")
-    N, bs = A.shape[1], B.shape
-    grouped = len(bs) == len(xs) + 1
-    G = bs[-2] if grouped else 1
-    want = xs[:-1] + ((G, N) if grouped else (N,))
-    _rows(x, xs, dtype, dev, "x")
-    _rows(dt, xs, dtype, dev, "dt")
-    _rows(B, want, dtype, dev, "B")
-    _rows(C, want, dtype, dev, "C")
-    if z is not None:
-        _rows(z, xs, dtype, dev, "z")
-    if G != 1:
-        if G < 1 or Dch % G:
-            raise ValueError(f"{G} groups do not divide {Dch} channels")
-        if (B.stride(-2) != N or C.stride(-2) != N) and B.numel():
-            raise ValueError("B, C: the last two dimensions must be contiguous")
-    return kind, Dch, N, G, _param(A, (Dch, N), x, "A"), _param(D, (Dch,), x, "D"), _param(dt_bias, (Dch,), x, "dt_bias")
+    return _native().causal_conv_step(x, weight, bias, state, _activation(activation), state_index, out, stream)
 
 
 def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = True, state_in=None,
@@ -231,29 +82,8 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
     [slots, Dch, N] float32: ``state_in`` (None: zeros), ``state_out`` (may be ``state_in``), ``state_index`` as for
     causal_conv.  ``workspace``: a uint8 tensor (``gdn_ssm_workspace_bytes``); a smaller one, or None, is replaced by
     one allocated here.  Returns (out like x, state_out or None)."""
-    kind, Dch, N, G, pA, pD, pbias = _ssm_operands(x, dt, A, B, C, D, z, dt_bias)
-    S, T = _lead(x, seq_offsets)
-    slots, new_state = _states(S, (Dch, N), torch.float32, x, state_in, state_out, state_index, want_state)
-    out, made = _output(out, x)
-    packed = seq_offsets is not None
-    zs = (0, 0) if z is None else _strides(z, packed)
-    problem = _g.gdn_ssm_problem_t(S, T, Dch, N, G, *_strides(x, packed), *_strides(dt, packed), *zs,
-                                   *_strides(B, packed), *_strides(C, packed), *_strides(out, packed), slots, kind,
-                                   _g.GDN_SSM_OPT_SOFTPLUS if dt_softplus else 0, _ptr(seq_offsets), _ptr(state_index),
-                                   _ptr(z), pbias, pD)
-    if state_out is None and new_state is not None:
-        made += (new_state,)
-    size = _g.gdn_ssm_workspace_bytes(problem)
-    if size:
-        if workspace is None or workspace.numel() < size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
-            made += (workspace,)
-        elif workspace.dtype != torch.uint8 or workspace.device != x.device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {x.device}")
-        problem.workspace, problem.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    _call(_g.lib().gdn_ssm_forward, problem, x.device, stream, made, x.data_ptr(), dt.data_ptr(), pA, B.data_ptr(),
-          C.data_ptr(), _ptr(state_in), _ptr(new_state), out.data_ptr())
-    return out, new_state
+    return _native().selective_scan(x, dt, A, B, C, D, z, dt_bias, bool(dt_softplus), state_in, seq_offsets, state_index,
+                                    out, state_out, bool(want_state), workspace, stream)
 
 
 def selective_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = True, state=None,
@@ -261,18 +91,7 @@ def selective_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
     """The selective scan of one new token per sequence: x, dt, z [S, Dch], B, C [S, G, N] or [S, N]; ``state``
     [slots, Dch, N] float32 is read and advanced in place.  A row whose ``state_index`` is out of range is skipped.
     Returns out [S, Dch]."""
-    if x.dim() != 2:
-        raise ValueError("x must be [S, D]")
-    kind, Dch, N, G, pA, pD, pbias = _ssm_operands(x, dt, A, B, C, D, z, dt_bias)
-    S = x.shape[0]
-    slots, ps, pi = _step_state(state, (Dch, N), _F32, x.device, state_index, S)
-    out, made = _output(out, x)
-    problem = _g.gdn_ssm_problem_t(S, 1, Dch, N, G, x.stride(0), 0, dt.stride(0), 0, 0 if z is None else z.stride(0),
-                                   0, B.stride(0), 0, C.stride(0), 0, out.stride(0), 0, slots, kind,
-                                   _g.GDN_SSM_OPT_SOFTPLUS if dt_softplus else 0, None, pi, _ptr(z), pbias, pD)
-    _call(_g.lib().gdn_ssm_step, problem, x.device, stream, made, x.data_ptr(), dt.data_ptr(), pA, B.data_ptr(), C.data_ptr(),
-          ps, out.data_ptr())
-    return out
+    return _native().selective_step(x, dt, A, B, C, D, z, dt_bias, bool(dt_softplus), state, state_index, out, stream)
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -321,53 +140,8 @@ def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, sections: 
     ``rotary_frequencies``).  ``positions`` [B, T] or [axes, B, T], int32 or int64 (None: position0 + t); with several
     axes ``sections`` gives the pairs that follow each axis.  ``inverse`` turns back: the gradient of the call.
     ``q_out`` and ``k_out`` may be q and k (in place).  Returns (q_out, k_out or None)."""
-    dt = _type(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [B, T, H, d]")
-    B, T, Hq, d = q.shape
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot / 2]")
-    pairs = inv_freq.shape[0]
-    pf = _param(inv_freq, (pairs,), q, "inv_freq", torch.float64)
-    Hk = 0
-    for t, name in ((q, "q"), (k, "k")):
-        if t is None:
-            continue
-        if t.dtype != q.dtype or t.device != q.device or t.dim() != 4 or t.shape[:2] != q.shape[:2] or t.shape[3] != d:
-            raise ValueError(f"{name} must be [{B}, {T}, H, {d}] of the type and on the device of q")
-        if d != 1 and t.stride(3) != 1 and t.numel():
-            raise ValueError(f"{name}: the last dimension must be contiguous")
-    q_out, made = _output(q_out, q, "q_out")
-    if k is not None:
-        Hk = k.shape[2]
-        k_out, mk = _output(k_out, k, "k_out")
-        made += mk
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    axes, bits = 1, 0
-    if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64) or positions.device != q.device \
-                or not positions.is_contiguous():
-            raise ValueError(f"positions must be contiguous int32 or int64 on {q.device}")
-        if positions.dim() == 3:
-            axes = positions.shape[0]
-        if positions.shape[-2:] != (B, T) or positions.dim() not in (2, 3):
-            raise ValueError(f"positions must be [{B}, {T}] or [axes, {B}, {T}]")
-        bits = 64 if positions.dtype == torch.int64 else 32
-    if sections is None:
-        if axes != 1:
-            raise ValueError("several axes need sections")
-        sections = (pairs,)
-    if len(sections) != axes or axes > 4:
-        raise ValueError(f"sections must give the pairs of each of {axes} axes (at most 4)")
-    problem = _g.gdn_rotary_problem_t(B, T, Hq, Hk, d, 2 * pairs, *q.stride()[:3],
-                                      *((0, 0, 0) if k is None else k.stride()[:3]), *q_out.stride()[:3],
-                                      *((0, 0, 0) if k is None else k_out.stride()[:3]), position0, dt,
-                                      (_g.GDN_ROTARY_OPT_INTERLEAVED if interleaved else 0)
-                                      | (_g.GDN_ROTARY_OPT_INVERSE if inverse else 0), bits, axes, tuple(sections), scale)
-    _call(_g.lib().gdn_rotary, problem, q.device, stream, made, q.data_ptr(), _ptr(k), pf, _ptr(positions), q_out.data_ptr(),
-          None if k is None else k_out.data_ptr())
-    return q_out, k_out
+    options = (_g.GDN_ROTARY_OPT_INTERLEAVED if interleaved else 0) | (_g.GDN_ROTARY_OPT_INVERSE if inverse else 0)
+    return _native().rotary(q, k, inv_freq, positions, options, sections, scale, position0, q_out, k_out, stream)
 
 
 def delta_step(q, k, v, log_alpha, beta, state, state_index=None, erase: bool = True, exclusive: bool = False,
@@ -377,36 +151,9 @@ def delta_step(q, k, v, log_alpha, beta, state, state_index=None, erase: bool = 
     slot ``state_index[b]`` (None: slot b; out of range: the row is skipped).  ``erase``, ``exclusive`` (o read
     before the token's own write), ``gate`` [B, H, dv], ``norm_weight`` [dv] and ``norm_eps`` as for ``forward``.
     Returns out [B, H, dv] float32."""
-    dtype, dev, qs = q.dtype, q.device, q.shape
-    dt = _type(q, "q")
-    if len(qs) != 3 or v.dim() != 3:
-        raise ValueError("q, k must be [B, H, dk] and v [B, H, dv]")
-    B, H, dk = qs
-    dv = v.shape[2]
-    vs, gs = (B, H, dv), (B, H)
-    if not (k.shape == qs and v.shape == vs and k.dtype is dtype and v.dtype is dtype and k.device == dev
-            and v.device == dev and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
-        raise ValueError(f"q, k, v must be contiguous {str(dtype)[6:]} {list(qs)}, {list(qs)}, {list(vs)} on {dev}")
-    if not (log_alpha.shape == gs and beta.shape == gs and log_alpha.dtype is _F32 and beta.dtype is _F32
-            and log_alpha.device == dev and beta.device == dev and log_alpha.is_contiguous() and beta.is_contiguous()):
-        raise ValueError(f"log_alpha and beta must be contiguous float32 {list(gs)} on {dev}")
-    slots, ps, pi = _step_state(state, (H, dv, dk), _F32, dev, state_index, B)
-    pg, pw = None, None
-    if gate is not None:
-        pg, pw = _param(gate, (B, H, dv), q, "gate", dtype), _param(norm_weight, (dv,), q, "norm_weight")
-        if pw is None:
-            raise ValueError(f"norm_weight must be float32 [{dv}] when gate is given")
-    made = ()
-    if out is None:
-        out = torch.empty_like(v, dtype=_F32)
-        made = (out,)
-    else:
-        _param(out, (B, H, dv), q, "out")
-    problem = _g.gdn_step_problem_t(B, H, dk, dv, slots, dt, (0 if erase else _g.GDN_OPT_NO_ERASE)
-                                    | (_g.GDN_OPT_EXCLUSIVE_FORWARD if exclusive else 0), pi, pg, pw, norm_eps)
-    _call(_g.lib().gdn_step, problem, dev, stream, made, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(),
-          beta.data_ptr(), ps, out.data_ptr())
-    return out
+    options = (0 if erase else _g.GDN_OPT_NO_ERASE) | (_g.GDN_OPT_EXCLUSIVE_FORWARD if exclusive else 0)
+    return _native().delta_step(q, k, v, log_alpha, beta, state, state_index, options, gate, norm_weight, norm_eps, out,
+                                stream)
 
 
 def register_ops() -> None:
