@@ -167,19 +167,27 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int tx_log2,
   const int64_t d = ((int64_t)(blockIdx.x % channel_tiles) * TX + (threadIdx.x & (TX - 1))) * V;
   if (b >= a.B || d >= a.D) return;
   const int m = a.D - d < V ? (int)(a.D - d) : V;  // channels of this pack
+  // everything but the state is on its way before the slot is known
   const int64_t slot = slot_of(a.index, b, a.slots);
-  if (slot < 0) return;
-  MT* state = static_cast<MT*>(a.state_out) + slot * (W - 1) * a.D + d;
   Pack<MT, V> r[W], y;
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) r[j] = load_pack<MT, V, WHOLE>(state + j * a.D, m);
   r[W - 1] = load_pack<MT, V, WHOLE>(static_cast<const MT*>(a.x) + b * a.x_sb + d, m);
+  float w[V][W], bias[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     const int64_t c = d + (e < m ? e : m - 1);
-    float acc = a.bias ? a.bias[c] : 0.0f;
+    bias[e] = a.bias ? a.bias[c] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) acc = fmaf(a.weight[c * W + j], to_float(r[j].e[e]), acc);
+    for (int j = 0; j < W; ++j) w[e][j] = a.weight[c * W + j];
+  }
+  if (slot < 0) return;
+  MT* state = static_cast<MT*>(a.state_out) + slot * (W - 1) * a.D + d;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) r[j] = load_pack<MT, V, WHOLE>(state + j * a.D, m);
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    float acc = bias[e];
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc = fmaf(w[e][j], to_float(r[j].e[e]), acc);
     y.e[e] = (MT)(a.silu ? silu(acc) : acc);
   }
 #pragma unroll

@@ -214,7 +214,7 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
     pd += (uint64_t)kAhead * sd;
   };
 
-  float total = 0.0f;
+  double total = 0.0;  // of the step sizes: a chunk may have very many
   float* partial = lds + NG * CT * 2 * kStage * NN + wave * kAhead * 64 + lane;
   int left = (int)(c.t1 - c.t0);  // tokens not yet computed
   if (left > 0) {
@@ -243,11 +243,12 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
       if (left > kAhead) load_rows(left - kAhead);
       const float* bcp = stage + part * NN;
       const rsrc_t ro = make_rsrc(po, kReach);
+      float sum = 0.0f;
       auto token = [&](int i, bool in) {
         float s = step_size(a, dc[i], bias);
         if (!in) s = 0.0f;  // past the end: decay 1, no input
         const float u = s * xc[i];
-        if (STATES) total += s;
+        if (STATES) sum += s;
         float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
         for (int j = 0; j < NN / 4; ++j) {
@@ -279,6 +280,7 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) token(i, i < left);
       }
+      if (STATES) total += (double)sum;
       if (!STATES && MULTI) {
         // the waves of a channel tile share out the tokens' sums; px and pz
         // lie behind these tokens
@@ -300,7 +302,7 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
   if (!live) return;
   if (STATES) {
     store_entries(a.ends + c.item * a.D * N + row, wide, a.vec4, h);
-    if (ng == 0) a.steps[c.item * a.D + d] = total;
+    if (ng == 0) a.steps[c.item * a.D + d] = (float)total;
   } else if (a.state_out && slot >= 0 && c.t1 >= c.len) {
     store_entries(a.state_out + slot * a.D * N + row, wide, a.vec4, h);
   }

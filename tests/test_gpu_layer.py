@@ -232,6 +232,90 @@ def test_selective_scan(kind, lens, D, N, G, gate, skip, bias, softplus, state):
         oracle.check(n(h)[i], hw, he, "f32", f"final state {i}")
 
 
+@pytest.mark.parametrize("T", [72, 73, 96, 97, 103, 104, 129])
+@pytest.mark.parametrize("D,N,G", [(70, 16, 1), (200, 16, 2), (130, 33, 1), (65, 100, 1), (12, 256, 3)])
+def test_selective_scan_around_chunk_borders(T, D, N, G):
+    """Lengths on both sides of the split and of chunk, stage and load borders; channel tiles with a rest, groups that
+    are no whole tile, entries over several waves."""
+    import gated_delta_rule_scan_amd as gdn
+
+    r = Rng(T * 7 + N)
+    kw = _ssm_inputs(r, "f32", (1, T), D, N, G, True, True, True, True)
+    s = r.t(1, D, N)
+    y, h = gdn.selective_scan(**kw, state_in=s)
+    (want, err), (hw, he) = _ssm_oracle(kw, 0, n(s)[0])
+    oracle.check(n(y)[0], want, err, "f32", "out")
+    oracle.check(n(h)[0], hw, he, "f32", "state")
+
+
+@pytest.mark.parametrize("B,T,D,packed", [(1100, 75, 8, False), (2, 76, 33000, False), (90, 900, 6, True), (700, 5000, 3, True)])
+def test_selective_scan_many_sequences_or_channels(B, T, D, packed):
+    """Enough waves for one kernel, and packed batches of many sequences (one round of the search and several), a few
+    sequences and channels of each against the oracle."""
+    import gated_delta_rule_scan_amd as gdn
+
+    r = Rng(B + T)
+    lens = None
+    if packed:
+        cuts = np.sort(r.g.integers(0, T + 1, B - 1))
+        lens = np.diff(np.concatenate([[0], cuts, [T]]))
+    kw = _ssm_inputs(r, "bf16", (T,) if packed else (B, T), D, 16, 1, True, True, True, True)
+    s = r.t(B, D, 16)
+    y, h = gdn.selective_scan(**kw, state_in=s, seq_offsets=offsets(lens) if packed else None)
+    at = np.concatenate([[0], np.cumsum(lens)]) if packed else None
+    ch = np.unique(np.concatenate([r.g.integers(0, D, 4), [0, D - 1]]))
+    cut = lambda t: t if t is None else t[..., ch]
+    few = dict(kw, x=cut(kw["x"]), dt=cut(kw["dt"]), z=cut(kw["z"]), A=kw["A"][ch], D=cut(kw["D"]), dt_bias=cut(kw["dt_bias"]))
+    seqs = np.unique(np.concatenate([r.g.integers(0, B, 6), [0, B - 1], [] if lens is None else [int(np.argmax(lens))]])).astype(int)
+    for i in seqs:
+        rows = slice(at[i], at[i + 1]) if packed else int(i)
+        (want, err), (hw, he) = _ssm_oracle(few, rows, n(s)[i][ch])
+        oracle.check(n(y[rows])[..., ch], want, err, "bf16", f"sequence {i}")
+        oracle.check(n(h)[i][ch], hw, he, "f32", f"state {i}")
+
+
+def test_selective_scan_with_the_callers_workspace():
+    """A workspace of the caller's, full of NaN, used twice; one that is too small is replaced."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    r = Rng(18)
+    kw = _ssm_inputs(r, "bf16", (1, 700), 96, 16, 1, True, True, True, True)
+    want, hw = gdn.selective_scan(**kw)
+    for size in (1 << 22, 16):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            y, h = gdn.selective_scan(**kw, workspace=ws)
+            assert torch.equal(y, want) and torch.equal(h, hw)
+    with pytest.raises(ValueError):
+        gdn.selective_scan(**kw, workspace=torch.zeros(1 << 22, device="cuda"))
+
+
+def test_selective_scan_slow_channels_over_a_long_document():
+    """Steps so small that nothing decays over 70000 tokens: the sums of step sizes that carry states over chunks keep
+    their precision (against 64 bits, a running sum of the same inputs)."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    r = Rng(19)
+    T, D, N = 70001, 64, 4
+    x, B = r.t(1, T, D), r.t(1, T, N)
+    dt = r.t(1, T, D).abs() * 1e-6 + 1e-6
+    A = -torch.rand(D, N, device="cuda") - 0.5
+    y, h = gdn.selective_scan(x, dt, A, B, B, dt_softplus=False)
+    # h_T = sum_t exp(A (S_T - S_t)) dt_t x_t B_t
+    S = torch.cumsum(dt[0].double(), 0)
+    want = torch.zeros(D, N, dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(want)
+    for k in range(N):
+        term = torch.exp(A[:, k].double() * (S[-1] - S)) * (dt[0] .double() * x[0].double()) * B[0, :, k:k + 1].double()
+        want[:, k], mag[:, k] = term.sum(0), term.abs().sum(0)
+    # per token a decay and an update round (10 U), over what is left of each term
+    bound = 10 * oracle.U * (T * mag) / 2
+    assert ((h[0].double() - want).abs() <= bound).all()
+    assert float((h[0].double() - want).norm() / want.norm()) < 1e-5
+
+
 def test_selective_scan_slots_in_place():
     """States in a pool by index (one out of range: it starts from zero and leaves no state), advanced in place."""
     import gated_delta_rule_scan_amd as gdn
