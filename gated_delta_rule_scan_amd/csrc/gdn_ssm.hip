@@ -37,8 +37,7 @@ __device__ __forceinline__ float step_size(const SsmArgs& a, float dt, float bia
 // once more; a sequence's last chunk, and with it a sequence of one chunk, is
 // spared it.
 
-constexpr int kStage = 8;   // tokens whose B and C are staged at a time
-constexpr int kAhead = 4;   // tokens of x, dt and z in flight per lane
+constexpr int kStage = 8;      // tokens computed while the next ones' inputs are in flight
 constexpr int kShortest = 32;  // tokens of a chunk at least
 
 struct Chunk {
@@ -73,10 +72,17 @@ __device__ __forceinline__ Chunk chunk_of(const SsmArgs& a, int64_t item) {
 
 // One element through a buffer resource: uniform base, the lane's offset, a
 // uniform offset (bytes).
+// A loaded value as its bits in a register of its own, converted where it is
+// used: bf16 values held as such get packed in pairs right behind their loads,
+// which waits for the loads there.
 template <typename MT>
-__device__ __forceinline__ MT buffer_load(rsrc_t r, unsigned lane_off, unsigned off) {
-  if constexpr (sizeof(MT) == 2) return __builtin_bit_cast(MT, __builtin_amdgcn_raw_buffer_load_b16(r, (int)lane_off, (int)off, 0));
-  else return __builtin_bit_cast(MT, __builtin_amdgcn_raw_buffer_load_b32(r, (int)lane_off, (int)off, 0));
+__device__ __forceinline__ unsigned buffer_load(rsrc_t r, unsigned lane_off, unsigned off) {
+  if constexpr (sizeof(MT) == 2) return (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, (int)lane_off, (int)off, 0);
+  else return __builtin_amdgcn_raw_buffer_load_b32(r, (int)lane_off, (int)off, 0);
+}
+template <typename MT>
+__device__ __forceinline__ float from_bits(unsigned bits) {
+  return __builtin_bit_cast(float, sizeof(MT) == 2 ? bits << 16 : bits);
 }
 template <typename MT>
 __device__ __forceinline__ void buffer_store(MT v, rsrc_t r, unsigned lane_off, unsigned off) {
@@ -116,12 +122,12 @@ __device__ __forceinline__ void store_entries(float* p, int wide, int vec4, cons
   }
 }
 
-template <typename MT, int NN, bool STATES, bool MULTI>
+template <typename MT, int NN, bool STATES, bool MULTI, bool GATE>
 __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, int waves_n, int CT, int tiles_per_group) {
   constexpr int ES = sizeof(MT), STEP = 64 / NN;       // tokens of B (or C) that a wave loads at a time
   constexpr int ROUNDS = kStage / STEP;
-  static_assert(kStage % STEP == 0 && kStage % kAhead == 0, "whole rounds");
-  extern __shared__ __align__(16) float lds[];         // per wave [B, C][kStage][NN]; with MULTI then [wave][kAhead][64]
+  static_assert(kStage % STEP == 0, "whole rounds");
+  extern __shared__ __align__(16) float lds[];         // per wave [B, C][kStage][NN]; with MULTI then [wave][kStage][64]
   const int NG = MULTI ? waves_n : 1;                  // waves that share a channel tile's entries
   const int N = (int)a.N;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -178,7 +184,7 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
   float* stage = lds + wave * 2 * kStage * NN;
   const int bt = lane / NN, bn = lane % NN;
   const unsigned lane_b = bn < wide ? bt * sb + bn * ES : kNowhere, lane_c = bn < wide ? bt * sc + bn * ES : kNowhere;
-  MT bv[ROUNDS], cv[ROUNDS];
+  unsigned bv[ROUNDS], cv[ROUNDS];
   auto load_bc = [&](int left) {  // left: tokens from pb, pc on
     auto records = [&](unsigned st) {
       const uint64_t n = (uint64_t)(left - 1) * st + wide * ES;
@@ -193,29 +199,24 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
     pb += (uint64_t)kStage * sb;
     pc += (uint64_t)kStage * sc;
   };
-  // x, dt and z of kAhead tokens; past the end the last token repeats
-  MT xv[kAhead], dv[kAhead], zv[kAhead];
+  // x, dt and z of kStage tokens; past the end the last token repeats
+  unsigned xv[kStage], dv[kStage], zv[kStage];
   auto load_rows = [&](int left) {  // left: tokens from px, pd, pz on
     const rsrc_t rx = make_rsrc(px, kReach), rd = make_rsrc(pd, kReach), rz = make_rsrc(pz, kReach);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kStage; ++i) {
       const unsigned k = i < left ? i : left - 1;
       xv[i] = buffer_load<MT>(rx, lane_in, k * sx);
       dv[i] = buffer_load<MT>(rd, lane_in, k * sd);
+      if (GATE) zv[i] = buffer_load<MT>(rz, lane_in, k * sz);
     }
-    if (!STATES && !MULTI) {
-      if (pz) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) zv[i] = buffer_load<MT>(rz, lane_in, (i < left ? i : left - 1) * sz);
-        pz += (uint64_t)kAhead * sz;
-      }
-    }
-    px += (uint64_t)kAhead * sx;
-    pd += (uint64_t)kAhead * sd;
+    if (GATE) pz += (uint64_t)kStage * sz;
+    px += (uint64_t)kStage * sx;
+    pd += (uint64_t)kStage * sd;
   };
 
   double total = 0.0;  // of the step sizes: a chunk may have very many
-  float* partial = lds + NG * CT * 2 * kStage * NN + wave * kAhead * 64 + lane;
+  float* partial = lds + NG * CT * 2 * kStage * NN + wave * kStage * 64 + lane;
   int left = (int)(c.t1 - c.t0);  // tokens not yet computed
   if (left > 0) {
     load_bc(left);
@@ -226,78 +227,74 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < ROUNDS; ++i) {
-      stage[i * 64 + lane] = to_float(bv[i]);
-      if (!STATES) stage[kStage * NN + i * 64 + lane] = to_float(cv[i]);
+      stage[i * 64 + lane] = from_bits<MT>(bv[i]);
+      if (!STATES) stage[kStage * NN + i * 64 + lane] = from_bits<MT>(cv[i]);
     }
     __builtin_amdgcn_wave_barrier();
-    if (left > kStage) load_bc(left - kStage);
-#pragma unroll 1
-    for (int part = 0; part < kStage && left > 0; part += kAhead, left -= kAhead) {
-      float xc[kAhead], dc[kAhead], zc[kAhead];
+    float xc[kStage], dc[kStage], zc[kStage];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        xc[i] = to_float(xv[i]);
-        dc[i] = to_float(dv[i]);
-        zc[i] = !STATES && !MULTI && a.z ? to_float(zv[i]) : 0.0f;
-      }
-      if (left > kAhead) load_rows(left - kAhead);
-      const float* bcp = stage + part * NN;
-      const rsrc_t ro = make_rsrc(po, kReach);
-      float sum = 0.0f;
-      auto token = [&](int i, bool in) {
-        float s = step_size(a, dc[i], bias);
-        if (!in) s = 0.0f;  // past the end: decay 1, no input
-        const float u = s * xc[i];
-        if (STATES) sum += s;
-        float y0 = 0.0f, y1 = 0.0f;
+    for (int i = 0; i < kStage; ++i) {
+      xc[i] = from_bits<MT>(xv[i]);
+      dc[i] = from_bits<MT>(dv[i]);
+      if (GATE) zc[i] = from_bits<MT>(zv[i]);
+    }
+    if (left > kStage) {
+      load_bc(left - kStage);
+      load_rows(left - kStage);
+    }
+    const rsrc_t ro = make_rsrc(po, kReach);
+    float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NN / 4; ++j) {
-          const f32x4 B = *reinterpret_cast<const f32x4*>(bcp + i * NN + 4 * j);
-          f32x4 C = {0.f, 0.f, 0.f, 0.f};
-          if (!STATES) C = *reinterpret_cast<const f32x4*>(bcp + kStage * NN + i * NN + 4 * j);
+    for (int i = 0; i < kStage; ++i) {
+      // past the end: decay 1, no input (infinite x or dt too), no store
+      const bool in = i < left;
+      const float step = step_size(a, dc[i], bias);
+      const float s = in ? step : 0.0f, u = in ? step * xc[i] : 0.0f;
+      if (STATES) sum += s;
+      float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const int n = 4 * j + m;
-            h[n] = fmaf(hw_exp2(s * A[n]), h[n], u * B[m]);
-            if (!STATES) {
-              if (m & 1) y1 = fmaf(h[n], C[m], y1);
-              else y0 = fmaf(h[n], C[m], y0);
-            }
+      for (int j = 0; j < NN / 4; ++j) {
+        const f32x4 B = *reinterpret_cast<const f32x4*>(stage + i * NN + 4 * j);
+        f32x4 C = {0.f, 0.f, 0.f, 0.f};
+        if (!STATES) C = *reinterpret_cast<const f32x4*>(stage + kStage * NN + i * NN + 4 * j);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int n = 4 * j + m;
+          h[n] = fmaf(hw_exp2(s * A[n]), h[n], u * B[m]);
+          if (!STATES) {
+            if (m & 1) y1 = fmaf(h[n], C[m], y1);
+            else y0 = fmaf(h[n], C[m], y0);
           }
         }
-        if (!STATES && !MULTI) {
-          float y = fmaf(skip, xc[i], y0 + y1);
-          y *= a.z ? silu(zc[i]) : 1.0f;
-          if (in) buffer_store<MT>((MT)y, ro, lane_out, i * so);
-        }
-        if (!STATES && MULTI) partial[i * 64] = y0 + y1;
-        __builtin_amdgcn_sched_barrier(0);  // one token's B and C in registers at a time
-      };
-      if (left >= kAhead) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) token(i, true);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) token(i, i < left);
       }
-      if (STATES) total += (double)sum;
-      if (!STATES && MULTI) {
-        // the waves of a channel tile share out the tokens' sums; px and pz
-        // lie behind these tokens
-        __syncthreads();
-        const rsrc_t rx = make_rsrc(start(a.x, a.x_sb, a.x_st, d0) + (c.t1 - c.t0 - left) * (int64_t)sx, kReach);
-        const rsrc_t rz = make_rsrc(a.z ? start(a.z, a.z_sb, a.z_st, d0) + (c.t1 - c.t0 - left) * (int64_t)sz : nullptr, kReach);
-        for (int i = ng; i < kAhead && i < left; i += NG) {
-          const float* p = lds + NG * CT * 2 * kStage * NN + (ct * kAhead + i) * 64 + lane;
-          float y = skip * to_float(buffer_load<MT>(rx, lane_in, i * sx));
-          for (int k = 0; k < NG; ++k) y += p[k * CT * kAhead * 64];
-          if (a.z) y *= silu(to_float(buffer_load<MT>(rz, lane_in, i * sz)));
+      if (!STATES && !MULTI) {
+        float y = fmaf(skip, xc[i], y0 + y1);
+        if (GATE) y *= silu(zc[i]);
+        buffer_store<MT>((MT)y, ro, in ? lane_out : kNowhere, i * so);
+      }
+      if (!STATES && MULTI) partial[i * 64] = y0 + y1;
+      __builtin_amdgcn_sched_barrier(0);  // one token's B and C in registers at a time
+    }
+    if (STATES) total += (double)sum;
+    if (!STATES && MULTI) {
+      // the waves of a channel tile take turns at the tokens' sums
+      __syncthreads();
+      int turn = ng;
+#pragma unroll
+      for (int i = 0; i < kStage; ++i) {
+        if (turn == 0 && i < left) {
+          const float* p = lds + NG * CT * 2 * kStage * NN + (ct * kStage + i) * 64 + lane;
+          float y = skip * xc[i];
+          for (int k = 0; k < NG; ++k) y += p[k * CT * kStage * 64];
+          if (GATE) y *= silu(zc[i]);
           buffer_store<MT>((MT)y, ro, lane_out, i * so);
         }
-        __syncthreads();
+        turn = (turn ? turn : NG) - 1;
       }
-      po += (uint64_t)kAhead * so;
+      __syncthreads();
     }
+    po += (uint64_t)kStage * so;
+    left -= kStage;
   }
   if (!live) return;
   if (STATES) {
@@ -470,13 +467,14 @@ hipError_t ssm_launch(const SsmArgs& a, hipStream_t stream) {
   constexpr bool kMulti = NN == 32;
   const bool multi = kMulti && NG > 1;
   const unsigned stage = (unsigned)(NG * CT * kStage * 2 * NN * sizeof(float));
-  const unsigned partials = multi ? (unsigned)(NG * CT * kAhead * 64 * sizeof(float)) : 0;
+  const unsigned partials = multi ? (unsigned)(NG * CT * kStage * 64 * sizeof(float)) : 0;
   if (a.ends) {
-    const auto states = multi ? ssm_kernel<MT, NN, true, kMulti> : ssm_kernel<MT, NN, true, false>;
+    const auto states = multi ? ssm_kernel<MT, NN, true, kMulti, false> : ssm_kernel<MT, NN, true, false, false>;
     hipLaunchKernelGGL(states, dim3((unsigned)blocks), dim3(threads), stage, stream, a, NG, CT, (int)tiles);
     hipLaunchKernelGGL(ssm_carry_kernel, dim3((unsigned)carries), dim3(256), 0, stream, a);
   }
-  const auto scan = multi ? ssm_kernel<MT, NN, false, kMulti> : ssm_kernel<MT, NN, false, false>;
+  const auto scan = multi ? (a.z ? ssm_kernel<MT, NN, false, kMulti, true> : ssm_kernel<MT, NN, false, kMulti, false>)
+                          : (a.z ? ssm_kernel<MT, NN, false, false, true> : ssm_kernel<MT, NN, false, false, false>);
   hipLaunchKernelGGL(scan, dim3((unsigned)blocks), dim3(threads), stage + partials, stream, a, NG, CT, (int)tiles);
   return hipGetLastError();
 }
@@ -496,7 +494,7 @@ SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool pac
   if (packed) pieces = 2 * room / waves - B > room / (4 * waves) ? 2 * room / waves - B : room / (4 * waves);
   else pieces = room / (B * waves);
   if (pieces < 1) pieces = 1;
-  int64_t chunk = ((T + pieces - 1) / pieces + kAhead - 1) / kAhead * kAhead;
+  int64_t chunk = ((T + pieces - 1) / pieces + kStage - 1) / kStage * kStage;
   if (chunk < kShortest) chunk = kShortest;
   // One kernel where every SIMD has a wave anyway (16 sequences of 512 tokens
   // and 4096 channels: 262 us against 256 us split; 12: 260 and 210; 24: 335

@@ -381,6 +381,27 @@ def test_selective_scan_nan_stays_in_its_place():
     assert torch.isnan(h[hb]).all() and torch.equal(h[~hb], href[~hb])
 
 
+@pytest.mark.parametrize("name", ["x", "dt"])
+@pytest.mark.parametrize("T,N", [(1, 16), (9, 5), (70, 100), (1003, 16)])
+def test_selective_scan_infinite_last_token(T, N, name):
+    """An infinite input or step size in a sequence's last token makes that channel's state infinite with the sign
+    of B (x > 0), not NaN, and changes no earlier output and no other channel."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    r = Rng(31)
+    kw = _ssm_inputs(r, "f32", (2, T), 80, N, 1, True, True, True, True)
+    kw["x"] = kw["x"].abs() + 0.5
+    ref, href = gdn.selective_scan(**kw)
+    kw[name] = kw[name].clone()
+    kw[name][1, T - 1, 70] = float("inf")
+    y, h = gdn.selective_scan(**kw)
+    assert torch.equal(y[0], ref[0]) and torch.equal(h[0], href[0])
+    assert torch.equal(y[1, :T - 1], ref[1, :T - 1])
+    assert torch.equal(h[1, :70], href[1, :70]) and torch.equal(h[1, 71:], href[1, 71:])
+    assert torch.equal(h[1, 70], kw["B"][1, T - 1, 0].float() * float("inf"))
+
+
 @pytest.mark.parametrize("kind,B,D,N,G,gate,skip,bias,softplus", [
     ("bf16", 128, 256, 16, 1, True, True, True, True), ("f32", 1, 1, 1, 1, False, False, False, False),
     ("bf16", 5, 96, 7, 3, True, False, True, True), ("f32", 3, 40, 256, 2, False, True, True, True),
