@@ -38,7 +38,6 @@ __device__ __forceinline__ float step_size(const SsmArgs& a, float dt, float bia
 // spared it.
 
 constexpr int kStage = 8;      // tokens computed while the next ones' inputs are in flight
-constexpr int kShortest = 32;  // tokens of a chunk at least
 
 struct Chunk {
   int64_t b;            // sequence
@@ -306,13 +305,20 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
 }
 
 // Chunk end states become entering states, in place: a thread per channel and
-// state entry of a sequence walks its chunks.
-constexpr int kCarry = 16;  // chunks in flight
+// state entry of a sequence walks its chunks, kCarry of them in flight.  More
+// chunks than that: PARTS threads take kCarry each at a time, join their parts'
+// decays and end states in LDS, and go on from the state that enters theirs.
+constexpr int kCarry = 16, kParts = 4;
 
+template <int PARTS>
 __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a) {
-  const int64_t DN = a.D * a.N, tiles = (DN + 255) / 256;
-  const int64_t b = blockIdx.x / tiles, r = (blockIdx.x - b * tiles) * 256 + threadIdx.x;
-  if (r >= DN) return;
+  constexpr int ENTRIES = 256 / PARTS;
+  __shared__ float2 joined[PARTS][ENTRIES];  // per part: decay and end state from zero
+  const int64_t DN = a.D * a.N, tiles = (DN + ENTRIES - 1) / ENTRIES;
+  const int i = threadIdx.x % ENTRIES, part = threadIdx.x / ENTRIES;
+  const int64_t b = blockIdx.x / tiles, want = (blockIdx.x - b * tiles) * ENTRIES + i;
+  const bool live = want < DN;
+  const int64_t r = live ? want : DN - 1;
   const int64_t d = (uint64_t)r / (unsigned)a.N;
   int64_t item0 = b * a.chunks, len = a.T;
   if (a.off) {
@@ -326,7 +332,8 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a) {
   float h = a.state_in && slot >= 0 ? a.state_in[slot * DN + r] : 0.0f;
   float* ends = a.ends + item0 * DN + r;
   const float* steps = a.steps + item0 * a.D + d;
-  for (int64_t c = 0; c < chunks; c += kCarry) {
+  for (int64_t c0 = 0; c0 < chunks; c0 += PARTS * kCarry) {
+    const int64_t c = c0 + part * kCarry;
     float e[kCarry], s[kCarry];
 #pragma unroll
     for (int k = 0; k < kCarry; ++k) {
@@ -334,11 +341,30 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a) {
       e[k] = in ? ends[(c + k) * DN] : 0.0f;
       s[k] = in ? steps[(c + k) * a.D] : 0.0f;
     }
+    float next = h;
+    if (PARTS > 1) {
+      float sum = 0.0f, end = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kCarry; ++k) {
+        sum += s[k];
+        end = fmaf(hw_exp2(s[k] * A), end, e[k]);
+      }
+      __syncthreads();  // the round before has been read
+      joined[part][i] = make_float2(hw_exp2(sum * A), end);
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) {
+        const float2 j = joined[q][i];
+        if (q < part) h = fmaf(j.x, h, j.y);
+        next = fmaf(j.x, next, j.y);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kCarry; ++k) {
-      if (c + k < chunks) ends[(c + k) * DN] = h;
+      if (live && c + k < chunks) ends[(c + k) * DN] = h;
       h = fmaf(hw_exp2(s[k] * A), h, e[k]);
     }
+    if (PARTS > 1) h = next;
   }
 }
 
@@ -462,7 +488,12 @@ hipError_t ssm_launch(const SsmArgs& a, hipStream_t stream) {
   const int NG = (int)((a.N + NN - 1) / NN), CT = NG >= 4 ? 1 : 4 / NG, threads = NG * CT * 64;
   const int64_t per = a.D / a.G, tiles = (per + 64 * CT - 1) / (64 * CT);
   const int64_t items = a.off ? a.T / a.chunk + a.B : a.B * a.chunks, blocks = items * a.G * tiles;
-  const int64_t carries = a.B * ((a.D * a.N + 255) / 256);
+  // parts where a sequence (a packed one of average length) fills half of them
+  // (32 chunks: 38 -> 33 us at 512 tokens of 4096 channels; 9 of each packed
+  // sequence: 147 -> 171 us at the sizes below)
+  const int64_t chunks = a.off ? (a.T / a.B + a.chunk - 1) / a.chunk : a.chunks;
+  const int parts = chunks >= kParts * kCarry / 2 ? kParts : 1;
+  const int64_t carries = a.B * ((a.D * a.N * parts + 255) / 256);
   if (!grid_fits(blocks, threads) || !grid_fits(carries, 256)) return hipErrorNotSupported;
   constexpr bool kMulti = NN == 32;
   const bool multi = kMulti && NG > 1;
@@ -471,7 +502,7 @@ hipError_t ssm_launch(const SsmArgs& a, hipStream_t stream) {
   if (a.ends) {
     const auto states = multi ? ssm_kernel<MT, NN, true, kMulti, false> : ssm_kernel<MT, NN, true, false, false>;
     hipLaunchKernelGGL(states, dim3((unsigned)blocks), dim3(threads), stage, stream, a, NG, CT, (int)tiles);
-    hipLaunchKernelGGL(ssm_carry_kernel, dim3((unsigned)carries), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(parts > 1 ? ssm_carry_kernel<kParts> : ssm_carry_kernel<1>, dim3((unsigned)carries), dim3(256), 0, stream, a);
   }
   const auto scan = multi ? (a.z ? ssm_kernel<MT, NN, false, kMulti, true> : ssm_kernel<MT, NN, false, kMulti, false>)
                           : (a.z ? ssm_kernel<MT, NN, false, false, true> : ssm_kernel<MT, NN, false, false, false>);
@@ -485,7 +516,10 @@ SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool pac
   SsmPlan p;
   const int64_t waves = G * ((D / G + 63) / 64) * ((N + 31) / 32);  // of one sequence
   // Waves that run at once (registers: four a SIMD up to 16 entries, else
-  // two); chunks as short as that takes, but no shorter than kShortest.
+  // two); chunks as short as that takes, but not so short that the carry over
+  // them costs more than their tokens (4096 channels: 128 tokens in chunks of
+  // 8, 16, 32: 20, 22, 30 us; 256: 29, 24, 31; 512: 35, 33, 34; 1024: 47, 47,
+  // 45).
   // Packed sequences, whose lengths differ, are cut finer (twice the waves), so
   // that no long one is left alone at the end: 187 -> 172 us at 24 sequences,
   // 9001 tokens and 2048 channels.
@@ -495,12 +529,13 @@ SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool pac
   else pieces = room / (B * waves);
   if (pieces < 1) pieces = 1;
   int64_t chunk = ((T + pieces - 1) / pieces + kStage - 1) / kStage * kStage;
-  if (chunk < kShortest) chunk = kShortest;
+  const int64_t least = T <= 128 ? kStage : T <= 512 ? 2 * kStage : 4 * kStage;
+  if (chunk < least) chunk = least;
   // One kernel where every SIMD has a wave anyway (16 sequences of 512 tokens
   // and 4096 channels: 262 us against 256 us split; 12: 260 and 210; 24: 335
-  // and 395), or few tokens (0.4 us each at a wave a SIMD; three kernels take
-  // 32 us: 64 tokens 29 us, 96 tokens 41 us).
-  p.split = T > 72 && chunk < T && (packed || B * waves < 1024);
+  // and 395), or few tokens (0.35 us each at a wave a SIMD: 32 tokens 15.3 us
+  // against 16.2, 40 tokens 18.0 against 16.6).
+  p.split = T > 36 && chunk < T && (packed || B * waves < 1024);
   if (!p.split) chunk = T < 1 ? 1 : T;
   p.chunk = chunk;
   p.chunks = T < 1 ? 1 : (T + chunk - 1) / chunk;

@@ -232,7 +232,7 @@ def test_selective_scan(kind, lens, D, N, G, gate, skip, bias, softplus, state):
         oracle.check(n(h)[i], hw, he, "f32", f"final state {i}")
 
 
-@pytest.mark.parametrize("T", [72, 73, 96, 97, 103, 104, 129])
+@pytest.mark.parametrize("T", [36, 37, 40, 72, 73, 96, 97, 103, 104, 128, 129, 511, 512, 513])
 @pytest.mark.parametrize("D,N,G", [(70, 16, 1), (200, 16, 2), (130, 33, 1), (65, 100, 1), (12, 256, 3)])
 def test_selective_scan_around_chunk_borders(T, D, N, G):
     """Lengths on both sides of the split and of chunk, stage and load borders; channel tiles with a rest, groups that

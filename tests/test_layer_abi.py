@@ -196,7 +196,7 @@ def test_ssm_workspace():
 
     small = size()
     assert 0 < small and size(T=8192) >= small and size(packed=True) > 0
-    assert size(T=0) == 0 and size(T=1) == 0 and size(T=72) == 0       # few tokens
+    assert size(T=0) == 0 and size(T=1) == 0 and size(T=36) == 0       # few tokens
     assert size(B=64) == 0                                             # enough sequences
     assert size(N=257) == 0 and size(dtype=7) == 0 and size(G=3) == 0  # unsupported, invalid
     assert ssm(workspace_bytes=4096) == gdn.GDN_ERR_WORKSPACE_TOO_SMALL
