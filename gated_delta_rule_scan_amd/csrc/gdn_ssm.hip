@@ -521,7 +521,7 @@ SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool pac
   // 8, 16, 32: 20, 22, 30 us; 256: 29, 24, 31; 512: 35, 33, 34; 1024: 47, 47,
   // 45).
   // Packed sequences, whose lengths differ, are cut finer (twice the waves), so
-  // that no long one is left alone at the end: 187 -> 172 us at 24 sequences,
+  // that no long one is left alone at the end: 160 -> 147 us at 24 sequences,
   // 9001 tokens and 2048 channels.
   const int64_t room = N <= 16 ? 4096 : 2048;
   int64_t pieces;  // chunks of a sequence; of the whole packed batch (where every sequence may leave a rest)
@@ -531,11 +531,11 @@ SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool pac
   int64_t chunk = ((T + pieces - 1) / pieces + kStage - 1) / kStage * kStage;
   const int64_t least = T <= 128 ? kStage : T <= 512 ? 2 * kStage : 4 * kStage;
   if (chunk < least) chunk = least;
-  // One kernel where every SIMD has a wave anyway (16 sequences of 512 tokens
-  // and 4096 channels: 262 us against 256 us split; 12: 260 and 210; 24: 335
-  // and 395), or few tokens (0.35 us each at a wave a SIMD: 32 tokens 15.3 us
+  // One kernel where most SIMDs have a wave anyway (512 tokens of 4096
+  // channels: 8 sequences 189 us against 123 us split, 12: 189 and 186, 16: 191
+  // and 223), or few tokens (0.35 us each at a wave a SIMD: 32 tokens 15.3 us
   // against 16.2, 40 tokens 18.0 against 16.6).
-  p.split = T > 36 && chunk < T && (packed || B * waves < 1024);
+  p.split = T > 36 && chunk < T && (packed || B * waves < 768);
   if (!p.split) chunk = T < 1 ? 1 : T;
   p.chunk = chunk;
   p.chunks = T < 1 ? 1 : (T + chunk - 1) / chunk;
