@@ -11,7 +11,9 @@
 // so a row is read once, kept in registers, and written once: memory-bound on
 // the state (8 bytes per entry).  A workgroup takes one head, its waves shares
 // of its rows; dk / 4 lanes hold a row, 16 bytes each, and all of a wave's
-// rows are in flight together.
+// rows are in flight together.  128 sequences x 16 heads of 128 x 128: 52-56 us
+// for 271 MB, 4.9-5.2 TB/s, the rate of a large copy; one sequence x 12 heads:
+// 4.3 us, launch and one chain of loads.
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -120,8 +122,9 @@ hipError_t step_launch(const StepArgs& a, hipStream_t stream) {
 
 template <typename MT, int DK>
 hipError_t step_for(const StepArgs& a, hipStream_t stream) {
-  // few heads: sixteen waves each, for latency; many: four, whose loads in
-  // flight (up to 64 KB a workgroup) already keep the memory busy
+  // few heads: sixteen waves each, for latency (256 heads of 128 x 128: 6.7 us
+  // against 8.2); many: four, whose loads in flight (up to 64 KB a workgroup)
+  // already keep the memory busy (512 heads: 12.8 us against 13.4)
   if (a.B * a.H < 512)
     return a.dv == 64 ? step_launch<MT, DK, 64, 16>(a, stream) : step_launch<MT, DK, 128, 16>(a, stream);
   return a.dv == 64 ? step_launch<MT, DK, 64, 4>(a, stream) : step_launch<MT, DK, 128, 4>(a, stream);
