@@ -180,7 +180,7 @@ gdn_status_t ssm_check(const gdn_ssm_problem_t* p, bool step, const void* x, con
                          p->z ? p->z_stride_b : 0};
   int64_t st[6] = {p->x_stride_t, p->dt_stride_t, p->b_stride_t, p->c_stride_t, p->out_stride_t, p->z ? p->z_stride_t : 0};
   for (int i = 0; i < 6; ++i) {
-    if (step) st[i] = 0;
+    if (T <= 1) st[i] = 0;  // no other token
     if (!stride_ok(sb[i]) || !stride_ok(st[i])) return GDN_ERR_INVALID_ARGUMENT;
     if (st[i] >= (int64_t)1 << 26) return GDN_ERR_UNSUPPORTED;  // some tokens' rows within 32-bit byte offsets
   }

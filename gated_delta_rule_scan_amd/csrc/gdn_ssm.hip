@@ -13,6 +13,14 @@ __device__ __forceinline__ float step_size(const SsmArgs& a, float dt, float bia
   return a.softplus ? p : v;
 }
 
+// A for base-2 exponents.  Minus infinity becomes the lowest number: its
+// product with a step size of zero is zero, not NaN.
+__device__ __forceinline__ float rate(float A) {
+  constexpr float kLowest = -3.402823466e38f;
+  const float r = A * kLog2e;
+  return r < kLowest ? kLowest : r;
+}
+
 // ---- prompts ----
 // Per token, channel and state entry a pass takes one exponential (the issue
 // time of three multiply-adds), the products dt A and dt x B, the update and
@@ -162,7 +170,7 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
   load_entries(a.A + row, wide, a.vec4, A);
 #pragma unroll
   for (int i = 0; i < NN; ++i) {
-    A[i] *= kLog2e;
+    A[i] = rate(A[i]);
     h[i] = 0.0f;
   }
   if (!STATES) {
@@ -253,7 +261,9 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kStage; ++i) {
-      // past the end: decay 1, no input (infinite x or dt too), no store
+      // past the end: decay 1, no input (infinite x or dt too), no store; a
+      // branch instead keeps tokens from overlapping (412 -> 436 us at the size
+      // above), a second copy of the loop spills
       const bool in = i < left;
       const float step = step_size(a, dc[i], bias);
       const float s = in ? step : 0.0f, u = in ? step * xc[i] : 0.0f;
@@ -336,7 +346,7 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a) {
   }
   const int64_t chunks = len > a.chunk ? (len + a.chunk - 1) / a.chunk : 1;
   const int64_t slot = slot_of(a.index, b, a.slots);
-  const float A = a.A[r] * kLog2e;
+  const float A = rate(a.A[r]);
   float h = a.state_in && slot >= 0 ? a.state_in[slot * DN + r] : 0.0f;
   float* ends = a.ends + item0 * DN + r;
   const float* steps = a.steps + item0 * a.D + d;
@@ -469,7 +479,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
       const int n = (q * L + l) * V;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        h[q][i].e[e] = fmaf(hw_exp2(s * (A[q][i].e[e] * kLog2e)), h[q][i].e[e], u * to_float(B[q].e[e]));
+        h[q][i].e[e] = fmaf(hw_exp2(s * rate(A[q][i].e[e])), h[q][i].e[e], u * to_float(B[q].e[e]));
         y[i] = fmaf(h[q][i].e[e], n < N ? to_float(C[q].e[e]) : 0.0f, y[i]);
       }
       if (live[i] && n < N) *reinterpret_cast<Entries<float, V>*>(S + c[i] * (unsigned)N + n) = h[q][i];
@@ -525,6 +535,7 @@ hipError_t ssm_launch(const SsmArgs& a, hipStream_t stream) {
 SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool packed) {
   SsmPlan p;
   const int64_t waves = G * ((D / G + 63) / 64) * ((N + 31) / 32);  // of one sequence
+  const int64_t all = B < ((int64_t)1 << 40) / waves ? B * waves : (int64_t)1 << 40;
   // Waves that run at once (registers: four a SIMD up to 16 entries, else
   // two); chunks as short as that takes, but not so short that the carry over
   // them costs more than their tokens (4096 channels: 128 tokens in chunks of
@@ -536,7 +547,7 @@ SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool pac
   const int64_t room = N <= 16 ? 4096 : 2048;
   int64_t pieces;  // chunks of a sequence; of the whole packed batch (where every sequence may leave a rest)
   if (packed) pieces = 2 * room / waves - B > room / (4 * waves) ? 2 * room / waves - B : room / (4 * waves);
-  else pieces = room / (B * waves);
+  else pieces = room / all;
   if (pieces < 1) pieces = 1;
   int64_t chunk = ((T + pieces - 1) / pieces + kStage - 1) / kStage * kStage;
   const int64_t least = T <= 128 ? kStage : T <= 512 ? 2 * kStage : 4 * kStage;
@@ -545,7 +556,7 @@ SsmPlan ssm_plan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool pac
   // channels: 8 sequences 189 us against 123 us split, 12: 189 and 186, 16: 191
   // and 223), or few tokens (0.35 us each at a wave a SIMD: 32 tokens 15.3 us
   // against 16.2, 40 tokens 18.0 against 16.6).
-  p.split = T > 36 && chunk < T && (packed || B * waves < 768);
+  p.split = T > 36 && chunk < T && (packed || all < 768);
   if (!p.split) chunk = T < 1 ? 1 : T;
   p.chunk = chunk;
   p.chunks = T < 1 ? 1 : (T + chunk - 1) / chunk;

@@ -402,6 +402,37 @@ def test_selective_scan_infinite_last_token(T, N, name):
     assert torch.equal(h[1, 70], kw["B"][1, T - 1, 0].float() * float("inf"))
 
 
+@pytest.mark.parametrize("T", [1, 9, 70, 1003])
+def test_selective_scan_infinite_rate(T):
+    """A rate of minus infinity forgets everything at every token: that entry's state is the last token's own input
+    dt' x B.  Bound: softplus (polynomial, exponential, reciprocal and four roundings) and two products, under 16
+    half steps of fp32."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    r = Rng(32)
+    kw = _ssm_inputs(r, "f32", (1, T), 80, 16, 1, False, False, False, True)
+    kw["A"][70, 3] = float("-inf")
+    y, h = gdn.selective_scan(**kw)
+    dt, x, B = (kw[k][0, T - 1].double() for k in ("dt", "x", "B"))
+    want = torch.log1p(torch.exp(dt[70])) * x[70] * B[0, 3]
+    assert abs(float(h[0, 70, 3]) - float(want)) <= 16 * 2.0 ** -24 * abs(float(want))
+    assert torch.isfinite(y).all() and torch.isfinite(h).all()
+
+
+def test_selective_scan_stride_of_one_token():
+    """With a single token its stride means nothing, however large."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    r = Rng(33)
+    kw = _ssm_inputs(r, "f32", (2, 1), 20, 4, 1, True, True, True, True)
+    ref = gdn.selective_scan(**kw)
+    far = kw["x"].contiguous().as_strided((2, 1, 20), (20, 1 << 30, 1))
+    got = gdn.selective_scan(**{**kw, "x": far})
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
 @pytest.mark.parametrize("kind,B,D,N,G,gate,skip,bias,softplus", [
     ("bf16", 128, 256, 16, 1, True, True, True, True), ("f32", 1, 1, 1, 1, False, False, False, False),
     ("bf16", 5, 96, 7, 3, True, False, True, True), ("f32", 3, 40, 256, 2, False, True, True, True),
