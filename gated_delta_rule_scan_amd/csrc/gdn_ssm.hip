@@ -33,9 +33,9 @@ __device__ __forceinline__ float rate(float A) {
 // A lane owns a channel and NN state entries in registers and walks the tokens
 // in order, so rows of x, dt, z and out move in whole cache lines.  The B and C
 // of the next kStage tokens wait in the wave's own part of LDS as fp32 and
-// reach all lanes by 16-byte broadcast reads; waves never wait for each other.
-// More than 32 entries are split over waves, whose partial readouts meet in
-// LDS.
+// reach all lanes by 16-byte broadcast reads; waves do not wait for each other.
+// More than 32 entries are split over waves that do, to add up their partial
+// readouts in LDS.
 //
 // Too few channels to fill the GPU: sequences are cut into chunks and three
 // kernels run.  The first (STATES) finds each chunk's end state from a zero
@@ -45,11 +45,12 @@ __device__ __forceinline__ float rate(float A) {
 // once more; a sequence's last chunk, and with it a sequence of one chunk, is
 // spared it.
 //
-// 32768 tokens x 2048 channels x 16 entries, bf16, gated: 411 us (first pass
-// 200, carry 10, scan 255).  The scan issues 114 vector instructions per token
-// and wave, 80 of them the formula's, 18 of them exponentials; at their
-// measured issue times (3.1 cycles, exponentials 9, four waves a SIMD) 195 us.
-// Its memory traffic alone would take 107 us.
+// 32768 tokens x 2048 channels x 16 entries, bf16, gated: 411-420 us (under a
+// profiler, which slows them, first pass 200, carry 10, scan 255).  The scan
+// issues 114 vector instructions per token and wave, 80 of them the formula's,
+// 20 of them exponentials and reciprocals; at their measured issue times (3.1
+// and 9 cycles, four waves a SIMD) 200 us.  Its memory traffic alone would take
+// 107 us.
 
 // Tokens computed while the next ones' inputs are in flight (4: 435 us against
 // 427 with 8 at the size above).

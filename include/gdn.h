@@ -408,7 +408,9 @@ typedef struct {
 
 /* Workspace bytes of gdn_ssm_forward (0 if invalid or unsupported, or where
  * none is needed: enough sequences and channels to fill the GPU, or short
- * sequences).  It depends on the sizes and on whether seq_offsets is given. */
+ * sequences).  It depends on the sizes and on whether seq_offsets is given.
+ * Calls that may run at the same time, replayed graphs among them, need a
+ * workspace each. */
 size_t gdn_ssm_workspace_bytes(const gdn_ssm_problem_t* p);
 
 gdn_status_t gdn_ssm_forward(const gdn_ssm_problem_t* p, const void* x, const void* dt, const float* A,
