@@ -48,7 +48,7 @@ def binding_command() -> list:
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
             "-DUSE_ROCM=1", f"-I{torch}/include", f"-I{torch}/include/torch/csrc/api/include", f"-I{rocm}/include",
             f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", os.path.join(CSRC, "gdn_binding.cpp"), "-o",
-            BINDING + ".tmp", f"-L{torch}/lib", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+            BINDING + ".tmp", f"-L{torch}/lib", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
             f"-Wl,-rpath,{torch}/lib"]
 
 
