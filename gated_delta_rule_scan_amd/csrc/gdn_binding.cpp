@@ -51,7 +51,9 @@ const char* text(ScalarType t) {
 const Tensor* tensor(PyObject* o, const char* name) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) throw Refused{PyExc_TypeError, std::string(name) + " must be a tensor"};
-  return &THPVariable_Unpack(o);
+  const Tensor& t = THPVariable_Unpack(o);
+  if (t.is_neg()) refuse(std::string(name) + " is a negated view: its memory holds other values (resolve_neg)");
+  return &t;
 }
 const Tensor& given(PyObject* o, const char* name) {
   const Tensor* t = tensor(o, name);

@@ -372,7 +372,8 @@ def test_binding_refusals():
         lambda: gdn.rotary(x[:, :, None], x[:, :8, None], torch.ones(2, dtype=torch.float64, device="cuda")),
         lambda: gdn.rotary(x[:, :, None], None, torch.ones(2, dtype=torch.float64, device="cuda"),
                            torch.zeros(3, 2, 9, dtype=torch.int32, device="cuda")),
-        lambda: gdn.delta_step(x, x, x, i2, i2, x),
+        lambda: gdn.delta_step(x, x, x, i2, i2, x), lambda: gdn.causal_conv(torch._neg_view(x), w),
+        lambda: gdn.selective_scan(x, **dict(kw, z=torch._neg_view(kw["z"]))),
     ]
     for i, call in enumerate(bad):
         with pytest.raises(ValueError):
