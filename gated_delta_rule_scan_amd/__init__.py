@@ -47,6 +47,7 @@ EXCLUSIVE = {"none": 0, "fwd": GDN_OPT_EXCLUSIVE_FORWARD, "rev": GDN_OPT_EXCLUSI
 
 GDN_VDA_OPT_ADDITIVE = 1
 
+GDN_LAYER_OPT_ZERO_UNUSED = 256
 GDN_ACT_NONE = 0
 GDN_ACT_SILU = 1
 ACTIVATIONS = {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU}
@@ -93,6 +94,7 @@ class gdn_conv_problem_t(ctypes.Structure):
         ("out_stride_b", ctypes.c_int64), ("out_stride_t", ctypes.c_int64),
         ("slots", ctypes.c_int64),
         ("dtype", ctypes.c_int32), ("width", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("options", ctypes.c_int32),
         ("seq_offsets", ctypes.c_void_p), ("state_index", ctypes.c_void_p),
         ("stream", ctypes.c_void_p),
     ]

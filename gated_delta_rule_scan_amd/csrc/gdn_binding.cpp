@@ -111,6 +111,9 @@ Tensor fresh(IntArrayRef sizes, ScalarType type, const Tensor& like) {
   return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
 }
 
+// (its rows of no sequence hold nothing yet)
+int32_t unused_rows(const Tensor* out) { return out ? 0 : GDN_LAYER_OPT_ZERO_UNUSED; }
+
 Tensor output(const Tensor* out, const Tensor& like, const char* name = "out") {
   if (!out) return fresh(like.sizes(), like.scalar_type(), like);
   rows(*out, like.sizes(), like, name);
@@ -238,6 +241,7 @@ PyObject* conv(PyObject* const* a) {
   p.slots = st.slots;
   p.width = (int32_t)W;
   p.activation = (int32_t)whole(a[4], "activation");
+  p.options = unused_rows(out);
   p.seq_offsets = static_cast<const int32_t*>(ptr(off));
   p.state_index = static_cast<const int32_t*>(ptr(index));
   p.stream = s.raw;
@@ -268,6 +272,7 @@ PyObject* conv_step(PyObject* const* a) {
   p.out_stride_b = y.stride(0);
   p.width = (int32_t)W;
   p.activation = (int32_t)whole(a[4], "activation");
+  p.options = unused_rows(out);
   p.state_index = static_cast<const int32_t*>(ptr(index));
   p.stream = s.raw;
   const c10::DeviceGuard guard(x.device());
@@ -336,6 +341,7 @@ PyObject* ssm(PyObject* const* a) {
   if (!out) s.keeps(y);
   if (st.made) s.keeps(st.out);
   q.strides(y, off ? -1 : 0, off ? 0 : 1);
+  p.options |= unused_rows(out);
   p.slots = st.slots;
   p.seq_offsets = static_cast<const int32_t*>(ptr(off));
   p.state_index = static_cast<const int32_t*>(ptr(index));
@@ -372,6 +378,7 @@ PyObject* ssm_step(PyObject* const* a) {
   const Tensor y = output(out, x);
   if (!out) s.keeps(y);
   q.strides(y, 0, -1);
+  p.options |= unused_rows(out);
   p.state_index = static_cast<const int32_t*>(ptr(index));
   p.stream = s.raw;
   const c10::DeviceGuard guard(x.device());
@@ -485,7 +492,7 @@ PyObject* delta_step(PyObject* const* a) {
     y = fresh({p.B, p.H, p.dv}, at::kFloat, q);
     s.keeps(y);
   }
-  p.options = (int32_t)whole(a[7], "options");
+  p.options = (int32_t)whole(a[7], "options") | unused_rows(out);
   p.norm_eps = real(a[10], "norm_eps");
   p.state_index = static_cast<const int32_t*>(ptr(index));
   p.stream = s.raw;

@@ -42,6 +42,13 @@ __device__ __forceinline__ Pack<MT, V> load_pack(const MT* p, int m) {
   }
   return r;
 }
+template <typename MT, int V>
+__device__ __forceinline__ Pack<MT, V> zeros() {
+  Pack<MT, V> r;
+#pragma unroll
+  for (int e = 0; e < V; ++e) r.e[e] = (MT)0.0f;
+  return r;
+}
 template <typename MT, int V, bool WHOLE>
 __device__ __forceinline__ void store_pack(MT* p, const Pack<MT, V>& v, int m) {
   if constexpr (WHOLE) {
@@ -56,7 +63,8 @@ __device__ __forceinline__ void store_pack(MT* p, const Pack<MT, V>& v, int m) {
 }
 
 // row `pos` of a sequence: its own rows from `x`, the W - 1 before them from
-// the state (zeros without one)
+// the state (zeros without one; spelled out here, since with zeros() the
+// compiler splits and joins the pairs of every loaded row: 110 us at the size above)
 template <typename MT, int W, int V, bool WHOLE>
 __device__ __forceinline__ Pack<MT, V> load_row(const MT* x, int64_t st, const MT* state, int64_t D, int64_t pos, int m) {
   if (pos >= 0) return load_pack<MT, V, WHOLE>(x + pos * st, m);
@@ -80,6 +88,13 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a, int tx_log2, int 
     s = find_packed(a.off, a.B, a.T, C, item);
     x0 = s.row0 * a.x_st;
     o0 = s.row0 * a.o_st;
+    // the last sequence's items also hold the rows behind it
+    if (a.zero_unused && s.b == a.B - 1 && d < a.D && s.chunk >= 0) {
+      int64_t t = s.chunk * C + ty * run;
+      const int64_t rows = a.T - s.row0, t1 = t + run < rows ? t + run : rows;
+      for (t = t > s.len ? t : s.len; t < t1; ++t)
+        store_pack<MT, V, WHOLE>(static_cast<MT*>(a.out) + o0 + t * a.o_st + d, zeros<MT, V>(), a.D - d < V ? (int)(a.D - d) : V);
+    }
   } else {
     s.b = item / chunks;
     s.chunk = item % chunks;
@@ -180,7 +195,11 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int tx_log2,
 #pragma unroll
     for (int j = 0; j < W; ++j) w[e][j] = a.weight[c * W + j];
   }
-  if (slot < 0) return;
+  MT* out = static_cast<MT*>(a.out) + b * a.o_sb + d;
+  if (slot < 0) {
+    if (a.zero_unused) store_pack<MT, V, WHOLE>(out, zeros<MT, V>(), m);
+    return;
+  }
   MT* state = static_cast<MT*>(a.state_out) + slot * (W - 1) * a.D + d;
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) r[j] = load_pack<MT, V, WHOLE>(state + j * a.D, m);
@@ -193,7 +212,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int tx_log2,
   }
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) store_pack<MT, V, WHOLE>(state + j * a.D, r[j + 1], m);
-  store_pack<MT, V, WHOLE>(static_cast<MT*>(a.out) + b * a.o_sb + d, y, m);
+  store_pack<MT, V, WHOLE>(out, y, m);
 }
 
 // lanes across channels: enough for the row, at most a wave

@@ -23,6 +23,7 @@ struct ConvArgs {
   int64_t B, T, D, slots;
   int64_t x_sb, x_st, o_sb, o_st;
   int silu;
+  int zero_unused;       // rows of no sequence become zero
   int batches;           // runs of kConvRows tokens per thread
 };
 
@@ -43,6 +44,7 @@ struct SsmArgs {
   int64_t B, T, D, N, G, slots;
   int64_t x_sb, x_st, dt_sb, dt_st, z_sb, z_st, b_sb, b_st, c_sb, c_st, o_sb, o_st;
   int softplus;
+  int zero_unused;
   int vec4;  // entries of A and of the states come in whole, aligned 16-byte pieces
   // prompts: tokens per chunk, chunks of an unpacked sequence, and where
   // sequences are split (else null) the workspace: chunk end states, then
@@ -93,7 +95,7 @@ struct StepArgs {
   float norm_eps;
   int64_t B, H, slots;
   int dv;
-  int erase, exclusive;
+  int erase, exclusive, zero_unused;
 };
 
 // ---- launchers (host) ----
@@ -157,7 +159,9 @@ __device__ __forceinline__ int64_t slot_of(const int32_t* index, int64_t b, int6
 // sequence's first item lie at least ceil(len / C) (and at least 1) further,
 // so items never collide, an empty sequence still has one item, and
 // floor(T / C) + B items hold them all.  An item past its sequence's chunks
-// has nothing to do.
+// has nothing to do; those behind the last sequence's hold the rows behind it,
+// all of them: its items go on up to floor(T / C) + B - 1, chunks enough for
+// T - off[B - 1] tokens.
 struct SeqItem {
   int64_t b;      // sequence
   int64_t row0;   // its first row in a packed buffer (0 for equal sequences)

@@ -120,6 +120,7 @@ gdn_status_t conv_check(const gdn_conv_problem_t* p, bool step, const void* x, c
   const int32_t* off = step ? nullptr : p->seq_offsets;
   if (B < 1 || B > kMost || T < 0 || T > kMost || D < 1 || D > kMost) return GDN_ERR_INVALID_ARGUMENT;
   if (p->activation != GDN_ACT_NONE && p->activation != GDN_ACT_SILU) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->options & ~GDN_LAYER_OPT_ZERO_UNUSED) return GDN_ERR_INVALID_ARGUMENT;
   if (p->dtype != GDN_DTYPE_F32 && p->dtype != GDN_DTYPE_BF16) return GDN_ERR_UNSUPPORTED;
   if (p->width < 2 || p->width > 4) return GDN_ERR_UNSUPPORTED;
   const int64_t x_st = step ? 0 : p->x_stride_t, o_st = step ? 0 : p->out_stride_t;
@@ -152,6 +153,7 @@ gdn_status_t conv_check(const gdn_conv_problem_t* p, bool step, const void* x, c
   a->B = B; a->T = T; a->D = D; a->slots = p->slots;
   a->x_sb = p->x_stride_b; a->x_st = x_st; a->o_sb = p->out_stride_b; a->o_st = o_st;
   a->silu = p->activation == GDN_ACT_SILU;
+  a->zero_unused = (p->options & GDN_LAYER_OPT_ZERO_UNUSED) != 0;
   *aligned = D * es % 16 == 0 && is_aligned(state_in, 16) && is_aligned(state_out, 16) &&
              rows_aligned(x, es, B, p->x_stride_b, T, x_st, off) && rows_aligned(out, es, B, p->out_stride_b, T, o_st, off);
   return GDN_OK;
@@ -163,7 +165,7 @@ gdn_status_t ssm_sizes(const gdn_ssm_problem_t* p, bool step) {
   const int64_t B = p->B, T = step ? 1 : p->T, D = p->D, N = p->N, G = p->G;
   if (B < 1 || B > kMost || T < 0 || T > kMost || D < 1 || D > kMost || N < 1 || G < 1 || G > D || D % G != 0)
     return GDN_ERR_INVALID_ARGUMENT;
-  if (p->options & ~GDN_SSM_OPT_SOFTPLUS) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->options & ~(GDN_SSM_OPT_SOFTPLUS | GDN_LAYER_OPT_ZERO_UNUSED)) return GDN_ERR_INVALID_ARGUMENT;
   if (p->dtype != GDN_DTYPE_F32 && p->dtype != GDN_DTYPE_BF16) return GDN_ERR_UNSUPPORTED;
   if (N > 256) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
@@ -232,6 +234,7 @@ gdn_status_t ssm_check(const gdn_ssm_problem_t* p, bool step, const void* x, con
   a->x_sb = sb[0]; a->dt_sb = sb[1]; a->b_sb = sb[2]; a->c_sb = sb[3]; a->o_sb = sb[4]; a->z_sb = sb[5];
   a->x_st = st[0]; a->dt_st = st[1]; a->b_st = st[2]; a->c_st = st[3]; a->o_st = st[4]; a->z_st = st[5];
   a->softplus = (p->options & GDN_SSM_OPT_SOFTPLUS) != 0;
+  a->zero_unused = (p->options & GDN_LAYER_OPT_ZERO_UNUSED) != 0;
   a->vec4 = N % 4 == 0 && is_aligned(A, 16) && is_aligned(state_in, 16) && is_aligned(state_out, 16);
   return GDN_OK;
 }
@@ -386,7 +389,7 @@ extern "C" gdn_status_t gdn_step(const gdn_step_problem_t* p, const void* q, con
   if (!p) return GDN_ERR_INVALID_ARGUMENT;
   const int64_t B = p->B, H = p->H, dk = p->dk, dv = p->dv;
   if (B < 1 || B > kMost || H < 1 || H > kMost || dk < 1 || dv < 1) return GDN_ERR_INVALID_ARGUMENT;
-  if (p->options & ~(GDN_OPT_NO_ERASE | GDN_OPT_EXCLUSIVE_FORWARD)) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->options & ~(GDN_OPT_NO_ERASE | GDN_OPT_EXCLUSIVE_FORWARD | GDN_LAYER_OPT_ZERO_UNUSED)) return GDN_ERR_INVALID_ARGUMENT;
   if (p->gate && (!p->norm_weight || !(p->norm_eps >= 0.f) || !(p->norm_eps <= 3.4e38f))) return GDN_ERR_INVALID_ARGUMENT;
   if (p->dtype != GDN_DTYPE_F32 && p->dtype != GDN_DTYPE_BF16) return GDN_ERR_UNSUPPORTED;
   if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return GDN_ERR_UNSUPPORTED;
@@ -416,6 +419,7 @@ extern "C" gdn_status_t gdn_step(const gdn_step_problem_t* p, const void* q, con
   a.B = B; a.H = H; a.slots = p->slots; a.dv = (int)dv;
   a.erase = (p->options & GDN_OPT_NO_ERASE) ? 0 : 1;
   a.exclusive = (p->options & GDN_OPT_EXCLUSIVE_FORWARD) != 0;
+  a.zero_unused = (p->options & GDN_LAYER_OPT_ZERO_UNUSED) != 0;
   hipStream_t stream = static_cast<hipStream_t>(p->stream);
   return launched(p->dtype == GDN_DTYPE_BF16 ? launch_step<bf16>(a, (int)dk, stream) : launch_step<float>(a, (int)dk, stream));
 }

@@ -61,6 +61,7 @@ struct Chunk {
   int64_t item;         // its place in the workspace
   int64_t t0, t1, len;  // tokens of the sequence
   int64_t row0;         // first row of a packed sequence
+  int64_t clear;        // rows of no sequence from this item's tokens on, up to this one (0: none)
   bool work;
 };
 
@@ -83,6 +84,12 @@ __device__ __forceinline__ Chunk chunk_of(const SsmArgs& a, int64_t item) {
   c.t0 = k * a.chunk;
   c.t1 = c.t0 + a.chunk < c.len ? c.t0 + a.chunk : c.len;
   c.work = k >= 0 && (c.t0 < c.len || k == 0);
+  // the last sequence's items also hold the rows behind it
+  c.clear = 0;
+  if (a.zero_unused && a.off && c.b == a.B - 1 && k >= 0) {
+    c.clear = a.T - c.row0 < c.t0 + a.chunk ? a.T - c.row0 : c.t0 + a.chunk;
+    if (c.clear <= c.t1 || c.clear <= c.t0) c.clear = 0;
+  }
   return c;
 }
 
@@ -150,8 +157,7 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
   const int ng = wave / CT, ct = wave % CT;            // this wave's entries and channel tile
   const unsigned tiles = (unsigned)tiles_per_group * (unsigned)a.G;
   const Chunk c = chunk_of(a, blockIdx.x / tiles);
-  if (!c.work) return;
-  if (STATES && c.t1 >= c.len) return;  // nothing follows the last chunk
+  if (STATES ? !c.work || c.t1 >= c.len : !c.work && !c.clear) return;  // (nothing follows a sequence's last chunk)
   const unsigned tile = blockIdx.x % tiles, g = tile / (unsigned)tiles_per_group;
   // the wave's first channel (uniform) and the lane's behind it; lanes without
   // a channel repeat the group's last one and store nothing
@@ -162,6 +168,11 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
   const bool live = want + lane < end;
   const unsigned dl = live ? lane : (unsigned)(end - 1 - d0);
   const int64_t d = d0 + dl;
+  if (!STATES && c.clear) {
+    if (live && ng == 0)
+      for (int64_t t = c.t0 > c.t1 ? c.t0 : c.t1; t < c.clear; ++t) static_cast<MT*>(a.out)[(c.row0 + t) * a.o_st + d] = (MT)0.0f;
+    if (!c.work) return;  // the whole workgroup
+  }
   const int64_t slot = slot_of(a.index, c.b, a.slots);
   const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f, skip = a.skip ? a.skip[d] : 0.0f;
 
@@ -461,7 +472,15 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
 #pragma unroll
     for (int i = 0; i < kChannels; ++i) A[q][i] = *reinterpret_cast<const Entries<float, V>*>(Ab + c[i] * (unsigned)N + (in ? n : 0));
   }
-  if (slot < 0) return;  // the whole workgroup
+  MT* po = static_cast<MT*>(a.out) + b * a.o_sb + base;
+  if (slot < 0) {  // the whole workgroup
+    if (a.zero_unused) {
+#pragma unroll
+      for (int i = 0; i < kChannels; ++i)
+        if (live[i] && l == 0) po[c[i]] = (MT)0.0f;
+    }
+    return;
+  }
   float* S = a.state_out + (slot * a.D + base) * N;
 #pragma unroll
   for (int q = 0; q < PARTS; ++q) {
@@ -490,7 +509,6 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
 #pragma unroll
     for (int i = 0; i < kChannels; ++i) y[i] += __shfl_xor(y[i], m, 64);
   }
-  MT* po = static_cast<MT*>(a.out) + b * a.o_sb + base;
 #pragma unroll
   for (int i = 0; i < kChannels; ++i) {
     if (!live[i] || l != (L >= kChannels ? i : 0)) continue;

@@ -57,7 +57,10 @@ __global__ __launch_bounds__(WAVES * 64) void step_kernel(StepArgs a) {
   const int sub = lane / LANES, l = lane % LANES;
   const int64_t bh = blockIdx.x, b = bh / a.H, h = bh % a.H;
   const int64_t slot = slot_of(a.index, b, a.slots);
-  if (slot < 0) return;  // the whole workgroup
+  if (slot < 0) {  // the whole workgroup
+    if (a.zero_unused && threadIdx.x < DV) a.out[bh * DV + threadIdx.x] = 0.0f;
+    return;
+  }
   float* S = a.state + (slot * a.H + h) * (DV * DK) + (wave * ROWS + sub) * DK + l * 4;
   f32x4 s[LOADS];
 #pragma unroll

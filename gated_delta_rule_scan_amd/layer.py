@@ -9,7 +9,10 @@ package, whose names these are.  Every call takes ``stream`` (a
 ``torch.cuda.Stream``; the current one of the tensors' device by default).
 Prompts come as equal sequences ([B, T, ...]) or packed ([T, ...] with
 ``seq_offsets`` [B + 1] int32); operands may be strided views whose last
-dimension is contiguous (the halves of one projection, say).
+dimension is contiguous (the halves of one projection, say).  Rows of the
+output that belong to no sequence (behind the last one of a packed batch; a
+step's row whose ``state_index`` is out of range) are zero in an output made by
+the call, and stay as they were in one that is given.
 """
 from __future__ import annotations
 
@@ -66,8 +69,8 @@ def causal_conv(x, weight, bias=None, state_in=None, activation: str = "silu", s
 def causal_conv_step(x, weight, bias=None, state=None, activation: str = "silu", state_index=None, out=None,
                      stream=None):
     """The convolution of one new token per sequence: x [B, D]; ``state`` [slots, W - 1, D] is read and advanced in
-    place.  A row whose ``state_index`` is out of range is skipped: its output row and every state stay as they
-    were.  Returns out [B, D]."""
+    place.  A row whose ``state_index`` is out of range is skipped: no state changes, and its output row is zero (in
+    a given ``out``: as it was).  Returns out [B, D]."""
     return _native().causal_conv_step(x, weight, bias, state, _activation(activation), state_index, out, stream)
 
 

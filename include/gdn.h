@@ -333,8 +333,15 @@ gdn_status_t gdn_vda_forward(const gdn_vda_problem_t* p,
  * of one call may name the same slot.  Without it, slots = B and sequence b
  * uses row b.
  *
+ * Rows of no sequence.  GDN_LAYER_OPT_ZERO_UNUSED, an option of the calls with
+ * packed batches or slots, sets the rows of `out` that the paragraphs above
+ * leave alone (behind the last sequence; of a step without a slot) to zero: for
+ * an output that holds nothing yet.
+ *
  * A float parameter pointer is fp32; x-like operands are fp32 or bf16
  * (`dtype`).  All arithmetic is fp32 with one rounding at the end. */
+
+typedef enum { GDN_LAYER_OPT_ZERO_UNUSED = 256 } gdn_layer_option_t;
 
 typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation_t;
 
@@ -355,6 +362,7 @@ typedef struct {
   int32_t dtype;             /* gdn_dtype_t: type of x, out and the states */
   int32_t width;
   int32_t activation;        /* gdn_activation_t */
+  int32_t options;           /* 0 or GDN_LAYER_OPT_ZERO_UNUSED */
   const int32_t* seq_offsets;
   const int32_t* state_index;
   void* stream;
@@ -395,7 +403,7 @@ typedef struct {
   int64_t out_stride_b, out_stride_t;
   int64_t slots;
   int32_t dtype;             /* gdn_dtype_t: type of x, dt, z, Bm, Cm and out */
-  int32_t options;           /* 0 or GDN_SSM_OPT_SOFTPLUS */
+  int32_t options;           /* of GDN_SSM_OPT_SOFTPLUS, GDN_LAYER_OPT_ZERO_UNUSED */
   const int32_t* seq_offsets;
   const int32_t* state_index;
   const void* z;
@@ -464,8 +472,9 @@ gdn_status_t gdn_rotary(const gdn_rotary_problem_t* p, const void* q, const void
  * direction) for each of B sequences, the state advanced in place:
  *   S' = a S (I - beta k^ k^T) + beta v k^T,  o = S' q^
  * with q^, k^ normalised and a = exp(log_alpha), as in gdn_forward.  Options:
- * GDN_OPT_NO_ERASE and GDN_OPT_EXCLUSIVE_FORWARD (o = a S q^); gate,
- * norm_weight and norm_eps are gdn_problem_t's readout epilogue.
+ * GDN_OPT_NO_ERASE, GDN_OPT_EXCLUSIVE_FORWARD (o = a S q^) and
+ * GDN_LAYER_OPT_ZERO_UNUSED; gate, norm_weight and norm_eps are gdn_problem_t's
+ * readout epilogue.
  *   q, k       [B, H, dk] (dtype); v, gate [B, H, dv] (dtype), 16-byte aligned
  *   log_alpha, beta  [B, H] fp32
  *   state      [slots, H, dv, dk] fp32, 16-byte aligned
