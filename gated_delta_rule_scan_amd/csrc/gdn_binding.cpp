@@ -7,6 +7,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -106,27 +107,20 @@ void rows(const Tensor& t, IntArrayRef shape, const Tensor& like, const char* na
 
 void* ptr(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
-// Memory of the current stream, without the dispatcher's part of a call (0.3 us).
-Tensor fresh(IntArrayRef sizes, ScalarType type, const Tensor& like) {
-  return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
-}
-
 // (its rows of no sequence hold nothing yet)
 int32_t unused_rows(const Tensor* out) { return out ? 0 : GDN_LAYER_OPT_ZERO_UNUSED; }
 
-Tensor output(const Tensor* out, const Tensor& like, const char* name = "out") {
-  if (!out) return fresh(like.sizes(), like.scalar_type(), like);
-  rows(*out, like.sizes(), like, name);
-  return *out;
-}
-
 // The stream of a call: the current one of the tensors' device, or the
-// caller's, which then keeps alive what was allocated here.
+// caller's.  What the call allocates belongs to it: a block of another stream's
+// memory may still be read or written by that stream's earlier work.  Tensors
+// that the caller gets back are meant for the current stream too, which keeps
+// their blocks from reuse when they are freed.
 struct Stream {
   void* raw;
   bool other = false;
   c10::Stream stream;
-  Stream(PyObject* o, const Tensor& x) : raw(nullptr), stream(c10::Stream::DEFAULT, x.device()) {
+  c10::Device device;
+  Stream(PyObject* o, const Tensor& x) : raw(nullptr), stream(c10::Stream::DEFAULT, x.device()), device(x.device()) {
     const c10::hip::HIPStream now = c10::hip::getCurrentHIPStream(x.get_device());
     raw = now.stream();
     if (o == Py_None) return;
@@ -146,10 +140,24 @@ struct Stream {
     }
     return v;
   }
-  void keeps(const Tensor& t) const {
-    if (other) t.record_stream(stream);
+  // (without the dispatcher's part of a call, 0.3 us)
+  Tensor fresh(IntArrayRef sizes, ScalarType type, bool returned = true) const {
+    if (!other) return at::detail::empty_cuda(sizes, type, device, std::nullopt);
+    Tensor t;
+    {
+      const c10::StreamGuard guard(stream);
+      t = at::detail::empty_cuda(sizes, type, device, std::nullopt);
+    }
+    if (returned) t.record_stream(c10::impl::VirtualGuardImpl(device.type()).getStream(device));
+    return t;
   }
 };
+
+Tensor output(const Stream& s, const Tensor* out, const Tensor& like, const char* name = "out") {
+  if (!out) return s.fresh(like.sizes(), like.scalar_type());
+  rows(*out, like.sizes(), like, name);
+  return *out;
+}
 
 void check(gdn_status_t st) {
   if (st != GDN_OK) throw Failed{(int)st};
@@ -175,8 +183,7 @@ void lead(const Tensor& x, const Tensor* off, int64_t* B, int64_t* T) {
 struct States {
   int64_t slots;
   Tensor out;  // undefined: none
-  bool made = false;
-  States(int64_t B, int64_t d1, int64_t d2, ScalarType type, const Tensor& x, const Tensor* in, const Tensor* given_out,
+  States(const Stream& s, int64_t B, int64_t d1, int64_t d2, ScalarType type, const Tensor& x, const Tensor* in, const Tensor* given_out,
          const Tensor* index, bool wanted)
       : slots(B) {
     if (index) want(*index, {B}, at::kInt, x, "state_index");
@@ -190,8 +197,7 @@ struct States {
       out = *given_out;
     } else if (wanted) {
       if (index) refuse("state_out must be given with state_index (or want_state=False)");
-      out = fresh({B, d1, d2}, type, x);
-      made = true;
+      out = s.fresh({B, d1, d2}, type);
     }
   }
   void* address() const { return out.defined() ? out.data_ptr() : nullptr; }
@@ -229,10 +235,8 @@ PyObject* conv(PyObject* const* a) {
   const float* pw = param(&w, {D, W}, at::kFloat, x, "weight");
   const float* pb = param(bias, {D}, at::kFloat, x, "bias");
   const Stream s(a[10], x);
-  const States st(p.B, W - 1, D, x.scalar_type(), x, in, so, index, a[9] == Py_True);
-  const Tensor y = output(out, x);
-  if (!out) s.keeps(y);
-  if (st.made) s.keeps(st.out);
+  const States st(s, p.B, W - 1, D, x.scalar_type(), x, in, so, index, a[9] == Py_True);
+  const Tensor y = output(s, out, x);
   p.D = D;
   p.x_stride_b = off ? 0 : x.stride(0);
   p.x_stride_t = x.stride(-2);
@@ -264,8 +268,7 @@ PyObject* conv_step(PyObject* const* a) {
   const float* pb = param(bias, {D}, at::kFloat, x, "bias");
   p.slots = step_slots(state, {W - 1, D}, x.scalar_type(), x, index, p.B);
   const Stream s(a[7], x);
-  const Tensor y = output(out, x);
-  if (!out) s.keeps(y);
+  const Tensor y = output(s, out, x);
   p.T = 1;
   p.D = D;
   p.x_stride_b = x.stride(0);
@@ -336,23 +339,18 @@ PyObject* ssm(PyObject* const* a) {
   const Tensor *out = tensor(a[12], "out"), *so = tensor(a[13], "state_out"), *ws = tensor(a[15], "workspace");
   lead(x, off, &p.B, &p.T);
   const Stream s(a[16], x);
-  const States st(p.B, p.D, p.N, at::kFloat, x, in, so, index, a[14] == Py_True);
-  const Tensor y = output(out, x);
-  if (!out) s.keeps(y);
-  if (st.made) s.keeps(st.out);
+  const States st(s, p.B, p.D, p.N, at::kFloat, x, in, so, index, a[14] == Py_True);
+  const Tensor y = output(s, out, x);
   q.strides(y, off ? -1 : 0, off ? 0 : 1);
   p.options |= unused_rows(out);
   p.slots = st.slots;
   p.seq_offsets = static_cast<const int32_t*>(ptr(off));
   p.state_index = static_cast<const int32_t*>(ptr(index));
-  Tensor mine;  // freed when the call returns: its stream keeps it
+  Tensor mine;  // freed when the call returns: later work of its stream may have it
   if (const int64_t size = (int64_t)f_ssm_workspace(&p)) {
     if (ws && (ws->scalar_type() != at::kByte || ws->device() != x.device() || !ws->is_contiguous()))
       refuse("workspace must be a contiguous uint8 tensor on " + x.device().str());
-    if (!ws || ws->numel() < size) {
-      mine = fresh({size}, at::kByte, x);
-      s.keeps(mine);
-    }
+    if (!ws || ws->numel() < size) mine = s.fresh({size}, at::kByte, false);
     const Tensor& w = mine.defined() ? mine : *ws;
     p.workspace = w.data_ptr();
     p.workspace_bytes = (size_t)w.numel();
@@ -375,8 +373,7 @@ PyObject* ssm_step(PyObject* const* a) {
   p.T = 1;
   p.slots = step_slots(state, {p.D, p.N}, at::kFloat, x, index, p.B);
   const Stream s(a[12], x);
-  const Tensor y = output(out, x);
-  if (!out) s.keeps(y);
+  const Tensor y = output(s, out, x);
   q.strides(y, 0, -1);
   p.options |= unused_rows(out);
   p.state_index = static_cast<const int32_t*>(ptr(index));
@@ -441,12 +438,10 @@ PyObject* rotary(PyObject* const* a) {
     if (n == 1 && p.section[0] != pairs) refuse("sections must add up to " + std::to_string(pairs) + " pairs");
   }
   const Stream s(a[10], q);
-  const Tensor y = output(qo, q, "q_out");
-  if (!qo) s.keeps(y);
+  const Tensor y = output(s, qo, q, "q_out");
   Tensor yk;
   if (k) {
-    yk = output(ko, *k, "k_out");
-    if (!ko) s.keeps(yk);
+    yk = output(s, ko, *k, "k_out");
     p.k_stride_b = k->stride(0), p.k_stride_t = k->stride(1), p.k_stride_h = k->stride(2);
     p.k_out_stride_b = yk.stride(0), p.k_out_stride_t = yk.stride(1), p.k_out_stride_h = yk.stride(2);
   }
@@ -489,8 +484,7 @@ PyObject* delta_step(PyObject* const* a) {
     want(*out, {p.B, p.H, p.dv}, at::kFloat, q, "out");
     y = *out;
   } else {
-    y = fresh({p.B, p.H, p.dv}, at::kFloat, q);
-    s.keeps(y);
+    y = s.fresh({p.B, p.H, p.dv}, at::kFloat);
   }
   p.options = (int32_t)whole(a[7], "options") | unused_rows(out);
   p.norm_eps = real(a[10], "norm_eps");

@@ -6,7 +6,10 @@ Argument checks and marshalling only, as in the package's other calls, here in
 native code (``csrc/gdn_binding.cpp``): the steps run a few microseconds, and
 the same checks in Python took longer than the launch.  Imported by the
 package, whose names these are.  Every call takes ``stream`` (a
-``torch.cuda.Stream``; the current one of the tensors' device by default).
+``torch.cuda.Stream``; the current one of the tensors' device by default): its
+work, and the memory of what it allocates, belong to that stream.  With one that
+is not the current one the caller orders the two, as for any work: inputs are
+ready on ``stream``, and the current stream waits for it before it uses results.
 Prompts come as equal sequences ([B, T, ...]) or packed ([T, ...] with
 ``seq_offsets`` [B + 1] int32); operands may be strided views whose last
 dimension is contiguous (the halves of one projection, say).  Rows of the

@@ -1,0 +1,87 @@
+"""Calls on a stream that is not the current one: what a call allocates shares no memory with work that is still
+pending on the current stream, and what it returns may be used and freed there."""
+import pytest
+
+from test_gpu_layer import Rng, _ssm_inputs
+
+pytestmark = pytest.mark.gpu
+
+LONG = 20_000_000  # cycles of waiting on the device, some ten milliseconds
+
+
+def _calls():
+    """name -> (call(stream), sizes in bytes of what it allocates)."""
+    import torch
+
+    import gated_delta_rule_scan_amd as gdn
+
+    r = Rng(61)
+    B, T, D, N, H, d = 3, 1200, 136, 16, 4, 64
+    w, x, t = r.t(D, 4), r.t(B, T, D), r.t(B, D)
+    kw, tk = _ssm_inputs(r, "f32", (B, T), D, N, 1, True, True, True, True), _ssm_inputs(r, "f32", (B,), D, N, 1, True, True, True, True)
+    q, f = r.t(B, T, H, d), gdn.rotary_frequencies(d)[0].cuda()
+    q0 = q[:, 0].contiguous()
+    la, beta = -r.t(B, H).abs(), torch.sigmoid(r.t(B, H))
+    cs, hs, S = r.t(B, 3, D), r.t(B, D, N), r.t(B, H, d, d)
+    p = gdn.gdn_ssm_problem_t(B=B, T=T, D=D, N=N, G=1, dtype=gdn.GDN_DTYPE_F32)
+    ws = gdn.gdn_ssm_workspace_bytes(p)
+    assert ws
+    many = lambda y: y if isinstance(y, tuple) else (y,)
+    out = {
+        "conv": (lambda s: gdn.causal_conv(x, w, stream=s), [x.numel() * 4, cs.numel() * 4]),
+        "conv step": (lambda s: gdn.causal_conv_step(t, w, None, cs.clone() if s is None else cs, stream=s), [t.numel() * 4]),
+        "scan": (lambda s: gdn.selective_scan(**kw, stream=s), [x.numel() * 4, hs.numel() * 4, ws]),
+        "step": (lambda s: gdn.selective_step(**tk, state=hs.clone() if s is None else hs, stream=s), [t.numel() * 4]),
+        "rotary": (lambda s: gdn.rotary(q, q, f, stream=s), [q.numel() * 4]),
+        "delta step": (lambda s: gdn.delta_step(q0, q0, q0, la, beta, S.clone() if s is None else S, stream=s), [q0.numel() * 4]),
+    }
+    return {k: ((lambda s, fn=fn: many(fn(s))), sizes) for k, (fn, sizes) in out.items()}
+
+
+NAMES = ["conv", "conv step", "scan", "step", "rotary", "delta step"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_results_share_no_memory_with_pending_work(name):
+    """Blocks of the very sizes that the call allocates are freed on the current stream while a fill of them is still
+    to come there."""
+    import torch
+
+    call, sizes = _calls()[name]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(LONG)
+    late = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255) for n in sizes for _ in range(3)]
+    taken = {t.data_ptr() for t in late}
+    del late
+    got = call(side)
+    assert not taken & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_results_freed_on_the_current_stream(name):
+    """A result that the current stream has still to read is freed: the side stream's next tensors leave it alone."""
+    import torch
+
+    call, _ = _calls()[name]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(LONG)
+    copies = [t.clone() for t in got]
+    shapes = [t.shape for t in got]
+    del got
+    with torch.cuda.stream(side):
+        junk = [torch.full(s, float("nan"), device="cuda") for s in shapes for _ in range(3)]
+    torch.cuda.synchronize()
+    for a, b in zip(copies, want):
+        assert torch.equal(a, b)
+    del junk
