@@ -15,6 +15,7 @@ operators a recurrent layer runs around its scan (``causal_conv``, ``rotary``,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -264,16 +265,30 @@ def gdn_version() -> str:
     return lib().gdn_version().decode()
 
 
-def _record_on(stream, tensors) -> None:
-    """Tensors the binding allocated on the current stream but hands to work
-    on another ``stream``: tell torch's caching allocator that ``stream`` uses
-    them, so their memory is not given to new allocations until that work is
-    done (the workspace and any temporary are freed when the call returns)."""
+_SAME = contextlib.nullcontext()
+
+
+def _owned_by(stream, device):
+    """A context in which what the binding allocates (and copies) belongs to the
+    caller's ``stream``: a block of the current stream's memory may still be read
+    or written by earlier work there, with which nothing orders the call."""
+    if stream is None:
+        return _SAME
     import torch
 
-    if stream != torch.cuda.current_stream(stream.device):
+    if stream.device != device:
+        raise ValueError(f"stream must be one of {device}")
+    return torch.cuda.stream(stream)
+
+
+def _returned(stream, tensors) -> None:
+    """Results allocated for ``stream`` are meant for the current stream too: when
+    they are freed, their memory waits for what that has still to do with them."""
+    import torch
+
+    if stream is not None:
         for t in tensors:
-            t.record_stream(stream)
+            t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def make_problem(B, T, H, dk, dv, dtype: int, chunk: int = 0, dv_tile: int = 0, workspace: int = 0,
@@ -300,6 +315,10 @@ def forward(q, k, v, log_alpha, beta, state_in=None, direction: str = "fwd", chu
     log_alpha, beta: [dirs,B,T,H] float32; state_in: [dirs,B,H,dv,dk] float32 or None.
     Returns (out [B,T,H,dv] float32, state_out or None).  ``state_out`` may be
     passed as the same tensor as ``state_in`` for an in-place carry.
+    ``stream``: the call's work, and the memory of what it allocates, belong to it
+    (default: the current stream).  With one that is not the current one the
+    caller orders the two: inputs are ready on ``stream``, and the current stream
+    waits for it before it uses results.
     ``serial`` keeps both kernels on ``stream`` (GDN_OPT_SERIAL); otherwise the
     library may run the chunk preparation concurrently on its own stream.
     ``erase=False`` selects the erase-free variant (GDN_OPT_NO_ERASE: gated
@@ -338,21 +357,22 @@ def forward(q, k, v, log_alpha, beta, state_in=None, direction: str = "fwd", chu
         raise ValueError(f"state_in must be contiguous float32 [{dirs},{B},{H},{dv},{dk}]")
     dev = q.device
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    mine = []  # tensors allocated here (on the current stream)
-    if out is None:
-        out = torch.empty((B, T, H, dv), dtype=torch.float32, device=dev)
-        mine.append(out)
-    if state_out is None and want_state:
-        state_out = torch.empty((dirs, B, H, dv, dk), dtype=torch.float32, device=dev)
-        mine.append(state_out)
+    made = []  # results allocated here
+    with _owned_by(stream, dev):
+        if out is None:
+            out = torch.empty((B, T, H, dv), dtype=torch.float32, device=dev)
+            made.append(out)
+        if state_out is None and want_state:
+            state_out = torch.empty((dirs, B, H, dv, dk), dtype=torch.float32, device=dev)
+            made.append(state_out)
+    _returned(stream, made)
     if gate is not None:
         if gate.dtype != q.dtype or not gate.is_contiguous() or tuple(gate.shape) != (B, T, H, dv):
             raise ValueError(f"gate must be contiguous [{B},{T},{H},{dv}] of the type of q")
         if norm_weight is None or norm_weight.dtype != torch.float32 or tuple(norm_weight.shape) != (dv,):
             raise ValueError(f"norm_weight must be float32 [{dv}] when gate is given")
-        if not norm_weight.is_contiguous():
+        with _owned_by(stream, dev):
             norm_weight = norm_weight.contiguous()
-            mine.append(norm_weight)
     prob = make_problem(B, T, H, dk, dv, dt, chunk, dv_tile)
     prob.options = (GDN_OPT_SERIAL if serial else 0) | (0 if erase else GDN_OPT_NO_ERASE) | EXCLUSIVE[exclusive]
     if gate is not None:
@@ -361,9 +381,8 @@ def forward(q, k, v, log_alpha, beta, state_in=None, direction: str = "fwd", chu
     if nbytes == 0 and T > 0:
         raise GdnError(GDN_ERR_UNSUPPORTED)
     if nbytes > 0 and (workspace is None or workspace.numel() < nbytes):
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        mine.append(workspace)
-    _record_on(s, mine)
+        with _owned_by(stream, dev):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     prob.workspace = workspace.data_ptr() if workspace is not None else None
     prob.workspace_bytes = workspace.numel() if workspace is not None else 0
     prob.stream = s.cuda_stream
@@ -385,7 +404,7 @@ def vda_forward(q, k, v, log_alpha, beta, state_in=None, direction: str = "fwd",
     ``frame`` tokens); beta [dirs,B,T,H]; state_in [dirs,B,H,dv,dk] or None.
     ``write``: "inverse" (the operator) or "additive" (GDN_VDA_OPT_ADDITIVE);
     ``lag``: the readout lag in frames; ``gate`` [B,T,H,dv] (type of q) with
-    ``norm_weight`` [dv] float32: the readout epilogue.
+    ``norm_weight`` [dv] float32: the readout epilogue; ``stream`` as for ``forward``.
     Returns (out [B,T,H,dv] float32, state_out or None)."""
     import torch
 
@@ -411,13 +430,15 @@ def vda_forward(q, k, v, log_alpha, beta, state_in=None, direction: str = "fwd",
         raise ValueError(f"state_in must be contiguous float32 [{dirs},{B},{H},{dv},{dk}]")
     dev = q.device
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    mine = []  # tensors allocated here (on the current stream)
-    if out is None:
-        out = torch.empty((B, T, H, dv), dtype=torch.float32, device=dev)
-        mine.append(out)
-    if state_out is None and want_state:
-        state_out = torch.empty((dirs, B, H, dv, dk), dtype=torch.float32, device=dev)
-        mine.append(state_out)
+    made = []  # results allocated here
+    with _owned_by(stream, dev):
+        if out is None:
+            out = torch.empty((B, T, H, dv), dtype=torch.float32, device=dev)
+            made.append(out)
+        if state_out is None and want_state:
+            state_out = torch.empty((dirs, B, H, dv, dk), dtype=torch.float32, device=dev)
+            made.append(state_out)
+    _returned(stream, made)
     if write not in ("inverse", "additive"):
         raise ValueError("write must be 'inverse' or 'additive'")
     if gate is not None:
@@ -425,9 +446,8 @@ def vda_forward(q, k, v, log_alpha, beta, state_in=None, direction: str = "fwd",
             raise ValueError(f"gate must be contiguous [{B},{T},{H},{dv}] of the type of q")
         if norm_weight is None or norm_weight.dtype != torch.float32 or tuple(norm_weight.shape) != (dv,):
             raise ValueError(f"norm_weight must be float32 [{dv}] when gate is given")
-        if not norm_weight.is_contiguous():
+        with _owned_by(stream, dev):
             norm_weight = norm_weight.contiguous()
-            mine.append(norm_weight)
     prob = gdn_vda_problem_t(B=B, T=T, H=H, dk=dk, dv=dv, frame=frame, dtype=dt,
                              options=GDN_VDA_OPT_ADDITIVE if write == "additive" else 0, readout_lag=lag,
                              norm_eps=norm_eps, gate=None if gate is None else gate.data_ptr(),
@@ -436,9 +456,8 @@ def vda_forward(q, k, v, log_alpha, beta, state_in=None, direction: str = "fwd",
     if nbytes == 0 and T > 0:
         raise GdnError(GDN_ERR_UNSUPPORTED)
     if nbytes > 0 and (workspace is None or workspace.numel() < nbytes):
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        mine.append(workspace)
-    _record_on(s, mine)
+        with _owned_by(stream, dev):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     prob.workspace = workspace.data_ptr() if workspace is not None else None
     prob.workspace_bytes = workspace.numel() if workspace is not None else 0
     prob.stream = s.cuda_stream

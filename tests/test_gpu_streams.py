@@ -35,10 +35,23 @@ def _calls():
         "rotary": (lambda s: gdn.rotary(q, q, f, stream=s), [q.numel() * 4]),
         "delta step": (lambda s: gdn.delta_step(q0, q0, q0, la, beta, S.clone() if s is None else S, stream=s), [q0.numel() * 4]),
     }
+    # the scans themselves, the epilogue's weight a view that the call copies
+    sq, sv = r.t(1, 700, H, d), r.t(1, 700, H, d)
+    gate, nw = r.t(1, 700, H, d), r.t(d, 2)[:, 0]
+    sla, sbeta = -r.t(1, 1, 700, H).abs(), torch.sigmoid(r.t(1, 1, 700, H))
+    fla = -r.t(1, 1, 7, H).abs()
+    kw2 = dict(gate=gate, norm_weight=nw)
+    ws = gdn.workspace_bytes(1, 700, H, d, d, "f32")
+    assert ws
+    p = gdn.gdn_vda_problem_t(B=1, T=700, H=H, dk=d, dv=d, frame=100, dtype=gdn.GDN_DTYPE_F32)
+    fws = gdn.gdn_vda_workspace_bytes(p, gdn.DIRECTIONS["fwd"])
+    sizes = [sq.numel() * 4, H * d * d * 4, d * 4]
+    out["token scan"] = (lambda s: gdn.forward(sq, sq, sv, sla, sbeta, stream=s, **kw2), sizes + [ws])
+    out["frame-wise scan"] = (lambda s: gdn.vda_forward(sq, sq, sv, fla, sbeta, frame=100, stream=s, **kw2), sizes + [max(fws, 1)])
     return {k: ((lambda s, fn=fn: many(fn(s))), sizes) for k, (fn, sizes) in out.items()}
 
 
-NAMES = ["conv", "conv step", "scan", "step", "rotary", "delta step"]
+NAMES = ["conv", "conv step", "scan", "step", "rotary", "delta step", "token scan", "frame-wise scan"]
 
 
 @pytest.mark.parametrize("name", NAMES)
