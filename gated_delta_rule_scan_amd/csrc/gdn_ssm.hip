@@ -15,10 +15,10 @@ __device__ __forceinline__ float step_size(const SsmArgs& a, float dt, float bia
 
 // A for base-2 exponents.  Minus infinity becomes the lowest number: its
 // product with a step size of zero is zero, not NaN.
+constexpr float kLargest = 3.402823466e38f;
 __device__ __forceinline__ float rate(float A) {
-  constexpr float kLowest = -3.402823466e38f;
   const float r = A * kLog2e;
-  return r < kLowest ? kLowest : r;
+  return r < -kLargest ? -kLargest : r;
 }
 
 // ---- prompts ----
@@ -145,7 +145,11 @@ __device__ __forceinline__ void store_entries(float* p, int wide, int vec4, cons
   }
 }
 
-template <typename MT, int NN, bool STATES, bool MULTI, bool GATE>
+// PADDED, for the readout: some wave has fewer than NN entries.  The rest stay
+// zero by their zero B, but for an infinite input, whose product with it is NaN:
+// such a token's are cleared, and its readout taken again.  (One test a token,
+// below 1%; a mask an entry took 4% with up to 32 entries and 13% with more.)
+template <typename MT, int NN, bool STATES, bool MULTI, bool GATE, bool PADDED>
 __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, int waves_n, int CT, int tiles_per_group) {
   constexpr int ES = sizeof(MT), STEP = 64 / NN;       // tokens of B (or C) that a wave loads at a time
   constexpr int ROUNDS = kStage / STEP;
@@ -242,6 +246,8 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
     pd += (uint64_t)kStage * sd;
   };
 
+  constexpr int kWhole = MULTI || NN == 8 ? 1 : NN / 2 + 1;         // entries that every wave has
+  unsigned there = wide < 32 ? (1u << wide) - 1 : 0xFFFFFFFFu;  // bit n: entry n is there
   double total = 0.0;  // of the step sizes: a chunk may have very many
   float* partial = lds + NG * CT * 2 * kStage * NN + wave * kStage * 64 + lane;
   int left = (int)(c.t1 - c.t0);  // tokens not yet computed
@@ -294,6 +300,15 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
             if (m & 1) y1 = fmaf(h[n], C[m], y1);
             else y0 = fmaf(h[n], C[m], y0);
           }
+        }
+      }
+      if (PADDED && __builtin_expect(__any(!(fabsf(u) <= kLargest)), 0)) {
+        asm volatile("" : "+s"(there));  // masks made here: kept ready for all tokens they spill
+        y0 = y1 = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NN; ++n) {
+          if (n >= kWhole && !(there >> n & 1)) h[n] = 0.0f;
+          (n & 1 ? y1 : y0) = fmaf(h[n], stage[kStage * NN + i * NN + n], n & 1 ? y1 : y0);
         }
       }
       if (!STATES && !MULTI) {
@@ -472,12 +487,11 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
 #pragma unroll
     for (int i = 0; i < kChannels; ++i) A[q][i] = *reinterpret_cast<const Entries<float, V>*>(Ab + c[i] * (unsigned)N + (in ? n : 0));
   }
-  MT* po = static_cast<MT*>(a.out) + b * a.o_sb + base;
   if (slot < 0) {  // the whole workgroup
     if (a.zero_unused) {
 #pragma unroll
       for (int i = 0; i < kChannels; ++i)
-        if (live[i] && l == 0) po[c[i]] = (MT)0.0f;
+        if (live[i] && l == 0) (static_cast<MT*>(a.out) + b * a.o_sb + base)[c[i]] = (MT)0.0f;
     }
     return;
   }
@@ -497,10 +511,12 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
 #pragma unroll
     for (int q = 0; q < PARTS; ++q) {
       const int n = (q * L + l) * V;
+      if (V == 1 && n >= N) continue;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         h[q][i].e[e] = fmaf(hw_exp2(s * rate(A[q][i].e[e])), h[q][i].e[e], u * to_float(B[q].e[e]));
-        y[i] = fmaf(h[q][i].e[e], n < N ? to_float(C[q].e[e]) : 0.0f, y[i]);
+        // (lanes behind entry N run entry 0's state, infinite perhaps)
+        y[i] = n < N ? fmaf(h[q][i].e[e], to_float(C[q].e[e]), y[i]) : y[i];
       }
       if (live[i] && n < N) *reinterpret_cast<Entries<float, V>*>(S + c[i] * (unsigned)N + n) = h[q][i];
     }
@@ -509,6 +525,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
 #pragma unroll
     for (int i = 0; i < kChannels; ++i) y[i] += __shfl_xor(y[i], m, 64);
   }
+  MT* po = static_cast<MT*>(a.out) + b * a.o_sb + base;
 #pragma unroll
   for (int i = 0; i < kChannels; ++i) {
     if (!live[i] || l != (L >= kChannels ? i : 0)) continue;
@@ -518,6 +535,13 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
     const float v = fmaf(sk, x[i], y[i]);
     po[c[i]] = (MT)(a.z ? v * silu(zi) : v);
   }
+}
+
+template <typename MT, int NN, bool PADDED>
+auto scan_kernel(bool multi, bool gate) {
+  constexpr bool kMulti = NN == 32;
+  return multi ? (gate ? ssm_kernel<MT, NN, false, kMulti, true, PADDED> : ssm_kernel<MT, NN, false, kMulti, false, PADDED>)
+               : (gate ? ssm_kernel<MT, NN, false, false, true, PADDED> : ssm_kernel<MT, NN, false, false, false, PADDED>);
 }
 
 template <typename MT, int NN>
@@ -535,16 +559,15 @@ hipError_t ssm_launch(const SsmArgs& a, hipStream_t stream) {
   const int64_t carries = a.B * ((a.D * a.N * parts + 255) / 256);
   if (!grid_fits(blocks, threads) || !grid_fits(carries, 256)) return hipErrorNotSupported;
   constexpr bool kMulti = NN == 32;
-  const bool multi = kMulti && NG > 1;
+  const bool multi = kMulti && NG > 1, padded = a.N % NN != 0;
   const unsigned stage = (unsigned)(NG * CT * kStage * 2 * NN * sizeof(float));
   const unsigned partials = multi ? (unsigned)(NG * CT * kStage * 64 * sizeof(float)) : 0;
   if (a.ends) {
-    const auto states = multi ? ssm_kernel<MT, NN, true, kMulti, false> : ssm_kernel<MT, NN, true, false, false>;
+    const auto states = multi ? ssm_kernel<MT, NN, true, kMulti, false, false> : ssm_kernel<MT, NN, true, false, false, false>;
     hipLaunchKernelGGL(states, dim3((unsigned)blocks), dim3(threads), stage, stream, a, NG, CT, (int)tiles);
     hipLaunchKernelGGL(parts > 1 ? ssm_carry_kernel<kParts> : ssm_carry_kernel<1>, dim3((unsigned)carries), dim3(256), 0, stream, a);
   }
-  const auto scan = multi ? (a.z ? ssm_kernel<MT, NN, false, kMulti, true> : ssm_kernel<MT, NN, false, kMulti, false>)
-                          : (a.z ? ssm_kernel<MT, NN, false, false, true> : ssm_kernel<MT, NN, false, false, false>);
+  const auto scan = padded ? scan_kernel<MT, NN, true>(multi, a.z) : scan_kernel<MT, NN, false>(multi, a.z);
   hipLaunchKernelGGL(scan, dim3((unsigned)blocks), dim3(threads), stage + partials, stream, a, NG, CT, (int)tiles);
   return hipGetLastError();
 }

@@ -1,0 +1,95 @@
+"""Infinite inputs and states of the selective scan: where the formula gives an infinity, the operators give it, at any
+number of state entries."""
+import pytest
+
+from test_gpu_layer import Rng
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+ENTRIES = [1, 3, 5, 8, 12, 16, 20, 24, 33, 37, 64, 100, 256]
+
+
+def _inputs(lead, D, N, kind="f32", seed=51, rate=1.0):
+    """Positive inputs, B, C, skip and gate, so that every sum of the formula has one sign."""
+    import torch
+
+    r = Rng(seed)
+    pos = lambda *s, k=kind: (r.t(*s, kind=k).abs() + 0.25).to(torch.bfloat16 if k == "bf16" else torch.float32)
+    return dict(x=pos(*lead, D), dt=r.t(*lead, D, kind=kind, scale=0.5), A=-pos(D, N, k="f32") * rate, B=pos(*lead, N),
+                C=pos(*lead, N), D=pos(D, k="f32"), z=pos(*lead, D))
+
+
+@pytest.mark.parametrize("name", ["x", "dt"])
+@pytest.mark.parametrize("T", [1, 9, 70, 1003])
+@pytest.mark.parametrize("N", ENTRIES)
+def test_last_token(N, T, name):
+    """An infinite input or step size of the last token: output and state are infinite with the sign of C and of B,
+    and nothing else changes."""
+    import torch
+
+    import gated_delta_rule_scan_amd as gdn
+
+    for sign in (1.0, -1.0):
+        kw = _inputs((2, T), 80, N)
+        kw["C"], kw["D"] = kw["C"] * sign, kw["D"] * sign
+        ref, href = gdn.selective_scan(**kw)
+        kw[name] = kw[name].clone()
+        kw[name][1, T - 1, 70] = INF
+        y, h = gdn.selective_scan(**kw)
+        assert y[1, T - 1, 70] == sign * INF and (h[1, 70] == INF).all()
+        hit = torch.zeros_like(y, dtype=torch.bool)
+        hit[1, T - 1, 70] = True
+        assert torch.equal(y[~hit], ref[~hit])
+        h[1, 70] = href[1, 70]
+        assert torch.equal(h, href)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [30, 70, 300])
+@pytest.mark.parametrize("N", [1, 5, 12, 16, 20, 37, 64])
+def test_stays_infinite(N, T, kind):
+    """Behind an infinite input every output of the channel and its final state are infinite (decays above zero)."""
+    import torch
+
+    import gated_delta_rule_scan_amd as gdn
+
+    kw = _inputs((1, T), 70, N, kind, rate=0.3)
+    ref, href = gdn.selective_scan(**kw)
+    for at in (0, T // 2):
+        new = dict(kw, x=kw["x"].clone())
+        new["x"][0, at, 65] = INF
+        y, h = gdn.selective_scan(**new)
+        assert (y[0, at:, 65] == INF).all() and (h[0, 65] == INF).all()
+        y[0, at:, 65], h[0, 65] = ref[0, at:, 65], href[0, 65]
+        assert torch.equal(y, ref) and torch.equal(h, href)
+
+
+@pytest.mark.parametrize("N", ENTRIES)
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_step(N, kind):
+    """The single-token step: an infinite input, step size or state entry."""
+    import torch
+
+    import gated_delta_rule_scan_amd as gdn
+
+    kw = _inputs((3,), 37, N, kind)
+    state = torch.rand(3, 37, N, device="cuda")
+    s0 = state.clone()
+    ref = gdn.selective_step(**kw, state=s0)
+    for name in ("x", "dt", "first", "last"):
+        new, s = dict(kw), state.clone()
+        if name in kw:
+            new[name] = kw[name].clone()
+            new[name][1, 20] = INF
+        else:
+            s[1, 20, 0 if name == "first" else N - 1] = INF
+        y = gdn.selective_step(**new, state=s)
+        assert y[1, 20] == INF, name
+        if name in kw:
+            assert (s[1, 20] == INF).all(), name
+        else:
+            assert int((s[1, 20] == INF).sum()) == 1, name
+        assert not torch.isnan(y).any() and not torch.isnan(s).any()
+        y[1, 20], s[1, 20] = ref[1, 20], s0[1, 20]
+        assert torch.equal(y, ref) and torch.equal(s, s0)
