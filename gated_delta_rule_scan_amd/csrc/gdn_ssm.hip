@@ -312,7 +312,7 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
         }
       }
       if (!STATES && !MULTI) {
-        float y = fmaf(skip, xc[i], y0 + y1);
+        float y = fmaf(skip, a.skip ? xc[i] : 0.0f, y0 + y1);  // (no skip: nothing of x, infinite perhaps)
         if (GATE) y *= silu(zc[i]);
         buffer_store<MT>((MT)y, ro, in ? lane_out : kNowhere, i * so);
       }
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(512, NN == 32 ? 2 : 4) void ssm_kernel(SsmArgs a, i
       for (int i = 0; i < kStage; ++i) {
         if (turn == 0 && i < left) {
           const float* p = lds + NG * CT * 2 * kStage * NN + (ct * kStage + i) * 64 + lane;
-          float y = skip * xc[i];
+          float y = a.skip ? skip * xc[i] : 0.0f;
           for (int k = 0; k < NG; ++k) y += p[k * CT * kStage * 64];
           if (GATE) y *= silu(zc[i]);
           buffer_store<MT>((MT)y, ro, lane_out, i * so);
@@ -532,7 +532,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
     const bool own = L >= kChannels || i == 0;  // whose gate and skip this thread holds
     const float sk = own ? skipf : a.skip ? (a.skip + base)[c[i]] : 0.0f;
     const float zi = own ? zf : a.z ? to_float((static_cast<const MT*>(a.z) + b * a.z_sb + base)[c[i]]) : 0.0f;
-    const float v = fmaf(sk, x[i], y[i]);
+    const float v = a.skip ? fmaf(sk, x[i], y[i]) : y[i];
     po[c[i]] = (MT)(a.z ? v * silu(zi) : v);
   }
 }

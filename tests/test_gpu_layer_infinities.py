@@ -45,6 +45,28 @@ def test_last_token(N, T, name):
         assert torch.equal(h, href)
 
 
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 9, 70, 1003])
+@pytest.mark.parametrize("N", [1, 5, 8, 16, 32, 64, 100])
+def test_without_skip(N, T, kind, gate):
+    """No D: an infinite last input reaches the output through the state alone."""
+    import torch
+
+    import gated_delta_rule_scan_amd as gdn
+
+    kw = _inputs((2, T), 80, N, kind)
+    kw["D"], kw["z"] = None, kw["z"] if gate else None
+    kw["x"][1, T - 1, 70] = INF
+    for sign in (1.0, -1.0):
+        y, h = gdn.selective_scan(**dict(kw, C=kw["C"] * sign))
+        assert y[1, T - 1, 70] == sign * INF and (h[1, 70] == INF).all()
+        assert not torch.isnan(y).any() and int(torch.isinf(y).sum()) == 1
+    state = torch.zeros(2, 80, N, device="cuda")
+    y = gdn.selective_step(**{k: t if k in ("A", "D") or t is None else t[:, T - 1].contiguous() for k, t in kw.items()}, state=state)
+    assert y[1, 70] == INF and not torch.isnan(y).any() and int(torch.isinf(y).sum()) == 1
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [30, 70, 300])
 @pytest.mark.parametrize("N", [1, 5, 12, 16, 20, 37, 64])
