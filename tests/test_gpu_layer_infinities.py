@@ -1,8 +1,8 @@
 """Infinite inputs and states of the selective scan: where the formula gives an infinity, the operators give it, at any
-number of state entries."""
+number of state entries and however a sequence is split."""
 import pytest
 
-from test_gpu_layer import Rng
+from test_gpu_layer import Rng, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,53 @@ def test_step(N, kind):
         assert not torch.isnan(y).any() and not torch.isnan(s).any()
         y[1, 20], s[1, 20] = ref[1, 20], s0[1, 20]
         assert torch.equal(y, ref) and torch.equal(s, s0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [(1, 300), (1, 1003), (1, 5000), (3, 700), [40, 1003, 0, 5000, 300]])
+@pytest.mark.parametrize("N", [1, 5, 16, 37, 64])
+def test_decays_whose_product_rounds_to_zero(N, lens, kind):
+    """A sequence is split into chunks that each forget all of a finite state (e^-1 to e^-50 a token): an infinite one,
+    carried in or from an input, stays."""
+    import torch
+
+    import gated_delta_rule_scan_amd as gdn
+
+    packed = isinstance(lens, list)
+    kw = _inputs((sum(lens),) if packed else lens, 70, N, kind, rate=5.0)
+    B, longest = (len(lens), 3) if packed else (lens[0], 0)
+    first, last = (sum(lens[:3]), sum(lens[:4])) if packed else (0, lens[1])  # rows of sequence `longest`
+    off = offsets(lens) if packed else None
+    state = torch.rand(B, 70, N, device="cuda")
+    ref, href = gdn.selective_scan(**kw, state_in=state, seq_offsets=off)
+    assert torch.isfinite(ref).all() and torch.isfinite(href).all()
+    rows = lambda y: y if packed else y[longest]
+    for at in (None, 0, (last - first) // 2, last - first - 40):
+        new, s = dict(kw), state.clone()
+        if at is None:
+            s[longest, 65], at = INF, 0
+        else:
+            new["x"] = kw["x"].clone()
+            rows(new["x"])[first + at, 65] = INF
+        y, h = gdn.selective_scan(**new, state_in=s, seq_offsets=off)
+        assert (rows(y)[first + at: last, 65] == INF).all() and (h[longest, 65] == INF).all()
+        rows(y)[first + at: last, 65], h[longest, 65] = rows(ref)[first + at: last, 65], href[longest, 65]
+        assert torch.equal(y, ref) and torch.equal(h, href)
+
+
+@pytest.mark.parametrize("T", [20, 300, 1003, 5000])
+def test_rate_and_state_infinite(T):
+    """A rate of minus infinity forgets at once: exp(-inf) * inf is no number, however the sequence is split."""
+    import torch
+
+    import gated_delta_rule_scan_amd as gdn
+
+    kw = _inputs((1, T), 70, 16)
+    ref, href = gdn.selective_scan(**kw)
+    new = dict(kw, A=kw["A"].clone(), x=kw["x"].clone())
+    new["A"][65, 3], new["x"][0, 2, 65] = -INF, INF
+    y, h = gdn.selective_scan(**new)
+    assert torch.isnan(h[0, 65, 3]) and torch.isnan(y[0, 3:, 65]).all() and y[0, 2, 65] == INF
+    assert (h[0, 65, torch.arange(16) != 3] == INF).all()
+    y[0, :, 65], h[0, 65] = ref[0, :, 65], href[0, 65]
+    assert torch.equal(y, ref) and torch.equal(h, href)
