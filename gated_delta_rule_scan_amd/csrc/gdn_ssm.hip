@@ -602,7 +602,7 @@ hipError_t ssm_launch(const SsmArgs& a, hipStream_t stream) {
   const int64_t chunks = a.off ? (a.T / a.B + a.chunk - 1) / a.chunk : a.chunks;
   const int parts = chunks >= kParts * kCarry / 2 ? kParts : 1;
   const int64_t carries = a.B * ((a.D * a.N * parts + 255) / 256);
-  if (!grid_fits(blocks, threads) || !grid_fits(carries, 256)) return hipErrorNotSupported;
+  if (!grid_fits(blocks, threads) || (a.ends && !grid_fits(carries, 256))) return hipErrorNotSupported;
   constexpr bool kMulti = NN == 32;
   const bool multi = kMulti && NG > 1, padded = a.N % NN != 0;
   const unsigned stage = (unsigned)(NG * CT * kStage * 2 * NN * sizeof(float));
