@@ -496,6 +496,15 @@ PyObject* delta_step(PyObject* const* a) {
   return THPVariable_Wrap(y);
 }
 
+// torch's own exception for it (which its C++ interface does not export)
+void raise_out_of_memory(const char* what) {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+  if (type) PyErr_SetString(type, what);
+  Py_XDECREF(type);
+  Py_XDECREF(torch);
+}
+
 // No exception leaves a call but as a Python one.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -511,6 +520,10 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyObject* status = PyLong_FromLong(e.status);
     PyErr_SetObject(gdn_error, status);
     Py_XDECREF(status);
+  } catch (const c10::OutOfMemoryError& e) {
+    raise_out_of_memory(e.what_without_backtrace());
+  } catch (const c10::Error& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }
