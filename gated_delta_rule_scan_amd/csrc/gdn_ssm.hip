@@ -48,8 +48,8 @@ __device__ __forceinline__ float rate(float A) {
 // spared it.
 //
 // 32768 tokens x 2048 channels x 16 entries, bf16, gated: 411-420 us (under a
-// profiler, which slows them, first pass 200, carry 10, scan 255).  The scan
-// issues 114 vector instructions per token and wave, 80 of them the formula's,
+// profiler, which slows them, first pass 200, carry 11, scan 255-263).  The scan
+// issues 115 vector instructions per token and wave, 80 of them the formula's,
 // 20 of them exponentials and reciprocals; at their measured issue times (3.1
 // and 9 cycles, four waves a SIMD) 200 us.  Its memory traffic alone would take
 // 107 us.
@@ -464,7 +464,7 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a) {
 // Memory-bound on the state, read and written once, and on the latency of
 // what comes before: only the state's address waits for the slot index, and
 // everything else is on its way by then.  128 sequences x 4096 channels x 16
-// entries: 13.9 us for 72 MB (5.1 TB/s); with 1, 2, 4 channels a thread 18,
+// entries: 14.0 us for 72 MB (5.1 TB/s); with 1, 2, 4 channels a thread 18,
 // 14.3, 15.6 us.
 constexpr int kChannels = 2;
 
@@ -560,11 +560,11 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, int lanes_log2
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         h[q][i].e[e] = fmaf(hw_exp2(s * rate(A[q][i].e[e])), h[q][i].e[e], u * to_float(B[q].e[e]));
-        // (lanes behind entry N run entry 0's state, infinite perhaps)
-        y[i] = n < N ? fmaf(h[q][i].e[e], to_float(C[q].e[e]), y[i]) : y[i];
+        y[i] = fmaf(h[q][i].e[e], to_float(C[q].e[e]), y[i]);
       }
       if (live[i] && n < N) *reinterpret_cast<Entries<float, V>*>(S + c[i] * (unsigned)N + n) = h[q][i];
     }
+    if (V > 1 && l * V >= N) y[i] = 0.0f;  // a lane behind entry N ran entry 0's state, infinite perhaps
   }
   for (int m = L >> 1; m >= 1; m >>= 1) {
 #pragma unroll
