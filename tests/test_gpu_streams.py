@@ -98,3 +98,35 @@ def test_results_freed_on_the_current_stream(name):
     for a, b in zip(copies, want):
         assert torch.equal(a, b)
     del junk
+
+
+@pytest.mark.parametrize("name", ["conv step", "step", "delta step"])
+def test_given_outputs_and_states(name):
+    """Steps into outputs and states made before the side stream waits: rows with a slot are written, the others keep
+    what the current stream put there, and states advance as on the current stream."""
+    import torch
+
+    import gated_delta_rule_scan_amd as gdn
+
+    r = Rng(62)
+    B, D, N, H, d = 5, 136, 16, 4, 64
+    index = torch.tensor([3, -1, 0, 5, 1], dtype=torch.int32, device="cuda")
+    w, x, q = r.t(D, 4), r.t(B, D), r.t(B, H, d)
+    kw = _ssm_inputs(r, "f32", (B,), D, N, 1, True, True, True, True)
+    la, beta = -r.t(B, H).abs(), torch.sigmoid(r.t(B, H))
+    pool = {"conv step": r.t(5, 3, D), "step": r.t(5, D, N), "delta step": r.t(5, H, d, d)}[name]
+    call = {"conv step": lambda s, o, **k: gdn.causal_conv_step(x, w, None, s, state_index=index, out=o, **k),
+            "step": lambda s, o, **k: gdn.selective_step(**kw, state=s, state_index=index, out=o, **k),
+            "delta step": lambda s, o, **k: gdn.delta_step(q, q, q, la, beta, s, index, out=o, **k)}[name]
+    like = q if name == "delta step" else x
+    want, wanted = torch.full_like(like, 3.0), pool.clone()
+    call(wanted, want)
+    assert (want[[1, 3]] == 3).all() and not (want[[0, 2, 4]] == 3).any()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda._sleep(LONG)
+        out, state = torch.full_like(like, 3.0), pool.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        assert call(state, out, stream=side).data_ptr() == out.data_ptr()
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(out, want) and torch.equal(state, wanted)
