@@ -11,7 +11,9 @@ The C ABI (``include/gdn.h``) is mirrored name for name:
 convenience wrapper that allocates outputs and workspace with torch.  The
 operators a recurrent layer runs around its scan (``causal_conv``, ``rotary``,
 ``selective_scan``) and the single-token steps (``causal_conv_step``,
-``selective_step``, ``delta_step``) are in ``layer.py``.
+``selective_step``, ``delta_step``) are in ``layer.py``, what a hybrid model runs
+beside them (a paged cache of keys and values, a new token's attention over it,
+the seam between two blocks) in ``hybrid.py``.
 """
 from __future__ import annotations
 
@@ -56,9 +58,15 @@ GDN_SSM_OPT_SOFTPLUS = 1
 GDN_ROTARY_OPT_INTERLEAVED = 1
 GDN_ROTARY_OPT_INVERSE = 2
 
+GDN_KV_F32 = 0
+GDN_KV_BF16 = 1
+GDN_KV_MXFP8 = 2
+GDN_KV_MXFP4 = 3
+
 EXPORTED = ("gdn_workspace_bytes", "gdn_forward", "gdn_forward_noalloc", "gdn_vda_workspace_bytes", "gdn_vda_forward",
             "gdn_conv_forward", "gdn_conv_step", "gdn_ssm_workspace_bytes", "gdn_ssm_forward", "gdn_ssm_step",
-            "gdn_rotary", "gdn_step", "gdn_status_string", "gdn_version")
+            "gdn_rotary", "gdn_step", "gdn_kv_write", "gdn_kv_read", "gdn_attention_workspace_bytes", "gdn_attention_step",
+            "gdn_norm_forward", "gdn_norm_workspace_bytes", "gdn_norm_backward", "gdn_status_string", "gdn_version")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # GDN_NOALLOC_SCRATCH_BYTES
 
 
@@ -146,6 +154,51 @@ class gdn_step_problem_t(ctypes.Structure):
     ]
 
 
+class gdn_kv_problem_t(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hk", ctypes.c_int64), ("d", ctypes.c_int64),
+        ("pages", ctypes.c_int64), ("page", ctypes.c_int64), ("table_width", ctypes.c_int64),
+        ("k_stride_b", ctypes.c_int64), ("k_stride_t", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+        ("v_stride_b", ctypes.c_int64), ("v_stride_t", ctypes.c_int64), ("v_stride_h", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("format", ctypes.c_int32), ("options", ctypes.c_int32),
+        ("seq_offsets", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("start", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class gdn_attention_problem_t(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64), ("d", ctypes.c_int64),
+        ("pages", ctypes.c_int64), ("page", ctypes.c_int64), ("table_width", ctypes.c_int64),
+        ("q_stride_b", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+        ("out_stride_b", ctypes.c_int64), ("out_stride_h", ctypes.c_int64),
+        ("window", ctypes.c_int64), ("sinks", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("format", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("page_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class gdn_norm_problem_t(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64),
+        ("x_stride_b", ctypes.c_int64), ("x_stride_t", ctypes.c_int64),
+        ("y_stride_b", ctypes.c_int64), ("y_stride_t", ctypes.c_int64),
+        ("h_stride_b", ctypes.c_int64), ("h_stride_t", ctypes.c_int64),
+        ("n_stride_b", ctypes.c_int64), ("n_stride_t", ctypes.c_int64),
+        ("dx_stride_b", ctypes.c_int64), ("dx_stride_t", ctypes.c_int64),
+        ("dy_stride_b", ctypes.c_int64), ("dy_stride_t", ctypes.c_int64),
+        ("gate_stride_b", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("options", ctypes.c_int32),
+        ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float),
+        ("seq_offsets", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int):
         self.status = status
@@ -179,12 +232,20 @@ def lib() -> ctypes.CDLL:
                                        ("gdn_conv_step", gdn_conv_problem_t, 5),
                                        ("gdn_ssm_forward", gdn_ssm_problem_t, 8),
                                        ("gdn_ssm_step", gdn_ssm_problem_t, 7),
-                                       ("gdn_rotary", gdn_rotary_problem_t, 6), ("gdn_step", gdn_step_problem_t, 7)):
+                                       ("gdn_rotary", gdn_rotary_problem_t, 6), ("gdn_step", gdn_step_problem_t, 7),
+                                       ("gdn_kv_write", gdn_kv_problem_t, 6), ("gdn_kv_read", gdn_kv_problem_t, 6),
+                                       ("gdn_attention_step", gdn_attention_problem_t, 7),
+                                       ("gdn_norm_forward", gdn_norm_problem_t, 4),
+                                       ("gdn_norm_backward", gdn_norm_problem_t, 9)):
             fn = getattr(L, name)
             fn.argtypes = [ctypes.POINTER(struct)] + [vp] * pointers
             fn.restype = ctypes.c_int
-        L.gdn_ssm_workspace_bytes.argtypes = [ctypes.POINTER(gdn_ssm_problem_t)]
-        L.gdn_ssm_workspace_bytes.restype = ctypes.c_size_t
+        for name, struct in (("gdn_ssm_workspace_bytes", gdn_ssm_problem_t),
+                             ("gdn_attention_workspace_bytes", gdn_attention_problem_t),
+                             ("gdn_norm_workspace_bytes", gdn_norm_problem_t)):
+            fn = getattr(L, name)
+            fn.argtypes = [ctypes.POINTER(struct)]
+            fn.restype = ctypes.c_size_t
         L.gdn_status_string.argtypes = [ctypes.c_int32]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_version.argtypes = []
@@ -255,6 +316,39 @@ def gdn_rotary(problem: gdn_rotary_problem_t, q, k, inv_freq, positions, q_out, 
 def gdn_step(problem: gdn_step_problem_t, q, k, v, log_alpha, beta, state, out) -> int:
     """Raw call with integer device pointers (None for NULL); returns the status."""
     return lib().gdn_step(ctypes.byref(problem), q, k, v, log_alpha, beta, state, out)
+
+
+def gdn_kv_write(problem: gdn_kv_problem_t, k, v, k_cache, v_cache, k_scales, v_scales) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_kv_write(ctypes.byref(problem), k, v, k_cache, v_cache, k_scales, v_scales)
+
+
+def gdn_kv_read(problem: gdn_kv_problem_t, k_cache, v_cache, k_scales, v_scales, k, v) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_kv_read(ctypes.byref(problem), k_cache, v_cache, k_scales, v_scales, k, v)
+
+
+def gdn_attention_workspace_bytes(problem: gdn_attention_problem_t) -> int:
+    return lib().gdn_attention_workspace_bytes(ctypes.byref(problem))
+
+
+def gdn_attention_step(problem: gdn_attention_problem_t, q, k_cache, v_cache, k_scales, v_scales, out, lse) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_attention_step(ctypes.byref(problem), q, k_cache, v_cache, k_scales, v_scales, out, lse)
+
+
+def gdn_norm_forward(problem: gdn_norm_problem_t, x, y, h, n) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_norm_forward(ctypes.byref(problem), x, y, h, n)
+
+
+def gdn_norm_workspace_bytes(problem: gdn_norm_problem_t) -> int:
+    return lib().gdn_norm_workspace_bytes(ctypes.byref(problem))
+
+
+def gdn_norm_backward(problem: gdn_norm_problem_t, x, y, dh, dn, dx, dy, dgate, dpost_weight, dweight) -> int:
+    """Raw call with integer device pointers (None for NULL); returns the status."""
+    return lib().gdn_norm_backward(ctypes.byref(problem), x, y, dh, dn, dx, dy, dgate, dpost_weight, dweight)
 
 
 def gdn_status_string(status: int) -> str:
@@ -476,12 +570,21 @@ LAYER = ("causal_conv", "causal_conv_step", "selective_scan", "selective_step", 
          "delta_step")
 
 
+HYBRID = ("KVCache", "kv_cache", "kv_write", "kv_read", "attention_step", "residual_norm", "residual_norm_backward")
+
+
 def __getattr__(name: str):
     if name in LAYER:
         from . import layer
 
         for n in LAYER:
             globals()[n] = getattr(layer, n)
+        return globals()[name]
+    if name in HYBRID:
+        from . import hybrid
+
+        for n in HYBRID:
+            globals()[n] = getattr(hybrid, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
@@ -496,7 +599,8 @@ _ops_registered = False
 def register_torch_ops() -> None:
     """Register torch.ops.gdn.forward, torch.ops.gdn.vda_forward and the layer
     operators (causal_conv, causal_conv_step, selective_scan, selective_step,
-    rotary, delta_step) for CUDA tensors (outputs allocated by the op) with
+    rotary, delta_step, kv_write, kv_read, attention_step, residual_norm,
+    residual_norm_backward) for CUDA tensors (outputs allocated by the op) with
     fake implementations for tracing.  Idempotent."""
     global _ops_registered
     if _ops_registered:
@@ -538,7 +642,8 @@ def register_torch_ops() -> None:
         return (q.new_empty((B, T, H, dv), dtype=torch.float32),
                 q.new_empty((dirs, B, H, dv, dk), dtype=torch.float32))
 
-    from . import layer
+    from . import hybrid, layer
 
     layer.register_ops()
+    hybrid.register_ops()
     _ops_registered = True

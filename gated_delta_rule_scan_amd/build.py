@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["gdn_api.hip", "gdn_prep.hip", "gdn_prep_wide.hip", "gdn_chain.hip", "gdn_colchain.hip", "gdn_epilogue.hip", "gdn_vda.hip",
-           "gdn_layer.hip", "gdn_conv.hip", "gdn_ssm.hip", "gdn_rotary.hip", "gdn_step.hip"]
+           "gdn_layer.hip", "gdn_conv.hip", "gdn_ssm.hip", "gdn_rotary.hip", "gdn_step.hip", "gdn_hybrid.hip", "gdn_kv.hip",
+           "gdn_attend.hip", "gdn_norm.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 VALU ops.

@@ -11,7 +11,9 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "gdn.h"
 
@@ -28,6 +30,13 @@ decltype(&gdn_ssm_forward) f_ssm_forward;
 decltype(&gdn_ssm_step) f_ssm_step;
 decltype(&gdn_rotary) f_rotary;
 decltype(&gdn_step) f_step;
+decltype(&gdn_kv_write) f_kv_write;
+decltype(&gdn_kv_read) f_kv_read;
+decltype(&gdn_attention_workspace_bytes) f_attention_workspace;
+decltype(&gdn_attention_step) f_attention_step;
+decltype(&gdn_norm_forward) f_norm_forward;
+decltype(&gdn_norm_workspace_bytes) f_norm_workspace;
+decltype(&gdn_norm_backward) f_norm_backward;
 PyObject* gdn_error;  // the package's exception, made from a status
 
 struct Refused {  // becomes a Python exception
@@ -45,7 +54,7 @@ std::string text(IntArrayRef s) {
   return t + "]";
 }
 const char* text(ScalarType t) {
-  return t == at::kFloat ? "float32" : t == at::kBFloat16 ? "bfloat16" : t == at::kInt ? "int32" : t == at::kDouble ? "float64" : t == at::kByte ? "uint8" : "?";
+  return t == at::kFloat ? "float32" : t == at::kBFloat16 ? "bfloat16" : t == at::kInt ? "int32" : t == at::kDouble ? "float64" : t == at::kByte ? "uint8" : t == at::kFloat8_e4m3fn ? "float8_e4m3fn" : "?";
 }
 
 // an argument: a tensor, or null for None
@@ -496,6 +505,308 @@ PyObject* delta_step(PyObject* const* a) {
   return THPVariable_Wrap(y);
 }
 
+// ---- the paged cache ----
+
+PyObject* none_or(const Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); }
+
+// A cache: (k, v), or (k, v, k_scales, v_scales) with 8 or 4 bits a channel.
+// The scales say that it is quantised, the pools' type how.
+struct Cache {
+  const Tensor *k = nullptr, *v = nullptr, *ks = nullptr, *vs = nullptr;
+  int64_t pages, heads, page, d;
+  int32_t format;
+
+  explicit Cache(PyObject* o) {
+    PyObject* item[4] = {Py_None, Py_None, Py_None, Py_None};
+    // (borrowed: the caller's sequence keeps them, so a tuple or a list only)
+    const bool tuple = PyTuple_Check(o);
+    const Py_ssize_t n = tuple ? PyTuple_GET_SIZE(o) : PyList_Check(o) ? PyList_GET_SIZE(o) : 0;
+    if (n != 2 && n != 4) throw Refused{PyExc_TypeError, "cache must be (k, v) or (k, v, k_scales, v_scales)"};
+    for (Py_ssize_t i = 0; i < n; ++i) item[i] = tuple ? PyTuple_GET_ITEM(o, i) : PyList_GET_ITEM(o, i);
+    k = &given(item[0], "cache k");
+    v = &given(item[1], "cache v");
+    ks = tensor(item[2], "cache k_scales");
+    vs = tensor(item[3], "cache v_scales");
+    if (!k->is_cuda()) refuse("cache k must be a CUDA tensor");
+    if (k->dim() != 4) refuse("cache k must be [pages, heads, page, d]");
+    if (!ks != !vs) refuse("a cache has both scales or none");
+    const ScalarType t = k->scalar_type();
+    if (!ks && (t == at::kFloat || t == at::kBFloat16)) format = t == at::kFloat ? GDN_KV_F32 : GDN_KV_BF16;
+    else if (ks && t == at::kFloat8_e4m3fn) format = GDN_KV_MXFP8;
+    else if (ks && t == at::kByte) format = GDN_KV_MXFP4;
+    else throw Refused{PyExc_TypeError, "cache k must be float32 or bfloat16, or with scales float8_e4m3fn or uint8 (two channels a byte)"};
+    pages = k->size(0), heads = k->size(1), page = k->size(2);
+    d = format == GDN_KV_MXFP4 ? 2 * k->size(3) : k->size(3);
+    want(*k, k->sizes(), t, *k, "cache k");
+    want(*v, k->sizes(), t, *k, "cache v");
+    if (ks) {
+      want(*ks, {pages, heads, page, d / 32}, at::kByte, *k, "cache k_scales");
+      want(*vs, {pages, heads, page, d / 32}, at::kByte, *k, "cache v_scales");
+    }
+  }
+  // the type of the rows beside it
+  void rows_type(ScalarType t, const char* name) const {
+    if (!ks && t != k->scalar_type()) refuse(std::string(name) + " must be " + text(k->scalar_type()) + ", the type of the cache");
+  }
+};
+
+// page_table [B, W] beside a cache; its W
+int64_t table_width(const Tensor& table, int64_t B, const Tensor& like) {
+  if (table.dim() != 2) refuse("page_table must be [B, pages of a sequence]");
+  want(table, {B, table.size(1)}, at::kInt, like, "page_table");
+  return table.size(1);
+}
+
+template <typename P>
+void cache_fields(P& p, const Cache& c, const Tensor& table, int64_t B) {
+  p.Hk = c.heads;
+  p.d = c.d;
+  p.pages = c.pages;
+  p.page = c.page;
+  p.format = c.format;
+  p.table_width = table_width(table, B, *c.k);
+  p.page_table = static_cast<const int32_t*>(table.data_ptr());
+}
+
+// the rows' strides: sequences and tokens as they are shaped
+void kv_strides(gdn_kv_problem_t& p, const Tensor& k, const Tensor& v, bool packed) {
+  const bool one = !packed && k.dim() == 3;  // a token each
+  auto of = [&](const Tensor& t, int64_t* b, int64_t* s, int64_t* h) {
+    *b = packed ? 0 : t.stride(0);
+    *s = one ? 0 : t.stride(-3);
+    *h = t.stride(-2);
+  };
+  of(k, &p.k_stride_b, &p.k_stride_t, &p.k_stride_h);
+  of(v, &p.v_stride_b, &p.v_stride_t, &p.v_stride_h);
+}
+
+const Tensor* offsets_of(PyObject* o, const Tensor& like) {
+  const Tensor* off = tensor(o, "seq_offsets");
+  if (off && (off->scalar_type() != at::kInt || off->dim() != 1 || off->size(0) < 2 || !off->is_contiguous() ||
+              off->device() != like.device()))
+    refuse("seq_offsets must be contiguous int32 [B + 1] on " + like.device().str());
+  return off;
+}
+
+// k, v, cache, page_table, start, seq_offsets, stream
+PyObject* kv_write(PyObject* const* a) {
+  const Tensor &k = given(a[0], "k"), &v = given(a[1], "v"), &table = given(a[3], "page_table");
+  const Tensor* start = tensor(a[4], "start");
+  gdn_kv_problem_t p = {};
+  p.dtype = kind_of(k, "k");
+  const Tensor* off = offsets_of(a[5], k);
+  const Cache c(a[2]);
+  if (k.dim() != 3 && (off || k.dim() != 4)) refuse("k must be [B, T, H, d], [B, H, d] or, with seq_offsets, [T, H, d]");
+  p.B = off ? off->size(0) - 1 : k.size(0);
+  p.T = off ? k.size(0) : k.dim() == 4 ? k.size(1) : 1;
+  if (k.size(-2) != c.heads || k.size(-1) != c.d || k.device() != c.k->device())
+    refuse("k must have " + std::to_string(c.heads) + " heads of " + std::to_string(c.d) + " on " + c.k->device().str() + ", as the cache");
+  c.rows_type(k.scalar_type(), "k");
+  rows(k, k.sizes(), k, "k");
+  rows(v, k.sizes(), k, "v");
+  if (start) want(*start, {p.B}, at::kInt, k, "start");
+  cache_fields(p, c, table, p.B);
+  kv_strides(p, k, v, off);
+  const Stream s(a[6], k);
+  p.seq_offsets = static_cast<const int32_t*>(ptr(off));
+  p.start = static_cast<const int32_t*>(ptr(start));
+  p.stream = s.raw;
+  const c10::DeviceGuard guard(k.device());
+  check(f_kv_write(&p, k.data_ptr(), v.data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ptr(c.ks), ptr(c.vs)));
+  Py_RETURN_NONE;
+}
+
+// cache, page_table, tokens, start, seq_offsets, dtype code (-1: the cache's, or bfloat16), k_out, v_out, stream
+PyObject* kv_read(PyObject* const* a) {
+  const Cache c(a[0]);
+  const Tensor &table = given(a[1], "page_table"), &like = *c.k;
+  const Tensor *start = tensor(a[3], "start"), *ko = tensor(a[6], "k_out"), *vo = tensor(a[7], "v_out");
+  const Tensor* off = offsets_of(a[4], like);
+  gdn_kv_problem_t p = {};
+  p.T = whole(a[2], "tokens");
+  if (p.T < 0) refuse("tokens must not be negative");
+  const int64_t kind = whole(a[5], "dtype");
+  ScalarType type = kind == GDN_DTYPE_F32 ? at::kFloat : at::kBFloat16;
+  if (kind < 0) type = ko ? ko->scalar_type() : vo ? vo->scalar_type() : c.ks ? at::kBFloat16 : like.scalar_type();
+  c.rows_type(type, "dtype");
+  if (table.dim() != 2) refuse("page_table must be [B, pages of a sequence]");
+  p.B = off ? off->size(0) - 1 : table.size(0);
+  const int64_t dense[4] = {p.B, p.T, c.heads, c.d};
+  const IntArrayRef shape = off ? IntArrayRef(dense + 1, 3) : IntArrayRef(dense, 4);
+  for (const Tensor* o : {ko, vo}) {
+    if (!o) continue;
+    if (o->scalar_type() != type || o->sizes() != shape || o->device() != like.device())
+      refuse("k_out, v_out must be " + std::string(text(type)) + " " + text(shape) + " on " + like.device().str());
+    rows(*o, shape, *o, "k_out, v_out");
+  }
+  if (!ko != !vo) refuse("k_out and v_out go together");
+  if (start) want(*start, {p.B}, at::kInt, like, "start");
+  cache_fields(p, c, table, p.B);
+  const Stream s(a[8], like);
+  const Tensor k = ko ? *ko : s.fresh(shape, type), v = vo ? *vo : s.fresh(shape, type);
+  p.dtype = type == at::kFloat ? GDN_DTYPE_F32 : GDN_DTYPE_BF16;
+  kv_strides(p, k, v, off);
+  p.options = unused_rows(ko);
+  p.seq_offsets = static_cast<const int32_t*>(ptr(off));
+  p.start = static_cast<const int32_t*>(ptr(start));
+  p.stream = s.raw;
+  const c10::DeviceGuard guard(like.device());
+  check(f_kv_read(&p, c.k->data_ptr(), c.v->data_ptr(), ptr(c.ks), ptr(c.vs), k.data_ptr(), v.data_ptr()));
+  return pair(k, v);
+}
+
+// a call's workspace of `size` bytes: the caller's, or one that is freed when
+// the call returns (later work of its stream may have it)
+void* workspace(PyObject* o, const Stream& s, int64_t size, const Tensor& like, Tensor* mine, size_t* bytes) {
+  const Tensor* ws = tensor(o, "workspace");
+  if (ws && (ws->scalar_type() != at::kByte || ws->device() != like.device() || !ws->is_contiguous()))
+    refuse("workspace must be a contiguous uint8 tensor on " + like.device().str());
+  if (!size) return nullptr;
+  if (!ws || ws->numel() < size) {
+    *mine = s.fresh({size}, at::kByte, false);
+    ws = mine;
+  }
+  *bytes = (size_t)ws->numel();
+  return ws->data_ptr();
+}
+
+// q, cache, page_table, lengths, scale (None: d^-1/2), window, sinks, out, lse, workspace, stream
+PyObject* attention_step(PyObject* const* a) {
+  const Tensor &q = given(a[0], "q"), &table = given(a[2], "page_table"), &lengths = given(a[3], "lengths");
+  const Tensor *out = tensor(a[7], "out"), *lse = tensor(a[8], "lse");
+  gdn_attention_problem_t p = {};
+  p.dtype = kind_of(q, "q");
+  const Cache c(a[1]);
+  if (q.dim() != 3 || q.size(2) != c.d || q.device() != c.k->device())
+    refuse("q must be [B, heads, " + std::to_string(c.d) + "] on " + c.k->device().str() + ", as the cache");
+  c.rows_type(q.scalar_type(), "q");
+  rows(q, q.sizes(), q, "q");
+  p.B = q.size(0);
+  p.Hq = q.size(1);
+  if (c.heads < 1 || p.Hq % c.heads) refuse(std::to_string(c.heads) + " heads of the cache do not divide " + std::to_string(p.Hq) + " of q");
+  want(lengths, {p.B}, at::kInt, q, "lengths");
+  if (lse) want(*lse, {p.B, p.Hq}, at::kFloat, q, "lse");
+  cache_fields(p, c, table, p.B);
+  p.scale = a[4] == Py_None ? (float)(1.0 / std::sqrt((double)c.d)) : real(a[4], "scale");
+  p.window = whole(a[5], "window");
+  p.sinks = whole(a[6], "sinks");
+  if (p.window < 0 || p.sinks < 0) refuse("window and sinks must not be negative");
+  const Stream s(a[10], q);
+  const Tensor y = output(s, out, q);
+  p.q_stride_b = q.stride(0), p.q_stride_h = q.stride(1);
+  p.out_stride_b = y.stride(0), p.out_stride_h = y.stride(1);
+  p.lengths = static_cast<const int32_t*>(lengths.data_ptr());
+  Tensor mine;
+  p.workspace = workspace(a[9], s, (int64_t)f_attention_workspace(&p), q, &mine, &p.workspace_bytes);
+  p.stream = s.raw;
+  const c10::DeviceGuard guard(q.device());
+  check(f_attention_step(&p, q.data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ptr(c.ks), ptr(c.vs), y.data_ptr(),
+                         static_cast<float*>(ptr(lse))));
+  return THPVariable_Wrap(y);
+}
+
+// ---- the seam between two blocks ----
+
+// The rows [B, T, D], [B, D] (one each) or packed [T, D], parameters and
+// numbers that both directions share.
+struct Seam {
+  gdn_norm_problem_t p = {};
+  const Tensor& x;
+  const Tensor *y, *gate, *post, *weight, *off;
+  int b, t;  // dimensions of sequences and tokens; -1: none
+  // x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets
+  explicit Seam(PyObject* const* a)
+      : x(given(a[0], "x")), y(tensor(a[1], "y")), gate(tensor(a[2], "gate")), post(tensor(a[3], "post_weight")),
+        weight(tensor(a[4], "weight")) {
+    p.dtype = kind_of(x, "x");
+    off = offsets_of(a[7], x);
+    if (x.dim() != 2 && (off || x.dim() != 3)) refuse("x must be [B, T, D], [B, D] or, with seq_offsets, [T, D]");
+    b = off ? -1 : 0;
+    t = off ? 0 : x.dim() == 3 ? 1 : -1;
+    p.B = off ? off->size(0) - 1 : x.size(0);
+    p.T = t < 0 ? 1 : x.size(t);
+    p.D = x.size(-1);
+    rows(x, x.sizes(), x, "x");
+    if (y) rows(*y, x.sizes(), x, "y");
+    if ((gate || post) && !y) refuse("gate and post_weight go with y");
+    if (gate) {
+      if (gate->dim() == 2) p.gate_stride_b = p.D;
+      p.gate = gate->dim() == 2 ? param(gate, {p.B, p.D}, at::kFloat, x, "gate") : param(gate, {p.D}, at::kFloat, x, "gate");
+    }
+    p.post_weight = param(post, {p.D}, at::kFloat, x, "post_weight");
+    p.weight = param(weight, {p.D}, at::kFloat, x, "weight");
+    p.residual_scale = real(a[5], "residual_scale");
+    p.eps = real(a[6], "eps");
+    p.seq_offsets = static_cast<const int32_t*>(ptr(off));
+    stride(x, &p.x_stride_b, &p.x_stride_t);
+    if (y) stride(*y, &p.y_stride_b, &p.y_stride_t);
+  }
+  void stride(const Tensor& r, int64_t* sb, int64_t* st) const {
+    *sb = b < 0 ? 0 : r.stride(b);
+    *st = t < 0 ? 0 : r.stride(t);
+  }
+};
+
+// x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets, out, norm_out, stream
+PyObject* residual_norm(PyObject* const* a) {
+  Seam q(a);
+  gdn_norm_problem_t& p = q.p;
+  const Tensor *out = tensor(a[8], "out"), *nout = tensor(a[9], "norm_out");
+  if (nout && !q.weight) refuse("norm_out without weight");
+  // without a block's output and a scale the residual stream stays what it is
+  const bool moves = q.y || out || p.residual_scale != 1.0f;
+  if (!moves && !q.weight) refuse("nothing to compute: y or weight must be given");
+  const Stream s(a[10], q.x);
+  Tensor h, n;
+  if (moves) {
+    h = output(s, out, q.x);
+    q.stride(h, &p.h_stride_b, &p.h_stride_t);
+  }
+  if (q.weight) {
+    n = output(s, nout, q.x, "norm_out");
+    q.stride(n, &p.n_stride_b, &p.n_stride_t);
+  }
+  if (moves && q.weight && !out != !nout && q.off) refuse("out and norm_out go together in a packed batch");
+  p.options = unused_rows(out ? out : nout);
+  p.stream = s.raw;
+  const c10::DeviceGuard guard(q.x.device());
+  check(f_norm_forward(&p, q.x.data_ptr(), ptr(q.y), h.defined() ? h.data_ptr() : nullptr, n.defined() ? n.data_ptr() : nullptr));
+  return pair(h.defined() ? h : q.x, n);
+}
+
+// dh, dn, then x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets, then dx, dy, workspace, stream
+PyObject* residual_norm_backward(PyObject* const* a) {
+  Seam q(a + 2);
+  gdn_norm_problem_t& p = q.p;
+  const Tensor *dh = tensor(a[0], "dh"), *dn = tensor(a[1], "dn"), *dx = tensor(a[10], "dx"), *dy = tensor(a[11], "dy");
+  if (!dn != !q.weight) refuse("dn and weight go together");
+  if (!dh && !dn) refuse("dh or dn must be given");
+  if (dh) rows(*dh, q.x.sizes(), q.x, "dh"), q.stride(*dh, &p.h_stride_b, &p.h_stride_t);
+  if (dn) rows(*dn, q.x.sizes(), q.x, "dn"), q.stride(*dn, &p.n_stride_b, &p.n_stride_t);
+  if (dy && !q.y) refuse("dy without y");
+  if (q.y && !dx != !dy && q.off) refuse("dx and dy go together in a packed batch");
+  const Stream s(a[13], q.x);
+  const Tensor gx = output(s, dx, q.x, "dx");
+  q.stride(gx, &p.dx_stride_b, &p.dx_stride_t);
+  Tensor gy, gg, gp, gw;
+  if (q.y) {
+    gy = output(s, dy, q.x, "dy");
+    q.stride(gy, &p.dy_stride_b, &p.dy_stride_t);
+  }
+  if (q.gate) gg = s.fresh(q.gate->sizes(), at::kFloat);
+  if (q.post) gp = s.fresh({p.D}, at::kFloat);
+  if (q.weight) gw = s.fresh({p.D}, at::kFloat);
+  p.options = unused_rows(dx);
+  Tensor mine;
+  p.workspace = workspace(a[12], s, (int64_t)f_norm_workspace(&p), q.x, &mine, &p.workspace_bytes);
+  p.stream = s.raw;
+  const c10::DeviceGuard guard(q.x.device());
+  auto at = [](const Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; };
+  check(f_norm_backward(&p, q.x.data_ptr(), ptr(q.y), ptr(dh), ptr(dn), gx.data_ptr(), gy.defined() ? gy.data_ptr() : nullptr,
+                        at(gg), at(gp), at(gw)));
+  return Py_BuildValue("(NNNNN)", THPVariable_Wrap(gx), none_or(gy), none_or(gg), none_or(gp), none_or(gw));
+}
+
 // torch's own exception for it (which its C++ interface does not export)
 void raise_out_of_memory(const char* what) {
   PyObject* torch = PyImport_ImportModule("torch");
@@ -532,20 +843,19 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // the exception class, then the entry points' addresses in this order
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 8) {
-    PyErr_SetString(PyExc_TypeError, "8 arguments expected");
+  constexpr int kEntries = 14;
+  if (n != 1 + kEntries) {
+    PyErr_Format(PyExc_TypeError, "%d arguments expected", 1 + kEntries);
     return nullptr;
   }
-  void* f[7];
-  for (int i = 0; i < 7; ++i) f[i] = PyLong_AsVoidPtr(a[i + 1]);
+  void* f[kEntries];
+  for (int i = 0; i < kEntries; ++i) f[i] = PyLong_AsVoidPtr(a[i + 1]);
   if (PyErr_Occurred()) return nullptr;
-  f_conv_forward = reinterpret_cast<decltype(f_conv_forward)>(f[0]);
-  f_conv_step = reinterpret_cast<decltype(f_conv_step)>(f[1]);
-  f_ssm_workspace = reinterpret_cast<decltype(f_ssm_workspace)>(f[2]);
-  f_ssm_forward = reinterpret_cast<decltype(f_ssm_forward)>(f[3]);
-  f_ssm_step = reinterpret_cast<decltype(f_ssm_step)>(f[4]);
-  f_rotary = reinterpret_cast<decltype(f_rotary)>(f[5]);
-  f_step = reinterpret_cast<decltype(f_step)>(f[6]);
+  int i = 0;
+  auto bind = [&](auto& to) { to = reinterpret_cast<std::remove_reference_t<decltype(to)>>(f[i++]); };
+  bind(f_conv_forward), bind(f_conv_step), bind(f_ssm_workspace), bind(f_ssm_forward), bind(f_ssm_step), bind(f_rotary), bind(f_step);
+  bind(f_kv_write), bind(f_kv_read), bind(f_attention_workspace), bind(f_attention_step), bind(f_norm_forward);
+  bind(f_norm_workspace), bind(f_norm_backward);
   Py_INCREF(a[0]);
   Py_XSETREF(gdn_error, a[0]);
   Py_RETURN_NONE;
@@ -560,6 +870,11 @@ PyMethodDef methods[] = {
     GDN_CALL("selective_step", ssm_step, 13),
     GDN_CALL("rotary", rotary, 11),
     GDN_CALL("delta_step", delta_step, 13),
+    GDN_CALL("kv_write", kv_write, 7),
+    GDN_CALL("kv_read", kv_read, 9),
+    GDN_CALL("attention_step", attention_step, 11),
+    GDN_CALL("residual_norm", residual_norm, 11),
+    GDN_CALL("residual_norm_backward", residual_norm_backward, 14),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -98,7 +98,88 @@ struct StepArgs {
   int erase, exclusive, zero_unused;
 };
 
+// rows into the cache (k, v read) or out of it (k, v written)
+struct KvArgs {
+  void* k;
+  void* v;
+  void* k_cache;
+  void* v_cache;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  const int32_t* off;
+  const int32_t* table;
+  const int32_t* start;
+  int64_t B, T, width, pages;
+  int64_t k_sb, k_st, k_sh, v_sb, v_st, v_sh;
+  int Hk, d;
+  int page_bits;         // log2 of the tokens of a page
+  int zero_unused;
+  int64_t chunk;         // tokens per workgroup
+  int64_t chunks;        // workgroups per sequence (not packed)
+};
+
+struct AttendArgs {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  void* out;
+  float* lse;
+  const int32_t* table;
+  const int32_t* lengths;
+  int64_t B, width, pages;
+  int64_t q_sb, q_sh, o_sb, o_sh;
+  int64_t window, sinks;
+  int Hq, Hk, d, page_bits;
+  float scale;
+};
+
+struct NormArgs {
+  const void* x;
+  const void* y;
+  void* h;               // backward: dh, read
+  void* n;               // backward: dn, read
+  void* dx;
+  void* dy;
+  const float* gate;
+  const float* post;
+  const float* weight;
+  const int32_t* off;
+  int64_t B, T, D;
+  int64_t x_sb, x_st, y_sb, y_st, h_sb, h_st, n_sb, n_st, dx_sb, dx_st, dy_sb, dy_st;
+  int64_t gate_sb;
+  float alpha, eps;
+  int zero_unused;
+  int64_t chunk;         // rows per workgroup
+  int64_t chunks;        // workgroups per sequence (not packed)
+  int64_t items;         // workgroups
+  int rows;              // rows of a workgroup at a time
+  // backward: the sums over a workgroup's rows [item][rows][sums][D], and where
+  // the gradients' sums go (null: not wanted)
+  float* parts;
+  int sums;
+  float* dgate;
+  float* dpost;
+  float* dweight;
+};
+
+// How the rows of a seam are divided among workgroups.
+struct NormPlan {
+  int64_t chunk, chunks, items;
+  int rows;  // rows of a workgroup at a time: partial sums it writes
+};
+NormPlan norm_plan(int64_t B, int64_t T, int64_t D, bool packed, bool backward);
+
 // ---- launchers (host) ----
+template <typename MT>
+hipError_t launch_kv(const KvArgs& a, int format, bool write, bool aligned, hipStream_t stream);
+template <typename MT>
+hipError_t launch_attend(const AttendArgs& a, int format, hipStream_t stream);
+template <typename MT>
+hipError_t launch_norm(const NormArgs& a, bool aligned, hipStream_t stream);
+template <typename MT>
+hipError_t launch_norm_back(const NormArgs& a, bool aligned, hipStream_t stream);
 template <typename MT>
 hipError_t launch_conv(const ConvArgs& a, int width, bool aligned, hipStream_t stream);
 template <typename MT>

@@ -44,7 +44,8 @@ def _native():
         address = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
         _binding.init(_g.GdnError, *(address(n) for n in (
             "gdn_conv_forward", "gdn_conv_step", "gdn_ssm_workspace_bytes", "gdn_ssm_forward", "gdn_ssm_step",
-            "gdn_rotary", "gdn_step")))
+            "gdn_rotary", "gdn_step", "gdn_kv_write", "gdn_kv_read", "gdn_attention_workspace_bytes", "gdn_attention_step",
+            "gdn_norm_forward", "gdn_norm_workspace_bytes", "gdn_norm_backward")))
         _native.binding, _bound = _binding, lib
     return _native.binding
 

@@ -495,6 +495,144 @@ typedef struct {
 gdn_status_t gdn_step(const gdn_step_problem_t* p, const void* q, const void* k, const void* v,
                       const float* log_alpha, const float* beta, float* state, float* out);
 
+/* ---- A paged cache of keys and values, and a new token's attention over it ----
+ *
+ * The softmax block of a hybrid model keeps the keys and values of past tokens
+ * in pools of pages: k_cache, v_cache [pages, Hk, page, d], contiguous, 16-byte
+ * aligned.  The token at position p of sequence b lies in page
+ * page_table[b, p / page] (page_table [B, table_width] int32 in device memory),
+ * row p % page.  A position outside 0 .. table_width * page - 1, or whose page
+ * number is outside 0 .. pages - 1, has no place: it is not written, not read
+ * and not attended to.  No two tokens of one gdn_kv_write may have one place.
+ *
+ * Formats of a pool:
+ *   GDN_KV_F32, GDN_KV_BF16  the rows' own type (`dtype`)
+ *   GDN_KV_MXFP8             e4m3 codes, a byte a channel
+ *   GDN_KV_MXFP4             e2m1 codes, [pages, Hk, page, d / 2] bytes, the even
+ *                            channel in the low half
+ * The last two hold one scale byte per 32 channels beside the codes, k_scales,
+ * v_scales [pages, Hk, page, d / 32] (4-byte aligned): a byte s scales by 2^(s - 127).
+ * Writing chooses the least power of two, 2^-110 or more, with which the
+ * block's largest magnitude is at most 448 (6 for e2m1), and rounds x / 2^(s -
+ * 127) to the nearest code, ties to even: the only rounding.  A block that
+ * holds an infinity or a NaN gets byte 255 and reads back as NaN; magnitudes
+ * that round to 2^128 read back as infinities.  A pool of zero bytes holds zeros.
+ *
+ * Supported: d 64, 128 or 256; page a power of two, 16 to 1024; Hk <= 65536;
+ * B * T < 2^31. */
+typedef enum { GDN_KV_F32 = 0, GDN_KV_BF16 = 1, GDN_KV_MXFP8 = 2, GDN_KV_MXFP4 = 3 } gdn_kv_format_t;
+
+/* Rows of K and V into the cache, and back out of it.
+ *   k, v   head h of token (b, t) at b * stride_b + t * stride_t + h * stride_h,
+ *          d contiguous channels (dtype); packed with seq_offsets
+ *   start  [B] int32, position of each sequence's first row; NULL: 0
+ * Token t of sequence b has position start[b] + t.  gdn_kv_read leaves the rows
+ * of tokens without a place, and rows of no sequence, as they were; with
+ * GDN_LAYER_OPT_ZERO_UNUSED they become zero. */
+typedef struct {
+  int64_t B, T, Hk, d;
+  int64_t pages, page, table_width;
+  int64_t k_stride_b, k_stride_t, k_stride_h;
+  int64_t v_stride_b, v_stride_t, v_stride_h;
+  int32_t dtype;             /* gdn_dtype_t: type of the rows */
+  int32_t format;            /* gdn_kv_format_t */
+  int32_t options;           /* gdn_kv_read: 0 or GDN_LAYER_OPT_ZERO_UNUSED; else 0 */
+  const int32_t* seq_offsets;
+  const int32_t* page_table;
+  const int32_t* start;
+  void* stream;
+} gdn_kv_problem_t;
+
+gdn_status_t gdn_kv_write(const gdn_kv_problem_t* p, const void* k, const void* v, void* k_cache, void* v_cache,
+                          void* k_scales, void* v_scales);
+gdn_status_t gdn_kv_read(const gdn_kv_problem_t* p, const void* k_cache, const void* v_cache, const void* k_scales,
+                         const void* v_scales, void* k, void* v);
+
+/* Attention of one new token per sequence over the cache: query head h reads
+ * head h / (Hq / Hk) of the cache, and with the visible positions p (p <
+ * lengths[b], and with window > 0 only p >= lengths[b] - window or p < sinks)
+ *   s_p = scale q . k_p,  out = sum_p exp(s_p) v_p / sum_p exp(s_p),
+ *   lse = log(sum_p exp(s_p))
+ * No visible position: out is zero, lse minus infinity.  What lies in places
+ * that are not visible, NaN included, has no influence.  lengths beyond the table's
+ * reach count as that.
+ *   q, out  head h of sequence b at b * stride_b + h * stride_h, d contiguous
+ *           channels (dtype)
+ *   lengths [B] int32; lse [B, Hq] fp32, or NULL
+ * Supported: as above, Hk divides Hq, Hq <= 65536. */
+typedef struct {
+  int64_t B, Hq, Hk, d;
+  int64_t pages, page, table_width;
+  int64_t q_stride_b, q_stride_h;
+  int64_t out_stride_b, out_stride_h;
+  int64_t window, sinks;     /* 0: all positions; sinks only with a window */
+  int32_t dtype;             /* gdn_dtype_t: type of q and out */
+  int32_t format;            /* gdn_kv_format_t */
+  float scale;
+  const int32_t* page_table;
+  const int32_t* lengths;
+  void* workspace;           /* caller-owned device memory, 256-byte aligned */
+  size_t workspace_bytes;
+  void* stream;
+} gdn_attention_problem_t;
+
+/* Workspace bytes of gdn_attention_step (0 if invalid, unsupported, or where
+ * none is needed): it depends on the sizes alone.  Calls that may run at the
+ * same time, replayed graphs among them, need a workspace each. */
+size_t gdn_attention_workspace_bytes(const gdn_attention_problem_t* p);
+
+gdn_status_t gdn_attention_step(const gdn_attention_problem_t* p, const void* q, const void* k_cache, const void* v_cache,
+                                const void* k_scales, const void* v_scales, void* out, float* lse);
+
+/* ---- The seam between two blocks: norm, gate, residual, norm ------------------
+ *
+ * Per row of D channels, x the residual stream and y a block's output:
+ *   u = post_weight * y / sqrt(mean(y^2) + eps)     (post_weight NULL: u = y)
+ *   h = residual_scale * x + gate * u               (gate NULL: 1)
+ *   n = weight * h / sqrt(mean(h^2) + eps)          (weight NULL: no n)
+ * n is computed from h before h is rounded.
+ *   x, y, h, n   rows of D channels (dtype), strided, packed with seq_offsets;
+ *                y may be NULL (then h = residual_scale * x; gate and
+ *                post_weight NULL); h may be NULL, or x (in place)
+ *   gate         [D] fp32 (gate_stride_b 0), or [B, D] (gate_stride_b D)
+ *   weight, post_weight  [D] fp32
+ * The backward call takes the gradients dh (NULL: zero) and dn (with weight),
+ * at h's and n's strides, and gives
+ *   dx, dy               rows (dtype) at strides of their own; dy with y; dx may be dh
+ *   dgate                like gate; dpost_weight, dweight [D] fp32
+ * each NULL where it is not wanted.  Sums over rows are fp32 in a fixed order.
+ * Supported: D <= 16384, B * T < 2^31, eps finite and >= 0. */
+typedef struct {
+  int64_t B, T, D;
+  int64_t x_stride_b, x_stride_t;
+  int64_t y_stride_b, y_stride_t;
+  int64_t h_stride_b, h_stride_t;    /* of h and dh */
+  int64_t n_stride_b, n_stride_t;    /* of n and dn */
+  int64_t dx_stride_b, dx_stride_t;
+  int64_t dy_stride_b, dy_stride_t;
+  int64_t gate_stride_b;
+  int32_t dtype;
+  int32_t options;                   /* 0 or GDN_LAYER_OPT_ZERO_UNUSED (h, n, dx and dy) */
+  float residual_scale, eps;
+  const int32_t* seq_offsets;
+  const float* gate;
+  const float* post_weight;
+  const float* weight;
+  void* workspace;                   /* gdn_norm_backward: caller-owned device memory, 256-byte aligned */
+  size_t workspace_bytes;
+  void* stream;
+} gdn_norm_problem_t;
+
+gdn_status_t gdn_norm_forward(const gdn_norm_problem_t* p, const void* x, const void* y, void* h, void* n);
+
+/* Workspace bytes of gdn_norm_backward (0 if invalid or unsupported, or where
+ * no gradient is summed over rows): it depends on the sizes, on whether
+ * seq_offsets, gate, post_weight and weight are given, and on gate_stride_b. */
+size_t gdn_norm_workspace_bytes(const gdn_norm_problem_t* p);
+
+gdn_status_t gdn_norm_backward(const gdn_norm_problem_t* p, const void* x, const void* y, const void* dh, const void* dn,
+                               void* dx, void* dy, float* dgate, float* dpost_weight, float* dweight);
+
 /* Static description of a status code. */
 const char* gdn_status_string(int32_t status);
 
