@@ -3,98 +3,682 @@
 //   s_p = scale q . k_p,  out = sum_p e^(s_p - m) v_p / l,  l = sum_p e^(s_p - m),
 //   lse = m + log l,  m = max_p s_p
 //
-// One workgroup per sequence and query head: its waves take every fourth
-// token, each with a running maximum and sum of its own.
+// One pass over the keys and values with a running maximum and sum (in powers
+// of two), split over the length: bound by reading the cache.
+//
+// A wave walks tiles of 32 tokens of one head of the cache and up to 32 query
+// heads that share it, in registers alone.  With g = lane / 16, n = lane % 16:
+//   S^T = K Q^T  (tokens x queries): lane n of A holds the key of token n (of
+//     each half of the tile), group g channels of it; a lane of the result holds
+//     the scores of tokens 4g .. 4g+3 with query n.
+//   O^T = V^T P^T  (channels x queries): the contraction takes, in group g, just
+//     those tokens, so the weights go in as they came out.  A's row n is channel
+//     c of the ones that lane n loaded of each of the eight tokens: its values
+//     lie in one lane already and need only be put in pairs.
+// So keys and values are read as they lie in memory, once, and nothing crosses
+// lanes but the maximum over groups.  Query n is the lane's in both results, as
+// are its maximum, sum and rescaling.
+//
+// Rounding: queries and values of 16 bits or fewer enter bf16 products exactly;
+// weights enter as two bf16 terms (2^-17 of themselves), with fp32 queries both
+// as three (2^-25); a cache in fp32 goes through fp32 products.  Everything
+// else is fp32.
 #include "gdn_kv.h"
 
 namespace gdn {
 namespace {
 
+constexpr int kTile = 32;          // tokens
 constexpr int kWaves = 4;
+constexpr int kLeast = kWaves;     // tiles of an item: one a wave
+constexpr int kTarget = 1024;      // workgroups that a call is cut into, where it is long enough
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
+// What of a sequence is visible: [0, sinks) and [lo, len), as `tiles` tiles, the
+// first `first` of them from position 0 on, the others from tile `from` on.
+struct Seen {
+  int64_t len, lo, sinks, tiles, first, from;
+};
+
+__device__ __forceinline__ Seen seen_of(const AttendArgs& a, int64_t len) {
+  const int64_t reach = a.width << a.page_bits;
+  Seen s;
+  s.len = len < 0 ? 0 : len > reach ? reach : len;
+  s.lo = a.window && s.len > a.window ? s.len - a.window : 0;
+  s.sinks = a.sinks < s.lo ? a.sinks : s.lo;
+  s.from = s.lo / kTile;
+  s.first = (s.sinks + kTile - 1) / kTile;
+  if (s.first > s.from) s.first = s.from;
+  s.tiles = s.first + (s.len + kTile - 1) / kTile - s.from;
+  return s;
+}
+
+// Items: runs of C tiles of one sequence, C the least number that leaves at
+// most `a.items - B` whole ones; sequence s owns the items floor(before / C) + s
+// onwards, `before` the tiles of the sequences before it (as packed batches
+// are cut; see find_packed).  Each has one at least.
+struct Item {
+  int64_t b, chunk, chunks, C;
+  int64_t len;
+  bool any;  // something to do
+};
+
+// Running sum over a wave (modulo 2^32): rows of 16 shifted by 1, 2, 4 and 8,
+// then a row's last lane to the next and lane 31 to the upper half.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ unsigned moved(unsigned x) {
+  return (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ unsigned wave_scan(unsigned x) {
+  x += moved<0x111, 0xF>(x);
+  x += moved<0x112, 0xF>(x);
+  x += moved<0x114, 0xF>(x);
+  x += moved<0x118, 0xF>(x);
+  x += moved<0x142, 0xA>(x);
+  x += moved<0x143, 0xC>(x);
   return x;
 }
 
-template <typename MT, int FORMAT>
-__global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
-  __shared__ float part[kWaves][256 + 2];
-  const int64_t b = blockIdx.x / a.Hq;
-  const int h = (int)(blockIdx.x % a.Hq), kh = h / (a.Hq / a.Hk);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const bool mine = lane < a.d / 8;  // lanes that hold channels
-  const int64_t reach = a.width << a.page_bits;
-  int64_t len = a.lengths[b];
-  if (len > reach) len = reach;
-  float q[8] = {}, acc[8] = {};
-  if (mine) load8<MT, false>(static_cast<const MT*>(a.q) + b * a.q_sb + h * a.q_sh + 8 * lane, q);
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t p = wave; p < len; p += kWaves) {
-    if (a.window && p >= a.sinks && p < len - a.window) continue;
-    const int64_t row = kv_row(a.table + b * a.width, a.width, a.pages, a.page_bits, p, a.Hk, kh);
-    if (row < 0) continue;
-    float x[8] = {};
-    float s = 0.0f;
-    if (mine) {
-      pool8<MT, FORMAT>(a.k_cache, a.k_scales, row, a.d, lane, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(q[i], x[i], s);
-    }
-    s = wave_sum(s) * a.scale;
-    const float n = fmaxf(m, s);
-    const float keep = n == -INFINITY ? 1.0f : expf(m - n), e = n == -INFINITY ? 0.0f : expf(s - n);
-    m = n;
-    l = l * keep + e;
-    if (mine) {
-      pool8<MT, FORMAT>(a.v_cache, a.v_scales, row, a.d, lane, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(acc[i], keep, e * x[i]);
-    }
-  }
-  if (mine)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) part[wave][8 * lane + i] = acc[i];
-  if (lane == 0) {
-    part[wave][256] = m;
-    part[wave][257] = l;
-  }
-  __syncthreads();
-  if (wave != 0) return;
-  float top = -INFINITY, sum = 0.0f, o[8] = {};
-  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, part[w][256]);
-  for (int w = 0; w < kWaves; ++w) {
-    const float f = part[w][257] == 0.0f ? 0.0f : expf(part[w][256] - top);
-    sum += f * part[w][257];
-    if (mine)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] += f * part[w][8 * lane + i];
-  }
-  if (mine) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = sum == 0.0f ? 0.0f : o[i] / sum;
-    store8<MT, false>(static_cast<MT*>(a.out) + b * a.o_sb + h * a.o_sh + 8 * lane, o);
-  }
-  if (lane == 0 && a.lse) a.lse[b * a.Hq + h] = sum == 0.0f ? -INFINITY : top + logf(sum);
+// Lane l's value, the same for the whole wave.
+__device__ __forceinline__ int64_t of_lane(int64_t x, int l) {
+  const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)x, l), hi = (unsigned)__builtin_amdgcn_readlane((int)(x >> 32), l);
+  return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-template <typename MT, int FORMAT>
+__device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t i) {
+  const int lane = threadIdx.x & 63;
+  const int rounds = (int)((a.B + 63) / 64);
+  int64_t total = 0;
+  unsigned n = 0, before = 0;  // tiles of the lane's sequence, and before it in this round
+  int64_t len = 0;
+  for (int r = 0; r < rounds; ++r) {
+    const int64_t b = r * 64 + lane;
+    len = b < a.B ? a.lengths[b] : 0;
+    n = b < a.B ? (unsigned)seen_of(a, len).tiles : 0;
+    before = wave_scan(n) - n;
+    total += (int64_t)(unsigned)__builtin_amdgcn_readlane((int)before, 63) + (unsigned)__builtin_amdgcn_readlane((int)n, 63);
+  }
+  Item it;
+  const int64_t most = a.items - a.B;
+  it.C = (total + most - 1) / most;
+  if (it.C < kLeast) it.C = kLeast;
+  int64_t run = 0;
+  it.b = 0;
+  for (int r = 0; r < rounds; ++r) {
+    const int64_t b = r * 64 + lane;
+    if (rounds > 1) {
+      len = b < a.B ? a.lengths[b] : 0;
+      n = b < a.B ? (unsigned)seen_of(a, len).tiles : 0;
+      before = wave_scan(n) - n;
+    }
+    const int64_t at = run + before;
+    const int64_t first = (((at | it.C) >> 32) == 0 ? (int64_t)((unsigned)at / (unsigned)it.C) : at / it.C) + b;
+    const unsigned long long in = __ballot(b < a.B && first <= i);
+    if (in == 0) break;
+    const int l = 63 - __builtin_clzll(in);
+    it.b = r * 64 + l;
+    it.chunk = i - of_lane(first, l);
+    it.len = of_lane(len, l);
+    const int64_t tiles = (unsigned)__builtin_amdgcn_readlane((int)n, l);
+    it.chunks = tiles ? (tiles + it.C - 1) / it.C : 1;
+    if (in != ~0ull) break;
+    run += (int64_t)(unsigned)__builtin_amdgcn_readlane((int)before, 63) + (unsigned)__builtin_amdgcn_readlane((int)n, 63);
+  }
+  it.any = it.chunk < it.chunks;
+  return it;
+}
+
+// Over the four lane groups, for every n: rows of 16 lanes are swapped by pairs,
+// then the wave's halves.  (The swapped words are copied before they are taken
+// as floats: a bit cast of a vector's element takes the first one.)
+template <typename Join>
+__device__ __forceinline__ float over_groups(float x, Join join) {
+  unsigned u = __builtin_bit_cast(unsigned, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned a = r[0], b = r[1];
+  u = __builtin_bit_cast(unsigned, join(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned c = s[0], d = s[1];
+  return join(__builtin_bit_cast(float, c), __builtin_bit_cast(float, d));
+}
+__device__ __forceinline__ float over_groups_max(float x) {
+  return over_groups(x, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float over_groups_sum(float x) {
+  return over_groups(x, [](float a, float b) { return a + b; });
+}
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// N words from memory, aligned to `A` bytes
+template <int N, int A>
+__device__ __forceinline__ void words(const uint8_t* p, unsigned (&w)[N]) {
+  __builtin_memcpy(w, __builtin_assume_aligned(p, A), N * 4);
+}
+
+// Two channels from codes, as two bf16 values.
+template <int FORMAT, int AT>  // AT: which pair of the word
+__device__ __forceinline__ unsigned two(unsigned w, float scale) {
+  if constexpr (FORMAT == GDN_KV_BF16)
+    return w;
+  else if constexpr (FORMAT == GDN_KV_MXFP8)
+    return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, AT != 0));
+  else
+    return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, AT));
+}
+
+// The geometry of a row of D channels in a format.
+template <int FORMAT, int D>
+struct Shape {
+  static constexpr bool kWide = FORMAT == GDN_KV_F32;
+  static constexpr bool kCodes = FORMAT == GDN_KV_MXFP8 || FORMAT == GDN_KV_MXFP4;
+  static constexpr int kBits = kWide ? 32 : FORMAT == GDN_KV_BF16 ? 16 : FORMAT == GDN_KV_MXFP8 ? 8 : 4;
+  static constexpr int kRow = D * kBits / 8;             // bytes
+  static constexpr int kBlocks = D / 32;                 // scale bytes
+  static constexpr int kPerWord = 32 / kBits;            // channels
+  // keys: a lane loads kRun channels at a time, its group's of every 4 kRun
+  static constexpr int kRun = 128 / kBits < D / 4 ? 128 / kBits : D / 4;
+  static constexpr int kLoads = D / (4 * kRun);
+  static constexpr int kLoadWords = kRun / kPerWord;
+  // values: a lane loads kCols channels of a token, kPiece at a time
+  static constexpr int kCols = D / 16;
+  static constexpr int kPiece = 128 / kBits < kCols ? 128 / kBits : kCols;
+  static constexpr int kPieces = kCols / kPiece;
+  static constexpr int kPieceBytes = kPiece * kBits / 8;
+  static constexpr int kPieceWords = (kPieceBytes + 3) / 4;
+  // first channel of the eight (four, in fp32: one of four) that lane group g
+  // brings to product m
+  static __device__ __forceinline__ int channel(int m, int g) {
+    if constexpr (kWide) return m * 16 + g * 4;
+    constexpr int per = kRun / 8;
+    return (m / per) * 4 * kRun + g * kRun + (m % per) * 8;
+  }
+  // channel of the output that lane group g holds at (column c, register i)
+  static __device__ __forceinline__ int out_channel(int c, int g, int i) {
+    return (c / kPiece) * 16 * kPiece + (4 * g + i) * kPiece + c % kPiece;
+  }
+};
+
+template <typename MT, int FORMAT, int D, int QT>
+__global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
+  typedef Shape<FORMAT, D> F;
+  constexpr bool kWide = F::kWide, kCodes = F::kCodes;
+  constexpr int kQTerms = kWide || sizeof(MT) == 2 ? 1 : 3, kPTerms = kWide ? 1 : sizeof(MT) == 2 ? 2 : 3;
+  __shared__ f32x4 dump[2][QT * F::kCols * 64];
+  __shared__ float stat[2][kWaves][QT * 16];
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int g = lane >> 4, n = lane & 15;
+  const int G = a.Hq / a.Hk, shares = (G + 16 * QT - 1) / (16 * QT);
+  const int kh = (int)(blockIdx.x % a.Hk), share = (int)(blockIdx.x / a.Hk % shares);
+  const Item it = find_item(a, blockIdx.x / ((unsigned)a.Hk * shares));
+  const int64_t item = blockIdx.x / ((unsigned)a.Hk * shares);
+  if (!it.any) return;
+  const int64_t b = it.b;
+  const Seen seen = seen_of(a, it.len);
+  if (a.plan && it.chunk == 0 && kh == 0 && share == 0 && threadIdx.x == 0) {
+    a.plan[2 * b] = (int)item;
+    a.plan[2 * b + 1] = (int)it.chunks;
+  }
+
+  // queries, by the channels that the keys come in
+  const int heads = G - share * 16 * QT < 16 * QT ? G - share * 16 * QT : 16 * QT;  // of this workgroup
+  const int head0 = kh * G + share * 16 * QT;
+  bf16x8 qb[kWide ? 1 : QT][kQTerms][kWide ? 1 : D / 32];
+  f32x4 qw[kWide ? QT : 1][kWide ? D / 16 : 1];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const bool mine = t * 16 + n < heads;
+    const MT* q = static_cast<const MT*>(a.q) + b * a.q_sb + (head0 + (mine ? t * 16 + n : 0)) * a.q_sh;
+    if constexpr (kWide) {
+#pragma unroll
+      for (int m = 0; m < D / 16; ++m) {
+        if (a.q_aligned) {
+          qw[t][m] = *reinterpret_cast<const f32x4*>(q + F::channel(m, g));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qw[t][m][e] = q[F::channel(m, g) + e];
+        }
+        if (!mine) qw[t][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < D / 32; ++m) {
+        float x[8];
+        if (a.q_aligned) load8<MT, true>(q + F::channel(m, g), x);
+        else load8<MT, false>(q + F::channel(m, g), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float rest = mine ? x[e] : 0.0f;
+#pragma unroll
+          for (int k = 0; k < kQTerms; ++k) {
+            qb[t][k][m][e] = (bf16)rest;
+            rest -= (float)qb[t][k][m][e];
+          }
+        }
+      }
+    }
+  }
+
+  // tiles of this wave: every fourth of the item's
+  const int64_t end = (it.chunk + 1) * it.C < seen.tiles ? (it.chunk + 1) * it.C : seen.tiles;
+  int64_t tile = it.chunk * it.C + wave;
+  const int32_t* table = a.table + b * a.width;
+  const uint8_t* pools[2] = {static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache)};
+  const int64_t mask = ((int64_t)1 << a.page_bits) - 1;
+  const unsigned k_off = n * F::kRow + g * (F::kRun * F::kBits / 8), v_off = 4 * g * F::kRow + n * F::kPieceBytes;
+
+  auto place = [&](int64_t t) { return (t < seen.first ? t : t - seen.first + seen.from) * kTile; };
+  // page numbers of a tile's halves; no page: -1
+  struct Pages { int p[2]; };
+  auto pages_of = [&](int64_t t) {
+    Pages r;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int64_t i = (place(t) + 16 * s) >> a.page_bits;
+      const int64_t at = t < end && i < a.width ? i : 0;
+      const int v = *(const __attribute__((address_space(4))) int*)(uintptr_t)(table + at);
+      r.p[s] = i < a.width && v >= 0 && v < a.pages ? v : -1;
+    }
+    return r;
+  };
+  // first row in the pools of half s of a tile (page 0 where there is none)
+  auto row_of = [&](int64_t t, const Pages& p, int s) {
+    const int64_t page = p.p[s] < 0 ? 0 : p.p[s];
+    return ((page * a.Hk + kh) << a.page_bits) + ((place(t) + 16 * s) & mask);
+  };
+
+  unsigned kw[2][F::kLoads][F::kLoadWords], vw[8][F::kPieces][F::kPieceWords];
+  unsigned ksw[2][kCodes ? (F::kBlocks + 3) / 4 : 1], vsw[2][kCodes ? F::kBlocks : 1];
+  auto load_k = [&](int64_t t, const Pages& p) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int64_t row = row_of(t, p, s);
+      const uint8_t* base = pools[0] + row * F::kRow;
+#pragma unroll
+      for (int j = 0; j < F::kLoads; ++j)
+        words<F::kLoadWords, F::kLoadWords * 4>(base + k_off + j * (4 * F::kRun * F::kBits / 8), kw[s][j]);
+      if constexpr (kCodes) {
+        const uint8_t* scales = a.k_scales + row * F::kBlocks;
+        if constexpr (F::kBlocks == 2) ksw[s][0] = *reinterpret_cast<const uint16_t*>(scales + n * 2);
+        else words<F::kBlocks / 4, 4>(scales + n * F::kBlocks, ksw[s]);
+      }
+    }
+  };
+  auto load_v = [&](int64_t t, const Pages& p) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int64_t row = row_of(t, p, s);
+      const uint8_t* base = pools[1] + row * F::kRow;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < F::kPieces; ++j) {
+          const uint8_t* at = base + v_off + i * F::kRow + j * 16 * F::kPieceBytes;
+          if constexpr (F::kPieceBytes == 2) vw[4 * s + i][j][0] = *reinterpret_cast<const uint16_t*>(at);
+          else words<F::kPieceWords, F::kPieceBytes>(at, vw[4 * s + i][j]);
+        }
+      // the scale bytes of tokens 4g .. 4g + 3
+      if constexpr (kCodes) words<F::kBlocks, 4>(a.v_scales + (row + 4 * g) * F::kBlocks, vsw[s]);
+    }
+  };
+
+  f32x4 acc[QT][F::kCols];
+  float top[QT], sum[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    top[t] = -INFINITY;
+    sum[t] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < F::kCols; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  const float scale2 = a.scale * kLog2e;
+
+  Pages now = {}, next = {};
+  if (tile < end) {
+    now = pages_of(tile);
+    load_k(tile, now);
+    load_v(tile, now);
+    next = pages_of(tile + kWaves);
+  }
+  for (; tile < end; tile += kWaves) {
+    const bool more = tile + kWaves < end;
+    // scores
+    f32x4 s[QT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int t = 0; t < QT; ++t) s[t][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (kWide) {
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+              s[t][h] = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, kw[h][m][e]), qw[t][m][e], s[t][h], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) {
+          constexpr int per = F::kRun / 8, wpm = 8 / F::kPerWord;  // products of a load, words of a product
+          float f = 1.0f;
+          if constexpr (kCodes) {
+            // the block of channel(m, g): its word and byte
+            constexpr int kHalf = F::kRun == 16;  // two groups share a block
+            const int at = F::kRun == 16 ? 2 * (m / per) : 4 * (m / per);
+            const unsigned byte = (ksw[h][at / 4] >> (8 * (at % 4) + 8 * (kHalf ? g >> 1 : g))) & 255u;
+            f = __builtin_bit_cast(float, byte << 23);
+          }
+          unsigned w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const unsigned src = kw[h][m / per][(m % per) * wpm + e * wpm / 4];
+            if constexpr (FORMAT == GDN_KV_BF16) w[e] = src;
+            else if constexpr (FORMAT == GDN_KV_MXFP8) w[e] = e % 2 ? two<FORMAT, 1>(src, f) : two<FORMAT, 0>(src, f);
+            else w[e] = e == 0 ? two<FORMAT, 0>(src, f) : e == 1 ? two<FORMAT, 1>(src, f) : e == 2 ? two<FORMAT, 2>(src, f) : two<FORMAT, 3>(src, f);
+          }
+          bf16x8 k;
+          __builtin_memcpy(&k, w, 16);
+#pragma unroll
+          for (int t = 0; t < QT; ++t)
+#pragma unroll
+            for (int x = kQTerms - 1; x >= 0; --x)
+              s[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qb[t][x][m], s[t][h], 0, 0, 0);
+        }
+      }
+    }
+    Pages after = {};
+    if (more) {
+      after = pages_of(tile + 2 * kWaves);
+      load_k(tile + kWaves, next);
+    }
+    // a tile that is not visible as a whole: which of the lane's tokens are
+    const int64_t p0 = place(tile);
+    const bool whole = p0 + kTile <= seen.len && (p0 >= seen.lo || p0 + kTile <= seen.sinks) && now.p[0] >= 0 && now.p[1] >= 0;
+    unsigned ok = 0xFF;
+    if (!whole) {
+      ok = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t p = p0 + 16 * (i / 4) + 4 * g + i % 4;
+        if (p < seen.len && (p >= seen.lo || p < seen.sinks) && now.p[i / 4] >= 0) ok |= 1u << i;
+      }
+    }
+    bf16x8 pb[kWide ? 1 : QT][kPTerms];
+    float pw[QT][8];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      float x[8], most = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = s[t][i / 4][i % 4] * scale2;
+        if (!whole) x[i] = (ok >> i) & 1 ? x[i] : -INFINITY;
+        most = fmaxf(most, x[i]);
+      }
+      most = fmaxf(top[t], over_groups_max(most));
+      const float ref = most == -INFINITY ? 0.0f : most;
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        pw[t][i] = hw_exp2(x[i] - ref);
+        part += pw[t][i];
+      }
+      if (__any(most > top[t])) {
+        const float keep = hw_exp2(top[t] - ref);
+        sum[t] *= keep;
+#pragma unroll
+        for (int c = 0; c < F::kCols; ++c) acc[t][c] *= keep;
+        top[t] = most;
+      }
+      sum[t] += part;
+      if constexpr (!kWide)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float rest = pw[t][i];
+#pragma unroll
+          for (int k = 0; k < kPTerms; ++k) {
+            pb[t][k][i] = (bf16)rest;
+            rest -= (float)pb[t][k][i];
+          }
+        }
+    }
+    // values; what is not visible is zero, whatever lies there
+    float vs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      vs[i] = 0.0f;
+      if constexpr (kCodes) {
+        const int block = n * F::kCols / 32;  // of the lane's channels
+        const unsigned w = F::kBlocks == 2 ? vsw[i / 4][(i % 4) / 2] >> (16 * (i % 2))
+                           : F::kBlocks == 4 ? vsw[i / 4][i % 4]
+                                             : block >= 4 ? vsw[i / 4][2 * (i % 4) + 1] : vsw[i / 4][2 * (i % 4)];
+        vs[i] = __builtin_bit_cast(float, ((w >> (8 * (block & 3))) & 255u) << 23);
+      }
+    }
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!((ok >> i) & 1)) {
+          vs[i] = 0.0f;
+#pragma unroll
+          for (int j = 0; j < F::kPieces; ++j)
+#pragma unroll
+            for (int w = 0; w < F::kPieceWords; ++w) vw[i][j][w] = 0;
+        }
+    }
+    if constexpr (kWide) {
+#pragma unroll
+      for (int c = 0; c < F::kCols; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int t = 0; t < QT; ++t)
+            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, vw[i][c / F::kPiece][c % F::kPiece]), pw[t][i],
+                                                             acc[t][c], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int c = 0; c < F::kCols; c += 2) {
+        unsigned pair[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const unsigned src = vw[i][c / F::kPiece][c % F::kPiece / F::kPerWord];
+          const int at = c % F::kPerWord / 2;
+          pair[i] = at == 0 ? two<FORMAT, 0>(src, vs[i]) : at == 1 ? two<FORMAT, 1>(src, vs[i]) : at == 2 ? two<FORMAT, 2>(src, vs[i]) : two<FORMAT, 3>(src, vs[i]);
+        }
+        unsigned even[4], odd[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          even[u] = __builtin_amdgcn_perm(pair[2 * u + 1], pair[2 * u], 0x05040100u);
+          odd[u] = __builtin_amdgcn_perm(pair[2 * u + 1], pair[2 * u], 0x07060302u);
+        }
+        bf16x8 v[2];
+        __builtin_memcpy(&v[0], even, 16);
+        __builtin_memcpy(&v[1], odd, 16);
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int k = kPTerms - 1; k >= 0; --k)
+              acc[t][c + o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[o], pb[t][k], acc[t][c + o], 0, 0, 0);
+      }
+    }
+    if (more) load_v(tile + kWaves, next);
+    now = next;
+    next = after;
+  }
+
+  // the waves' parts, brought to one maximum and added by twos
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    sum[t] = over_groups_sum(sum[t]);
+    if (g == 0) {
+      stat[0][wave][t * 16 + n] = top[t];
+      stat[1][wave][t * 16 + n] = sum[t];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    float most = -INFINITY, all = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) most = fmaxf(most, stat[0][w][t * 16 + n]);
+    const float ref = most == -INFINITY ? 0.0f : most;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) all += hw_exp2(stat[0][w][t * 16 + n] - ref) * stat[1][w][t * 16 + n];
+    const float f = hw_exp2(top[t] - ref);
+#pragma unroll
+    for (int c = 0; c < F::kCols; ++c) acc[t][c] *= f;
+    top[t] = most;
+    sum[t] = all;
+  }
+#pragma unroll
+  for (int half = kWaves / 2; half >= 1; half /= 2) {
+    if (wave >= half && wave < 2 * half)
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int c = 0; c < F::kCols; ++c) dump[wave - half][(t * F::kCols + c) * 64 + lane] = acc[t][c];
+    __syncthreads();
+    if (wave < half)
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int c = 0; c < F::kCols; ++c) acc[t][c] += dump[wave][(t * F::kCols + c) * 64 + lane];
+    if (half > 1) __syncthreads();
+  }
+  if (wave != 0) return;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    if (t * 16 + n >= heads) continue;
+    const int h = head0 + t * 16 + n;
+    if (it.chunks > 1) {
+      float* to = a.parts + (item * a.Hq + h) * D;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < F::kCols; ++c) to[F::out_channel(c, g, i)] = acc[t][c][i];
+      if (g == 0) {
+        a.stats[2 * (item * a.Hq + h)] = top[t];
+        a.stats[2 * (item * a.Hq + h) + 1] = sum[t];
+      }
+    } else {
+      const float inv = sum[t] == 0.0f ? 0.0f : 1.0f / sum[t];
+      MT* to = static_cast<MT*>(a.out) + b * a.o_sb + h * a.o_sh;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < F::kCols; ++c) to[F::out_channel(c, g, i)] = (MT)(acc[t][c][i] * inv);
+      if (g == 0 && a.lse) a.lse[b * a.Hq + h] = sum[t] == 0.0f ? -INFINITY : (top[t] + log2f(sum[t])) * 0.6931471805599453f;
+    }
+  }
+}
+
+// The items of a sequence that was split, joined: a workgroup per sequence and
+// query head, its waves every fourth item, D / 64 channels a lane.
+template <typename MT, int D>
+__global__ __launch_bounds__(kWaves * 64) void join_kernel(AttendArgs a) {
+  constexpr int N = D / 64;
+  __shared__ float part[kWaves][D + 1];
+  const int64_t b = blockIdx.x / a.Hq;
+  const int h = (int)(blockIdx.x % a.Hq);
+  const int64_t first = a.plan[2 * b], chunks = a.plan[2 * b + 1];
+  if (chunks == 1) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const float* stats = a.stats + 2 * (first * a.Hq + h);
+  float most = -INFINITY;
+  for (int64_t c = lane; c < chunks; c += 64) most = fmaxf(most, stats[2 * c * a.Hq]);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) most = fmaxf(most, __shfl_xor(most, m, 64));
+  const float ref = most == -INFINITY ? 0.0f : most;
+  float sum = 0.0f, o[N] = {};
+#pragma unroll 4
+  for (int64_t c = wave; c < chunks; c += kWaves) {
+    const float f = hw_exp2(stats[2 * c * a.Hq] - ref);
+    sum = fmaf(f, stats[2 * c * a.Hq + 1], sum);
+    const float* from = a.parts + ((first + c) * a.Hq + h) * D + lane * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = fmaf(f, from[i], o[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) part[wave][lane * N + i] = o[i];
+  if (lane == 0) part[wave][D] = sum;
+  __syncthreads();
+  if (wave != 0) return;
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) sum += part[w][D];
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  MT* to = static_cast<MT*>(a.out) + b * a.o_sb + h * a.o_sh + lane * N;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) x += part[w][lane * N + i];
+    to[i] = (MT)(x * inv);
+  }
+  if (lane == 0 && a.lse) a.lse[b * a.Hq + h] = sum == 0.0f ? -INFINITY : (most + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <typename MT, int FORMAT, int D, int QT>
 hipError_t attend_launch(const AttendArgs& a, hipStream_t stream) {
-  const int64_t blocks = a.B * a.Hq;
-  if (!grid_fits(blocks, kWaves * 64)) return hipErrorNotSupported;
-  hipLaunchKernelGGL((attend_kernel<MT, FORMAT>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
+  const int64_t shares = (a.Hq / a.Hk + 16 * QT - 1) / (16 * QT);
+  const int64_t blocks = a.items * a.Hk * shares;
+  if (!grid_fits(blocks, kWaves * 64) || !grid_fits(a.B * a.Hq, kWaves * 64)) return hipErrorNotSupported;
+  hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.plan) return e;
+  hipLaunchKernelGGL((join_kernel<MT, D>), dim3((unsigned)(a.B * a.Hq)), dim3(kWaves * 64), 0, stream, a);
   return hipGetLastError();
 }
 
+// 32 query heads a workgroup where more than 16 share a head of the cache; 16
+// with fp32 rows of 256 channels, whose registers do not hold more
+template <typename MT, int FORMAT, int D>
+hipError_t attend_by_heads(const AttendArgs& a, hipStream_t stream) {
+  if constexpr (sizeof(MT) == 4 && D == 256)
+    return attend_launch<MT, FORMAT, D, 1>(a, stream);
+  else
+    return a.Hq / a.Hk <= 16 ? attend_launch<MT, FORMAT, D, 1>(a, stream) : attend_launch<MT, FORMAT, D, 2>(a, stream);
+}
+
+template <typename MT, int FORMAT>
+hipError_t attend_for(const AttendArgs& a, hipStream_t stream) {
+  return a.d == 64    ? attend_by_heads<MT, FORMAT, 64>(a, stream)
+         : a.d == 128 ? attend_by_heads<MT, FORMAT, 128>(a, stream)
+                      : attend_by_heads<MT, FORMAT, 256>(a, stream);
+}
+
+size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
 }  // namespace
+
+AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, int64_t reach, int64_t window, int64_t sinks) {
+  AttendPlan p = {};
+  const int64_t G = Hq / Hk, shares = G <= 16 ? 1 : (G + 31) / 32;
+  // tiles that a sequence can have
+  int64_t most = reach;
+  if (window && window + sinks < reach) most = window + sinks + 2 * kTile;
+  const int64_t tiles = (most + kTile - 1) / kTile;
+  int64_t whole = (kTarget + Hk * shares - 1) / (Hk * shares);
+  if (whole < 1) whole = 1;
+  // no more than all of them make
+  const int64_t all = (tiles + kLeast - 1) / kLeast;
+  if (all < (whole + B - 1) / B) whole = all * B;
+  p.items = whole + B;
+  if (tiles > kLeast && p.items < ((int64_t)1 << 31)) {
+    p.plan_bytes = padded((size_t)B * 8);
+    p.parts_bytes = padded((size_t)p.items * Hq * d * 4);
+    p.total_bytes = p.plan_bytes + p.parts_bytes + padded((size_t)p.items * Hq * 8);
+  }
+  return p;
+}
 
 template <typename MT>
 hipError_t launch_attend(const AttendArgs& a, int format, hipStream_t stream) {
   switch (format) {
-    case GDN_KV_MXFP8: return attend_launch<MT, GDN_KV_MXFP8>(a, stream);
-    case GDN_KV_MXFP4: return attend_launch<MT, GDN_KV_MXFP4>(a, stream);
-    default: return attend_launch<MT, sizeof(MT) == 4 ? GDN_KV_F32 : GDN_KV_BF16>(a, stream);
+    case GDN_KV_MXFP8: return attend_for<MT, GDN_KV_MXFP8>(a, stream);
+    case GDN_KV_MXFP4: return attend_for<MT, GDN_KV_MXFP4>(a, stream);
+    default: return attend_for<MT, sizeof(MT) == 4 ? GDN_KV_F32 : GDN_KV_BF16>(a, stream);
   }
 }
 

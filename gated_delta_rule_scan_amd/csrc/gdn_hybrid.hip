@@ -132,12 +132,16 @@ gdn_status_t kv_call(const gdn_kv_problem_t* p, bool write, const void* k, const
 
 gdn_status_t attention_sizes(const gdn_attention_problem_t* p) {
   if (!p) return GDN_ERR_INVALID_ARGUMENT;
-  if (p->Hq < 1 || p->window < 0 || p->sinks < 0) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->Hq < 1 || p->window < 0 || p->window > kMost || p->sinks < 0 || p->sinks > kMost) return GDN_ERR_INVALID_ARGUMENT;
   const gdn_status_t sizes = cache_sizes(p->B, p->Hk, p->d, p->pages, p->page, p->table_width, p->dtype, p->format);
   if (sizes != GDN_OK) return sizes;
   if (p->Hq % p->Hk != 0) return GDN_ERR_INVALID_ARGUMENT;
   if (p->Hq > kMostHeads || p->B > kMost / p->Hq) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
+}
+
+AttendPlan plan_of(const gdn_attention_problem_t* p) {
+  return attend_plan(p->B, p->Hq, p->Hk, p->d, p->table_width * p->page, p->window, p->window ? p->sinks : 0);
 }
 
 gdn_status_t norm_sizes(const gdn_norm_problem_t* p) {
@@ -251,7 +255,7 @@ extern "C" gdn_status_t gdn_kv_read(const gdn_kv_problem_t* p, const void* k_cac
 
 extern "C" size_t gdn_attention_workspace_bytes(const gdn_attention_problem_t* p) {
   if (attention_sizes(p) != GDN_OK) return 0;
-  return 0;
+  return plan_of(p).total_bytes;
 }
 
 extern "C" gdn_status_t gdn_attention_step(const gdn_attention_problem_t* p, const void* q, const void* k_cache,
@@ -276,7 +280,8 @@ extern "C" gdn_status_t gdn_attention_step(const gdn_attention_problem_t* p, con
   const Rows r_o = Rows(out, d * es).by(p->Hq, p->out_stride_h * es).by(B, p->out_stride_b * es);
   if (!r_q.fits() || !r_o.fits() || r_o.meets_itself()) return GDN_ERR_INVALID_ARGUMENT;
   const Rows r_l(lse, B * p->Hq * 4);
-  const size_t need = gdn_attention_workspace_bytes(p);
+  const AttendPlan plan = plan_of(p);
+  const size_t need = plan.total_bytes;
   if (need && (!p->workspace || !is_aligned(p->workspace, 256))) return GDN_ERR_INVALID_ARGUMENT;
   if (p->workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
   const Rows written[] = {r_o, r_l, Rows(need ? p->workspace : nullptr, (int64_t)need)};
@@ -297,6 +302,14 @@ extern "C" gdn_status_t gdn_attention_step(const gdn_attention_problem_t* p, con
   a.q_sb = p->q_stride_b; a.q_sh = p->q_stride_h; a.o_sb = p->out_stride_b; a.o_sh = p->out_stride_h;
   a.window = p->window; a.sinks = p->sinks;
   a.Hq = (int)p->Hq; a.Hk = (int)p->Hk; a.d = (int)d; a.page_bits = log2_of(p->page); a.scale = p->scale;
+  a.q_aligned = is_aligned(q, 16) && (p->Hq <= 1 || p->q_stride_h * es % 16 == 0) && (B <= 1 || p->q_stride_b * es % 16 == 0);
+  a.items = plan.items;
+  if (need) {
+    unsigned char* ws = static_cast<unsigned char*>(p->workspace);
+    a.plan = reinterpret_cast<int32_t*>(ws);
+    a.parts = reinterpret_cast<float*>(ws + plan.plan_bytes);
+    a.stats = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.parts_bytes);
+  }
   hipStream_t stream = static_cast<hipStream_t>(p->stream);
   return launched(p->dtype == GDN_DTYPE_BF16 ? launch_attend<bf16>(a, p->format, stream)
                                              : launch_attend<float>(a, p->format, stream));

@@ -132,8 +132,20 @@ struct AttendArgs {
   int64_t q_sb, q_sh, o_sb, o_sh;
   int64_t window, sinks;
   int Hq, Hk, d, page_bits;
+  int q_aligned;         // every row of q starts on 16 bytes
   float scale;
+  int64_t items;         // runs of tiles; the workspace, or null where no sequence can be split:
+  int32_t* plan;         // [B][2] first item and items of a sequence
+  float* parts;          // [items][Hq][d] sums of weighted values
+  float* stats;          // [items][Hq][2] maximum, sum of weights
 };
+
+// How a call's sequences are cut, and the workspace that takes.
+struct AttendPlan {
+  int64_t items;
+  size_t plan_bytes, parts_bytes, total_bytes;
+};
+AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, int64_t reach, int64_t window, int64_t sinks);
 
 struct NormArgs {
   const void* x;
