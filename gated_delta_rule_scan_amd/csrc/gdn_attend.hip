@@ -127,19 +127,6 @@ __device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t i) {
   return it;
 }
 
-// Over the four lane groups, for every n: rows of 16 lanes are swapped by pairs,
-// then the wave's halves.  (The swapped words are copied before they are taken
-// as floats: a bit cast of a vector's element takes the first one.)
-template <typename Join>
-__device__ __forceinline__ float over_groups(float x, Join join) {
-  unsigned u = __builtin_bit_cast(unsigned, x);
-  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const unsigned a = r[0], b = r[1];
-  u = __builtin_bit_cast(unsigned, join(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
-  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  const unsigned c = s[0], d = s[1];
-  return join(__builtin_bit_cast(float, c), __builtin_bit_cast(float, d));
-}
 __device__ __forceinline__ float over_groups_max(float x) {
   return over_groups(x, [](float a, float b) { return fmaxf(a, b); });
 }
@@ -149,10 +136,14 @@ __device__ __forceinline__ float over_groups_sum(float x) {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// N words from memory, aligned to `A` bytes
+// N words of a pool, aligned to `A` bytes.  Read once and not kept: the hint
+// for that (non-temporal) is worth a tenth and more of the rate here.
 template <int N, int A>
 __device__ __forceinline__ void words(const uint8_t* p, unsigned (&w)[N]) {
-  __builtin_memcpy(w, __builtin_assume_aligned(p, A), N * 4);
+  typedef unsigned vec __attribute__((ext_vector_type(N), aligned(A)));
+  const vec v = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p));
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = v[i];
 }
 
 // Two channels from codes, as two bf16 values.
@@ -259,9 +250,9 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
     }
   }
 
-  // tiles of this wave: every fourth of the item's
-  const int64_t end = (it.chunk + 1) * it.C < seen.tiles ? (it.chunk + 1) * it.C : seen.tiles;
-  int64_t tile = it.chunk * it.C + wave;
+  // tiles of this wave: the items of a sequence take turns, a tile a wave
+  const int64_t end = seen.tiles, step = it.chunks * kWaves;
+  int64_t tile = it.chunk * kWaves + wave;
   const int32_t* table = a.table + b * a.width;
   const uint8_t* pools[2] = {static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache)};
   const int64_t mask = ((int64_t)1 << a.page_bits) - 1;
@@ -338,10 +329,10 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
     now = pages_of(tile);
     load_k(tile, now);
     load_v(tile, now);
-    next = pages_of(tile + kWaves);
+    next = pages_of(tile + step);
   }
-  for (; tile < end; tile += kWaves) {
-    const bool more = tile + kWaves < end;
+  for (; tile < end; tile += step) {
+    const bool more = tile + step < end;
     // scores
     f32x4 s[QT][2];
 #pragma unroll
@@ -388,8 +379,8 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
     }
     Pages after = {};
     if (more) {
-      after = pages_of(tile + 2 * kWaves);
-      load_k(tile + kWaves, next);
+      after = pages_of(tile + 2 * step);
+      load_k(tile + step, next);
     }
     // a tile that is not visible as a whole: which of the lane's tokens are
     const int64_t p0 = place(tile);
@@ -502,7 +493,7 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
               acc[t][c + o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[o], pb[t][k], acc[t][c + o], 0, 0, 0);
       }
     }
-    if (more) load_v(tile + kWaves, next);
+    if (more) load_v(tile + step, next);
     now = next;
     next = after;
   }

@@ -157,8 +157,8 @@ gdn_status_t norm_sizes(const gdn_norm_problem_t* p) {
 }
 
 size_t norm_parts_bytes(const gdn_norm_problem_t* p, int sums) {
-  const NormPlan plan = norm_plan(p->B, p->T, p->D, p->seq_offsets != nullptr, true);
-  return (size_t)plan.items * plan.rows * sums * p->D * 4;
+  const NormPlan plan = norm_plan(p->B, p->T, p->D, p->dtype == GDN_DTYPE_BF16, p->seq_offsets != nullptr, true);
+  return (size_t)plan.items * sums * p->D * 4;
 }
 
 gdn_status_t norm_call(const gdn_norm_problem_t* p, bool backward, const void* x, const void* y, const void* h,
@@ -228,8 +228,8 @@ gdn_status_t norm_call(const gdn_norm_problem_t* p, bool backward, const void* x
   a.x_st = st[0]; a.y_st = st[1]; a.h_st = st[2]; a.n_st = st[3]; a.dx_st = st[4]; a.dy_st = st[5];
   a.gate_sb = p->gate_stride_b; a.alpha = p->residual_scale; a.eps = p->eps;
   a.zero_unused = (p->options & GDN_LAYER_OPT_ZERO_UNUSED) != 0;
-  const NormPlan plan = norm_plan(B, T, D, off != nullptr, backward);
-  a.chunk = plan.chunk; a.chunks = plan.chunks; a.items = plan.items; a.rows = plan.rows;
+  const NormPlan plan = norm_plan(B, T, D, p->dtype == GDN_DTYPE_BF16, off != nullptr, backward);
+  a.chunk = plan.chunk; a.chunks = plan.chunks; a.items = plan.items;
   a.parts = static_cast<float*>(p->workspace);
   a.sums = sums; a.dgate = dgate; a.dpost = dpost; a.dweight = dweight;
   hipStream_t stream = static_cast<hipStream_t>(p->stream);

@@ -166,8 +166,7 @@ struct NormArgs {
   int64_t chunk;         // rows per workgroup
   int64_t chunks;        // workgroups per sequence (not packed)
   int64_t items;         // workgroups
-  int rows;              // rows of a workgroup at a time
-  // backward: the sums over a workgroup's rows [item][rows][sums][D], and where
+  // backward: the sums over a workgroup's rows [item][sums][D], and where
   // the gradients' sums go (null: not wanted)
   float* parts;
   int sums;
@@ -179,9 +178,8 @@ struct NormArgs {
 // How the rows of a seam are divided among workgroups.
 struct NormPlan {
   int64_t chunk, chunks, items;
-  int rows;  // rows of a workgroup at a time: partial sums it writes
 };
-NormPlan norm_plan(int64_t B, int64_t T, int64_t D, bool packed, bool backward);
+NormPlan norm_plan(int64_t B, int64_t T, int64_t D, bool half, bool packed, bool backward);
 
 // ---- launchers (host) ----
 template <typename MT>
@@ -237,6 +235,21 @@ __device__ __forceinline__ float softplus(float x) {
   p = fmaf(p, w, 0.66666317f);
   p = fmaf(p, w, 2.0f);
   return fmaf(s, p, fmaxf(x, 0.0f));
+}
+
+// Joins x over the four lane groups of sixteen, for every place in a group:
+// rows of 16 lanes are swapped by pairs, then the wave's halves.  (The swapped
+// words are copied before they are taken as floats: a bit cast of a vector's
+// element takes the first one.)
+template <typename Join>
+__device__ __forceinline__ float over_groups(float x, Join join) {
+  unsigned u = __builtin_bit_cast(unsigned, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned a = r[0], b = r[1];
+  u = __builtin_bit_cast(unsigned, join(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned c = s[0], d = s[1];
+  return join(__builtin_bit_cast(float, c), __builtin_bit_cast(float, d));
 }
 
 // Slot of sequence b, or -1 (no state): an index outside 0..slots-1 is no slot.

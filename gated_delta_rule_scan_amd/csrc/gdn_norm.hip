@@ -19,58 +19,98 @@
 namespace gdn {
 namespace {
 
-// Sum over a wave, in every lane.
+// Sum over a wave, in every lane: quads, eights and sixteens by row
+// permutations, then pairs of rows and the halves swapped.
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
-  return x;
+  auto add = [](float v, int moved) { return v + __builtin_bit_cast(float, moved); };
+  x = add(x, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0xB1, 0xF, 0xF, true));   // quad: 1 0 3 2
+  x = add(x, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x4E, 0xF, 0xF, true));   // quad: 2 3 0 1
+  x = add(x, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x141, 0xF, 0xF, true));  // half row mirrored
+  x = add(x, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x140, 0xF, 0xF, true));  // row mirrored
+  return over_groups(x, [](float a, float b) { return a + b; });
+}
+
+// Waves of a compute unit at a time, by registers and LDS.  A call has
+// workgroups for so many, so that all of them run from its start to its end.
+constexpr int waves_at_once(int waves, int E, size_t size, bool backward) {
+  if (waves == 16) return 16;
+  if (backward) return E == 16 ? 8 : 16;
+  return E == 16 ? (size == 4 ? 12 : 16) : 20;
 }
 
 // WAVES waves per row, E channels per lane in vectors of VEC.
 template <typename MT, int WAVES, int E, int VEC>
 struct Lanes {
-  static constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;  // rows of a workgroup at a time
+  static_assert(WAVES == 1 || WAVES >= 4, "waves that share a row have the workgroup's barriers to themselves");
+  static constexpr int kRows = WAVES == 1 ? 4 : 1;  // rows of a workgroup at a time
   static constexpr int kThreads = WAVES * kRows * 64;
-  static constexpr int kWidth = WAVES * 64 * E;
+  static constexpr int kAlign = VEC * sizeof(MT) < 16 ? VEC * sizeof(MT) : 16;
+  // a lane's channels of a row as they lie in memory: what is in flight for the next row
+  struct Raw {
+    MT v[E];
+  };
+  // whether a row's loads are under way while the one before is worked on
+  static constexpr bool kAhead = WAVES * 64 * E <= 8192;
   int64_t D;
   int col0;  // the lane's first channel
   float* red;
   int phase = 0;
+  mutable int sums_taken = 0;
 
   __device__ __forceinline__ int col(int v) const { return v * WAVES * 64 * VEC + col0; }
 
-  template <typename T>
-  __device__ __forceinline__ void load(const T* p, float (&x)[E]) const {
+  __device__ __forceinline__ void load(const MT* p, Raw& x) const {
 #pragma unroll
     for (int v = 0; v < E / VEC; ++v) {
-      T t[VEC];
-      if (col(v) < D) {
-        __builtin_memcpy(t, __builtin_assume_aligned(p + col(v), VEC * sizeof(T) < 16 ? VEC * sizeof(T) : 16), sizeof(t));
+      // (rows are read once: with the hint for that the backward call of 32760 x 2048 took 160 us, without 175)
+      typedef MT vec __attribute__((ext_vector_type(VEC), aligned(kAlign)));
+      vec q = (vec)(MT)0.0f;
+      if (col(v) < D) q = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p + col(v)));
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[v * VEC + e] = (float)t[e];
+      for (int e = 0; e < VEC; ++e) x.v[v * VEC + e] = q[e];
+    }
+  }
+  static __device__ __forceinline__ void open(const Raw& r, float (&x)[E]) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = (float)r.v[i];
+  }
+  // The parameters g, wp and w, ones where they are not given.  Up to 8192
+  // channels they are loaded once: the forward kernel keeps them in registers,
+  // the backward one, which has sums there, in LDS (in LDS the forward call of
+  // 65520 x 2048 took 215 us, in registers 194).
+  static constexpr bool kOnce = WAVES * 64 * E <= 8192;
+  __device__ __forceinline__ void param(const float* p, float (&x)[E]) const {
+#pragma unroll
+    for (int v = 0; v < E / VEC; ++v) {
+      if (p && col(v) < D) {
+        __builtin_memcpy(x + v * VEC, p + col(v), VEC * 4);
       } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[v * VEC + e] = 0.0f;
+        for (int e = 0; e < VEC; ++e) x[v * VEC + e] = 1.0f;
       }
     }
   }
-  // parameters: fp32, aligned to their type only
-  __device__ __forceinline__ void param(const float* p, float (&x)[E], float none) const {
+  static constexpr int kStage = kOnce ? WAVES * 64 * E : 4;
+  __device__ __forceinline__ void stage(const float* p, float* to) const {
+    if constexpr (kOnce)
+      for (int i = threadIdx.x; i < kStage; i += kThreads) to[i] = p && i < D ? p[i] : 1.0f;
+  }
+  __device__ __forceinline__ void param(const float* p, const float* staged, float (&x)[E]) const {
+    if constexpr (!kOnce) return param(p, x);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = col(i / VEC) + i % VEC;
-      x[i] = p && c < D ? p[c] : none;
-    }
+    for (int v = 0; v < E / VEC; ++v)
+      __builtin_memcpy(x + v * VEC, __builtin_assume_aligned(staged + col(v), VEC * 4 < 16 ? VEC * 4 : 16), VEC * 4);
   }
   template <typename T>
   __device__ __forceinline__ void store(T* p, const float (&x)[E]) const {
+    constexpr int kTo = VEC * sizeof(T) < 16 ? VEC * sizeof(T) : 16;
 #pragma unroll
     for (int v = 0; v < E / VEC; ++v) {
       if (col(v) >= D) continue;
       T t[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) t[e] = (T)x[v * VEC + e];
-      __builtin_memcpy(__builtin_assume_aligned(p + col(v), VEC * sizeof(T) < 16 ? VEC * sizeof(T) : 16), t, sizeof(t));
+      __builtin_memcpy(__builtin_assume_aligned(p + col(v), sizeof(T) == 4 && sizeof(MT) != 4 ? 4 : kTo), t, sizeof(t));
     }
   }
   // K sums over the row, in all its lanes.  Several waves join theirs in LDS;
@@ -96,142 +136,221 @@ struct Lanes {
   }
 };
 
-// The rows of a workgroup: a run of one sequence's, or rows of no sequence.
-struct Run {
-  SeqItem s;
-  int64_t t0, t1;   // rows of the run
-  int64_t limit;    // ... with those behind the last sequence
+// A lane's sums over rows: in registers, or (the widest rows) in LDS, where
+// each lane has places of its own.
+template <typename L, int E, bool REGISTERS>
+struct Sum {
+  float x[E];
+  __device__ __forceinline__ explicit Sum(const L&) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = 0.0f;
+  }
+  __device__ __forceinline__ void add(const float (&y)[E]) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] += y[i];
+  }
+  __device__ __forceinline__ void get(float (&y)[E]) const {
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] = x[i];
+  }
+};
+template <typename L, int E>
+struct Sum<L, E, false> {
+  f32x4* at;
+  __device__ __forceinline__ explicit Sum(const L& lanes) {
+    __shared__ f32x4 places[2 * (E / 4) * L::kThreads];  // (of dgate and dpost)
+    at = places + lanes.sums_taken * (E / 4 * L::kThreads) + threadIdx.x;
+    ++lanes.sums_taken;
+#pragma unroll
+    for (int v = 0; v < E / 4; ++v) at[v * L::kThreads] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void add(const float (&y)[E]) {
+#pragma unroll
+    for (int v = 0; v < E / 4; ++v) at[v * L::kThreads] += f32x4{y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]};
+  }
+  __device__ __forceinline__ void get(float (&y)[E]) const {
+#pragma unroll
+    for (int v = 0; v < E / 4; ++v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[4 * v + e] = at[v * L::kThreads][e];
+  }
 };
 
-__device__ __forceinline__ Run run_of(const NormArgs& a) {
-  Run r;
+// The rows of a workgroup: of a sequence that is cut into n runs, run i takes
+// rows i, i + n, i + 2n, ... (R neighbouring ones in a row's place, where R are
+// taken at a time), so that the workgroups of a call read side by side; runs of
+// neighbouring rows start at distances that may all fall on the same memory
+// channels (32 rows of 4096 bytes a run, forward: 255 us against 248).  Rows of no
+// sequence lie behind the last one's, `chunk` of them a run.
+struct Run {
+  int64_t b, row0, len;   // the sequence, its first row and rows
+  int64_t t, step;        // the first row of this lane's, and the distance of the others
+  int64_t u0, u1;         // rows of no sequence
+};
+
+template <int R>
+__device__ __forceinline__ Run run_of(const NormArgs& a, int sub) {
+  SeqItem s;
   if (a.off) {
-    r.s = find_packed(a.off, a.B, a.T, a.chunk, blockIdx.x);
+    s = find_packed(a.off, a.B, a.T, a.chunk, blockIdx.x);
   } else {
-    r.s.b = blockIdx.x / a.chunks;
-    r.s.chunk = blockIdx.x % a.chunks;
-    r.s.row0 = 0;
-    r.s.len = a.T;
+    s.b = blockIdx.x / a.chunks;
+    s.chunk = blockIdx.x % a.chunks;
+    s.row0 = 0;
+    s.len = a.T;
   }
-  const int64_t all = a.off && a.zero_unused && r.s.b == a.B - 1 ? a.T - r.s.row0 : r.s.len;
-  r.t0 = r.s.chunk * a.chunk;
-  r.t1 = r.t0 + a.chunk < r.s.len ? r.t0 + a.chunk : r.s.len;
-  r.limit = r.t0 + a.chunk < all ? r.t0 + a.chunk : all;
+  Run r;
+  r.b = s.b;
+  r.row0 = s.row0;
+  r.len = s.len;
+  const int64_t runs = (s.len + a.chunk - 1) / a.chunk;
+  r.t = s.chunk < runs ? s.chunk * R + sub : s.len;
+  r.step = runs * R;
+  const int64_t all = a.off && a.zero_unused && s.b == a.B - 1 ? a.T - s.row0 : s.len;
+  r.u0 = s.chunk * a.chunk > s.len ? s.chunk * a.chunk : s.len;
+  r.u1 = (s.chunk + 1) * a.chunk < all ? (s.chunk + 1) * a.chunk : all;
   return r;
 }
 
 template <typename MT, int WAVES, int E, int VEC>
-__global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads)) void norm_kernel(NormArgs a) {
+__global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_once(WAVES, E, sizeof(MT), false) / 4)) void norm_kernel(NormArgs a) {
   typedef Lanes<MT, WAVES, E, VEC> L;
   __shared__ float red[4 * WAVES];
   const int sub = L::kRows > 1 ? threadIdx.x / (64 * WAVES) : 0;
   L lanes{a.D, (int)(threadIdx.x % (64 * WAVES)) * VEC, red};
-  const Run r = run_of(a);
-  if (r.t0 >= r.limit) return;
+  const Run r = run_of<L::kRows>(a, sub);
+  const int64_t b = a.off ? 0 : r.b;
+  const MT* x_rows = static_cast<const MT*>(a.x) + b * a.x_sb;
+  const MT* y_rows = static_cast<const MT*>(a.y) + b * a.y_sb;
+  MT* h_rows = static_cast<MT*>(a.h) + b * a.h_sb;
+  MT* n_rows = static_cast<MT*>(a.n) + b * a.n_sb;
+  // the next row's loads are under way while this one's sums are taken
+  typename L::Raw rx, ry;
+  int64_t t = r.t;
+  if (t < r.len) {
+    lanes.load(x_rows + (r.row0 + t) * a.x_st, rx);
+    if (a.y) lanes.load(y_rows + (r.row0 + t) * a.y_st, ry);
+  }
   const float inv_d = 1.0f / (float)a.D;
-  float g[E], pw[E], w[E];
-  lanes.param(a.gate ? a.gate + r.s.b * a.gate_sb : nullptr, g, 1.0f);
-  lanes.param(a.post, pw, 1.0f);
-  lanes.param(a.weight, w, 1.0f);
-  for (int64_t t = r.t0 + sub; t < r.limit; t += L::kRows) {
-    const int64_t row = r.s.row0 + t, b = a.off ? 0 : r.s.b;
-    float x[E], y[E];
-    MT* h = static_cast<MT*>(a.h) + b * a.h_sb + row * a.h_st;
-    MT* n = static_cast<MT*>(a.n) + b * a.n_sb + row * a.n_st;
-    if (t >= r.t1) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = 0.0f;
-      if (a.h) lanes.store(h, x);
-      if (a.n) lanes.store(n, x);
-      continue;
-    }
-    lanes.load(static_cast<const MT*>(a.x) + b * a.x_sb + row * a.x_st, x);
+  const float* gate = a.gate ? a.gate + r.b * a.gate_sb : nullptr;
+  float x[E], y[E], g[E], pw[E], w[E];
+  if (L::kOnce) {
+    lanes.param(gate, g);
+    lanes.param(a.post, pw);
+    lanes.param(a.weight, w);
+  }
+  for (; t < r.len; t += r.step) {
+    const int64_t row = r.row0 + t;
+    L::open(rx, x);
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] *= a.alpha;
+    if (a.y) L::open(ry, y);
+    if (t + r.step < r.len) {
+      lanes.load(x_rows + (row + r.step) * a.x_st, rx);
+      if (a.y) lanes.load(y_rows + (row + r.step) * a.y_st, ry);
+    }
+    asm volatile("" ::: "memory");  // (the loads are issued here, not where they are used)
     if (a.y) {
-      lanes.load(static_cast<const MT*>(a.y) + b * a.y_sb + row * a.y_st, y);
       if (a.post) {
         float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < E; ++i) s[0] = fmaf(y[i], y[i], s[0]);
         lanes.sum(s);
-        const float ry = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
+        const float inv = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
+        if (!L::kOnce) lanes.param(a.post, pw);
 #pragma unroll
-        for (int i = 0; i < E; ++i) y[i] *= ry * pw[i];
+        for (int i = 0; i < E; ++i) y[i] *= inv * pw[i];
       }
+      if (!L::kOnce) lanes.param(gate, g);
 #pragma unroll
       for (int i = 0; i < E; ++i) x[i] = fmaf(g[i], y[i], x[i]);
     }
-    if (a.h) lanes.store(h, x);
+    if (a.h) lanes.store(h_rows + row * a.h_st, x);
     if (a.n) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < E; ++i) s[0] = fmaf(x[i], x[i], s[0]);
       lanes.sum(s);
-      const float rh = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
+      const float inv = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
+      if (!L::kOnce) lanes.param(a.weight, w);
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] *= rh * w[i];
-      lanes.store(n, x);
+      for (int i = 0; i < E; ++i) x[i] *= inv * w[i];
+      lanes.store(n_rows + row * a.n_st, x);
     }
+  }
+  // rows of no sequence
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = 0.0f;
+  for (t = r.u0 + sub; t < r.u1; t += L::kRows) {
+    if (a.h) lanes.store(h_rows + (r.row0 + t) * a.h_st, x);
+    if (a.n) lanes.store(n_rows + (r.row0 + t) * a.n_st, x);
   }
 }
 
 template <typename MT, int WAVES, int E, int VEC>
-__global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads)) void norm_back_kernel(NormArgs a) {
+__global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_once(WAVES, E, sizeof(MT), true) / 4)) void norm_back_kernel(NormArgs a) {
   typedef Lanes<MT, WAVES, E, VEC> L;
   __shared__ float red[4 * WAVES];
   const int sub = L::kRows > 1 ? threadIdx.x / (64 * WAVES) : 0;
   L lanes{a.D, (int)(threadIdx.x % (64 * WAVES)) * VEC, red};
-  const Run r = run_of(a);
+  const Run r = run_of<L::kRows>(a, sub);
+  const int64_t b = a.off ? 0 : r.b;
+  const MT* x_rows = static_cast<const MT*>(a.x) + b * a.x_sb;
+  const MT* y_rows = static_cast<const MT*>(a.y) + b * a.y_sb;
+  const MT* dh_rows = static_cast<const MT*>(a.h) + b * a.h_sb;
+  const MT* dn_rows = static_cast<const MT*>(a.n) + b * a.n_sb;
+  MT* dx_rows = static_cast<MT*>(a.dx) + b * a.dx_sb;
+  MT* dy_rows = static_cast<MT*>(a.dy) + b * a.dy_sb;
+  typename L::Raw rx, ry, rdh, rdn;
+  auto load = [&](int64_t row) {
+    lanes.load(x_rows + row * a.x_st, rx);
+    if (a.y) lanes.load(y_rows + row * a.y_st, ry);
+    if (a.h) lanes.load(dh_rows + row * a.h_st, rdh);
+    if (a.n) lanes.load(dn_rows + row * a.n_st, rdn);
+  };
+  int64_t t = r.t;
+  if (t < r.len) load(r.row0 + t);
   const float inv_d = 1.0f / (float)a.D;
-  float g[E], pw[E], w[E], dg[E], dpw[E], dw[E];
-  lanes.param(a.gate ? a.gate + r.s.b * a.gate_sb : nullptr, g, 1.0f);
-  lanes.param(a.post, pw, 1.0f);
-  lanes.param(a.weight, w, 1.0f);
+  const float* gate = a.gate ? a.gate + r.b * a.gate_sb : nullptr;
+  __shared__ __align__(16) float params[3][L::kStage];
+  lanes.stage(gate, params[0]);
+  lanes.stage(a.post, params[1]);
+  lanes.stage(a.weight, params[2]);
+  __syncthreads();
+  float g[E], pw[E], dw[E];
+  Sum<L, E, L::kOnce> dg(lanes), dpw(lanes);
 #pragma unroll
-  for (int i = 0; i < E; ++i) dg[i] = dpw[i] = dw[i] = 0.0f;
-  for (int64_t t = r.t0 + sub; t < r.limit; t += L::kRows) {
-    const int64_t row = r.s.row0 + t, b = a.off ? 0 : r.s.b;
-    MT* dx = static_cast<MT*>(a.dx) + b * a.dx_sb + row * a.dx_st;
-    MT* dy = static_cast<MT*>(a.dy) + b * a.dy_sb + row * a.dy_st;
-    float h[E], y[E], u[E], d[E], dn[E];
-    if (t >= r.t1) {
+  for (int i = 0; i < E; ++i) dw[i] = 0.0f;
+  for (; t < r.len; t += r.step) {
+    const int64_t row = r.row0 + t;
+    asm volatile("" ::: "memory");  // (parameters are not kept in registers over the rows)
+    float h[E], y[E], d[E], dn[E];
+    if (!L::kAhead && t != r.t) load(row);
+    L::open(rx, h);
 #pragma unroll
-      for (int i = 0; i < E; ++i) d[i] = 0.0f;
-      if (a.dx) lanes.store(dx, d);
-      if (a.dy) lanes.store(dy, d);
-      continue;
-    }
-    lanes.load(static_cast<const MT*>(a.x) + b * a.x_sb + row * a.x_st, h);
-    if (a.y) {
-      lanes.load(static_cast<const MT*>(a.y) + b * a.y_sb + row * a.y_st, y);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) y[i] = 0.0f;
-    }
-    if (a.h) {
-      lanes.load(static_cast<const MT*>(a.h) + b * a.h_sb + row * a.h_st, d);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) d[i] = 0.0f;
-    }
-    float ry = 1.0f;
+    for (int i = 0; i < E; ++i) y[i] = d[i] = dn[i] = 0.0f;
+    if (a.y) L::open(ry, y);
+    if (a.h) L::open(rdh, d);
+    if (a.n) L::open(rdn, dn);
+    if (L::kAhead && t + r.step < r.len) load(row + r.step);
+    float ry_ = 1.0f;
     if (a.post) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < E; ++i) s[0] = fmaf(y[i], y[i], s[0]);
       lanes.sum(s);
-      ry = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
+      ry_ = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
     }
+    lanes.param(gate, params[0], g);
+    lanes.param(a.post, params[1], pw);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      y[i] *= ry;            // y^ (without a norm: y)
-      u[i] = y[i] * pw[i];
-      h[i] = fmaf(g[i], u[i], a.alpha * h[i]);
+      y[i] *= ry_;  // y^ (without a norm: y)
+      h[i] = fmaf(g[i], y[i] * pw[i], a.alpha * h[i]);
     }
     if (a.n) {
-      lanes.load(static_cast<const MT*>(a.n) + b * a.n_sb + row * a.n_st, dn);
-      float s[2] = {0.0f, 0.0f};
+      float s[2] = {0.0f, 0.0f}, w[E];
+      lanes.param(a.weight, params[2], w);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         s[0] = fmaf(h[i], h[i], s[0]);
@@ -250,41 +369,72 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads)) void norm_bac
     if (a.dx) {
 #pragma unroll
       for (int i = 0; i < E; ++i) h[i] = a.alpha * d[i];
-      lanes.store(dx, h);
+      lanes.store(dx_rows + row * a.dx_st, h);
     }
     if (!a.y) continue;
+    asm volatile("" ::: "memory");  // (nor over the sums before)
+    lanes.param(gate, params[0], g);
+    lanes.param(a.post, params[1], pw);
+    float u[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      dg[i] = fmaf(d[i], u[i], dg[i]);
+      u[i] = d[i] * (y[i] * pw[i]);
       d[i] *= g[i];
     }
+    if (a.dgate) dg.add(u);
     if (a.post) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        dpw[i] = fmaf(d[i], y[i], dpw[i]);
+        u[i] = d[i] * y[i];
         d[i] *= pw[i];
         s[0] = fmaf(d[i], y[i], s[0]);
       }
+      if (a.dpost) dpw.add(u);
       lanes.sum(s);
       const float c = s[0] * inv_d;
 #pragma unroll
-      for (int i = 0; i < E; ++i) d[i] = ry * fmaf(-y[i], c, d[i]);
+      for (int i = 0; i < E; ++i) d[i] = ry_ * fmaf(-y[i], c, d[i]);
     }
-    if (a.dy) lanes.store(dy, d);
+    if (a.dy) lanes.store(dy_rows + row * a.dy_st, d);
   }
-  // the sums over these rows: zero where the run is empty
-  float* part = a.parts + (blockIdx.x * (int64_t)L::kRows + sub) * a.sums * a.D;
-  auto put = [&](const float (&x)[E]) {
+  float u[E];
+  // rows of no sequence
+  float zero[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = lanes.col(i / VEC) + i % VEC;
-      if (c < a.D) part[c] = x[i];
+  for (int i = 0; i < E; ++i) zero[i] = 0.0f;
+  for (t = r.u0 + sub; t < r.u1; t += L::kRows) {
+    if (a.dx) lanes.store(dx_rows + (r.row0 + t) * a.dx_st, zero);
+    if (a.dy) lanes.store(dy_rows + (r.row0 + t) * a.dy_st, zero);
+  }
+  // the sums over these rows: zero where the run is empty.  Rows that were
+  // taken side by side are added first.
+  float* part = a.parts + blockIdx.x * (int64_t)a.sums * a.D;
+  auto put = [&](float (&x)[E]) {
+    if constexpr (L::kRows > 1) {
+      __shared__ float side[L::kRows - 1][E * 64 * WAVES];
+      __syncthreads();
+      if (sub > 0)
+#pragma unroll
+        for (int i = 0; i < E; ++i) side[sub - 1][i * 64 * WAVES + threadIdx.x % (64 * WAVES)] = x[i];
+      __syncthreads();
+      if (sub == 0)
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+#pragma unroll
+          for (int k = 0; k < L::kRows - 1; ++k) x[i] += side[k][i * 64 * WAVES + threadIdx.x];
     }
+    if (sub == 0) lanes.store(part, x);
     part += a.D;
   };
-  if (a.dgate) put(dg);
-  if (a.dpost) put(dpw);
+  if (a.dgate) {
+    dg.get(u);
+    put(u);
+  }
+  if (a.dpost) {
+    dpw.get(u);
+    put(u);
+  }
   if (a.dweight) put(dw);
 }
 
@@ -318,11 +468,21 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a) {
     kind = (a.dgate ? 1 : 0) + (int)which;
     to = which == 0 && a.dpost ? a.dpost : a.dweight;
   }
-  first *= a.rows;
-  last *= a.rows;
+  // (sixteen loads under way at a time: the sum is a chain of their latencies)
   float s = 0.0f;
-  if (c < a.D)
-    for (int64_t p = first + wave; p < last; p += 16) s += a.parts[(p * a.sums + kind) * a.D + c];
+  if (c < a.D) {
+    const float* from = a.parts + kind * a.D + c;
+    const int64_t step = a.sums * a.D;
+    int64_t p = first + wave;
+    for (; p + 15 * 16 < last; p += 16 * 16) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = from[(p + 16 * i) * step];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s += v[i];
+    }
+    for (; p < last; p += 16) s += from[p * step];
+  }
   red[wave][lane] = s;
   __syncthreads();
   if (wave != 0 || c >= a.D) return;
@@ -332,43 +492,53 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a) {
   to[c] = s;
 }
 
-// rows of a workgroup at a time, by the channels
-int rows_at_once(int64_t D) { return D <= 1024 ? 4 : 1; }
+// A row's waves and a lane's channels, by the row's width.
+struct Width {
+  int64_t D;
+  int waves, E;
+};
+template <bool BACKWARD>
+constexpr Width kWidths[] = {{256, 1, 4},
+                             {512, 1, 8},
+                             {1024, 1, 16},
+                             {2048, 4, 8},
+                             {4096, BACKWARD ? 8 : 4, BACKWARD ? 8 : 16},
+                             {8192, BACKWARD ? 16 : 8, BACKWARD ? 8 : 16},
+                             {16384, 16, 16}};
 
-template <typename MT, int WAVES, int E, int VEC>
-hipError_t norm_launch(const NormArgs& a, bool backward, hipStream_t stream) {
-  typedef Lanes<MT, WAVES, E, VEC> L;
-  if (!grid_fits(a.items, L::kThreads)) return hipErrorNotSupported;
-  if (backward)
-    hipLaunchKernelGGL((norm_back_kernel<MT, WAVES, E, VEC>), dim3((unsigned)a.items), dim3(L::kThreads), 0, stream, a);
+template <typename MT, int VEC, bool BACKWARD, int I = 0>
+hipError_t norm_by_width(const NormArgs& a, hipStream_t stream) {
+  constexpr Width w = kWidths<BACKWARD>[I];
+  if constexpr (w.D < 16384)
+    if (a.D > w.D) return norm_by_width<MT, VEC, BACKWARD, I + 1>(a, stream);
+  constexpr int kVec = VEC < w.E ? VEC : w.E;
+  constexpr int kThreads = Lanes<MT, w.waves, w.E, kVec>::kThreads;
+  if (!grid_fits(a.items, kThreads)) return hipErrorNotSupported;
+  if constexpr (BACKWARD)
+    hipLaunchKernelGGL((norm_back_kernel<MT, w.waves, w.E, kVec>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
   else
-    hipLaunchKernelGGL((norm_kernel<MT, WAVES, E, VEC>), dim3((unsigned)a.items), dim3(L::kThreads), 0, stream, a);
+    hipLaunchKernelGGL((norm_kernel<MT, w.waves, w.E, kVec>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
-template <typename MT, int VEC>
-hipError_t norm_by_width(const NormArgs& a, bool backward, hipStream_t stream) {
-  if (a.D <= 512) return norm_launch<MT, 1, 8, VEC>(a, backward, stream);
-  if (a.D <= 1024) return norm_launch<MT, 1, 16, VEC>(a, backward, stream);
-  if (a.D <= 2048) return norm_launch<MT, 4, 8, VEC>(a, backward, stream);
-  if (a.D <= 4096) return norm_launch<MT, 4, 16, VEC>(a, backward, stream);
-  if (a.D <= 8192) return norm_launch<MT, 16, 8, VEC>(a, backward, stream);
-  return norm_launch<MT, 16, 16, VEC>(a, backward, stream);
-}
-
-template <typename MT>
-hipError_t norm_for(const NormArgs& a, bool aligned, bool backward, hipStream_t stream) {
-  return aligned ? norm_by_width<MT, 16 / sizeof(MT)>(a, backward, stream) : norm_by_width<MT, 1>(a, backward, stream);
+template <typename MT, bool BACKWARD>
+hipError_t norm_for(const NormArgs& a, bool aligned, hipStream_t stream) {
+  return aligned ? norm_by_width<MT, 16 / sizeof(MT), BACKWARD>(a, stream) : norm_by_width<MT, 1, BACKWARD>(a, stream);
 }
 
 }  // namespace
 
-NormPlan norm_plan(int64_t B, int64_t T, int64_t D, bool packed, bool backward) {
+NormPlan norm_plan(int64_t B, int64_t T, int64_t D, bool half, bool packed, bool backward) {
   NormPlan p;
-  // rows a workgroup: many enough that its parameters and partial sums cost
-  // little beside them, with workgroups enough for every compute unit
-  const int64_t at_once = p.rows = rows_at_once(D), workgroups = backward ? 1024 : 2048;
+  const Width* widths = backward ? kWidths<true> : kWidths<false>;
+  while (D > widths->D && widths->D < 16384) ++widths;
+  const Width& w = *widths;
+  const int64_t at_once = w.waves == 1 ? 4 : 1;
+  int64_t workgroups = 256 * (waves_at_once(w.waves, w.E, half ? 2 : 4, backward) / (w.waves * at_once));
+  if (workgroups < 256) workgroups = 256;
   const int64_t rows = packed ? T : B * T;
+  // (a packed batch has up to a workgroup a sequence more)
+  if (packed) workgroups = B < workgroups / 2 ? workgroups - B : workgroups / 2;
   p.chunk = (rows + workgroups - 1) / workgroups;
   p.chunk = (p.chunk + at_once - 1) / at_once * at_once;
   if (p.chunk < at_once) p.chunk = at_once;
@@ -379,13 +549,13 @@ NormPlan norm_plan(int64_t B, int64_t T, int64_t D, bool packed, bool backward) 
 
 template <typename MT>
 hipError_t launch_norm(const NormArgs& a, bool aligned, hipStream_t stream) {
-  return a.items ? norm_for<MT>(a, aligned, false, stream) : hipSuccess;
+  return a.items ? norm_for<MT, false>(a, aligned, stream) : hipSuccess;
 }
 
 template <typename MT>
 hipError_t launch_norm_back(const NormArgs& a, bool aligned, hipStream_t stream) {
   if (a.items) {
-    const hipError_t e = norm_for<MT>(a, aligned, true, stream);
+    const hipError_t e = norm_for<MT, true>(a, aligned, stream);
     if (e != hipSuccess) return e;
   }
   const int64_t outs = (a.dgate ? (a.gate_sb ? a.B : 1) : 0) + (a.dpost ? 1 : 0) + (a.dweight ? 1 : 0);
