@@ -136,12 +136,11 @@ __device__ __forceinline__ float over_groups_sum(float x) {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// N words of a pool, aligned to `A` bytes.  Read once and not kept: the hint
-// for that (non-temporal) is worth a tenth and more of the rate here.
-template <int N, int A>
+// N words of a pool, aligned to `A` bytes, read ONCE (see fetch) or not.
+template <int N, int A, bool ONCE>
 __device__ __forceinline__ void words(const uint8_t* p, unsigned (&w)[N]) {
   typedef unsigned vec __attribute__((ext_vector_type(N), aligned(A)));
-  const vec v = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p));
+  const vec v = fetch<ONCE>(reinterpret_cast<const vec*>(p));
 #pragma unroll
   for (int i = 0; i < N; ++i) w[i] = v[i];
 }
@@ -189,7 +188,7 @@ struct Shape {
   }
 };
 
-template <typename MT, int FORMAT, int D, int QT>
+template <typename MT, int FORMAT, int D, int QT, bool ONCE>
 __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
   typedef Shape<FORMAT, D> F;
   constexpr bool kWide = F::kWide, kCodes = F::kCodes;
@@ -235,8 +234,8 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
 #pragma unroll
       for (int m = 0; m < D / 32; ++m) {
         float x[8];
-        if (a.q_aligned) load8<MT, true>(q + F::channel(m, g), x);
-        else load8<MT, false>(q + F::channel(m, g), x);
+        if (a.q_aligned) load8<MT, true, false>(q + F::channel(m, g), x);
+        else load8<MT, false, false>(q + F::channel(m, g), x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float rest = mine ? x[e] : 0.0f;
@@ -287,11 +286,11 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
       const uint8_t* base = pools[0] + row * F::kRow;
 #pragma unroll
       for (int j = 0; j < F::kLoads; ++j)
-        words<F::kLoadWords, F::kLoadWords * 4>(base + k_off + j * (4 * F::kRun * F::kBits / 8), kw[s][j]);
+        words<F::kLoadWords, F::kLoadWords * 4, ONCE>(base + k_off + j * (4 * F::kRun * F::kBits / 8), kw[s][j]);
       if constexpr (kCodes) {
         const uint8_t* scales = a.k_scales + row * F::kBlocks;
         if constexpr (F::kBlocks == 2) ksw[s][0] = *reinterpret_cast<const uint16_t*>(scales + n * 2);
-        else words<F::kBlocks / 4, 4>(scales + n * F::kBlocks, ksw[s]);
+        else words<F::kBlocks / 4, 4, ONCE>(scales + n * F::kBlocks, ksw[s]);
       }
     }
   };
@@ -306,10 +305,10 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
         for (int j = 0; j < F::kPieces; ++j) {
           const uint8_t* at = base + v_off + i * F::kRow + j * 16 * F::kPieceBytes;
           if constexpr (F::kPieceBytes == 2) vw[4 * s + i][j][0] = *reinterpret_cast<const uint16_t*>(at);
-          else words<F::kPieceWords, F::kPieceBytes>(at, vw[4 * s + i][j]);
+          else words<F::kPieceWords, F::kPieceBytes, ONCE>(at, vw[4 * s + i][j]);
         }
       // the scale bytes of tokens 4g .. 4g + 3
-      if constexpr (kCodes) words<F::kBlocks, 4>(a.v_scales + (row + 4 * g) * F::kBlocks, vsw[s]);
+      if constexpr (kCodes) words<F::kBlocks, 4, ONCE>(a.v_scales + (row + 4 * g) * F::kBlocks, vsw[s]);
     }
   };
 
@@ -615,7 +614,10 @@ hipError_t attend_launch(const AttendArgs& a, hipStream_t stream) {
   const int64_t shares = (a.Hq / a.Hk + 16 * QT - 1) / (16 * QT);
   const int64_t blocks = a.items * a.Hk * shares;
   if (!grid_fits(blocks, kWaves * 64) || !grid_fits(a.B * a.Hq, kWaves * 64)) return hipErrorNotSupported;
-  hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
+  if (a.once)
+    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, true>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
+  else
+    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, false>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.plan) return e;
   hipLaunchKernelGGL((join_kernel<MT, D>), dim3((unsigned)(a.B * a.Hq)), dim3(kWaves * 64), 0, stream, a);
@@ -665,7 +667,11 @@ AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, int64_t rea
 }
 
 template <typename MT>
-hipError_t launch_attend(const AttendArgs& a, int format, hipStream_t stream) {
+hipError_t launch_attend(const AttendArgs& given, int format, hipStream_t stream) {
+  AttendArgs a = given;
+  // (what can be visible: how much is, only the device knows)
+  const int64_t reach = a.width << a.page_bits, tokens = a.window && a.window + a.sinks < reach ? a.window + a.sinks : reach;
+  a.once = 2 * a.B * tokens >= kOnceBytes / (a.Hk * row_bytes(format, a.d));
   switch (format) {
     case GDN_KV_MXFP8: return attend_for<MT, GDN_KV_MXFP8>(a, stream);
     case GDN_KV_MXFP4: return attend_for<MT, GDN_KV_MXFP4>(a, stream);

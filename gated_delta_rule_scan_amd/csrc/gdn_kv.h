@@ -99,18 +99,35 @@ __device__ __forceinline__ void decode8(const unsigned (&w)[2], float scale, flo
   }
 }
 
-// Eight channels of rows in memory (not a pool), whole vectors or one by one.
-template <typename MT, bool ALIGNED>
+// A vector that is read `once`: non-temporal.  That is faster where the data
+// comes from memory (%s) and slower where it waits in the cache (%s), so a
+// call that reads less than kOnceBytes of a cache does without.
+constexpr int64_t kOnceBytes = (int64_t)64 << 20;
+template <bool ONCE, typename T>
+__device__ __forceinline__ T fetch(const T* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+
+inline int64_t row_bytes(int format, int d) {
+  return format == GDN_KV_F32 ? 4 * d : format == GDN_KV_BF16 ? 2 * d : (format == GDN_KV_MXFP8 ? d : d / 2) + d / 32;
+}
+
+// Eight channels of a row, in whole vectors or one by one.
+template <typename MT, bool ALIGNED, bool ONCE>
 __device__ __forceinline__ void load8(const MT* p, float (&x)[8]) {
-  MT v[8];
   if constexpr (ALIGNED) {
-    __builtin_memcpy(v, __builtin_assume_aligned(p, 16), sizeof(v));
+    typedef MT vec __attribute__((ext_vector_type(16 / sizeof(MT))));
+#pragma unroll
+    for (int i = 0; i < 8; i += 16 / sizeof(MT)) {
+      const vec v = fetch<ONCE>(reinterpret_cast<const vec*>(p + i));
+#pragma unroll
+      for (int e = 0; e < (int)(16 / sizeof(MT)); ++e) x[i + e] = (float)v[e];
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = p[i];
+    for (int i = 0; i < 8; ++i) x[i] = (float)p[i];
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
 }
 
 template <typename MT, bool ALIGNED>
@@ -127,18 +144,19 @@ __device__ __forceinline__ void store8(MT* p, const float (&x)[8]) {
 }
 
 // Eight channels from 8 * c on of row `row` of a pool, as floats.
-template <typename MT, int FORMAT>
+template <typename MT, int FORMAT, bool ONCE>
 __device__ __forceinline__ void pool8(const void* pool, const uint8_t* scales, int64_t row, int d, int c, float (&x)[8]) {
   if constexpr (FORMAT == GDN_KV_F32 || FORMAT == GDN_KV_BF16) {
-    load8<MT, true>(static_cast<const MT*>(pool) + row * d + 8 * c, x);
+    load8<MT, true, ONCE>(static_cast<const MT*>(pool) + row * d + 8 * c, x);
   } else {
     unsigned w[2];
     if constexpr (FORMAT == GDN_KV_MXFP8) {
-      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + row * d + 8 * c);
-      w[0] = v.x;
-      w[1] = v.y;
+      typedef unsigned vec __attribute__((ext_vector_type(2)));
+      const vec v = fetch<ONCE>(reinterpret_cast<const vec*>(static_cast<const uint8_t*>(pool) + row * d + 8 * c));
+      w[0] = v[0];
+      w[1] = v[1];
     } else {
-      w[0] = *reinterpret_cast<const unsigned*>(static_cast<const uint8_t*>(pool) + row * (d / 2) + 4 * c);
+      w[0] = fetch<ONCE>(reinterpret_cast<const unsigned*>(static_cast<const uint8_t*>(pool) + row * (d / 2) + 4 * c));
       w[1] = 0;
     }
     decode8<FORMAT>(w, kv_scale(scales[row * (d / 32) + c / 4]), x);

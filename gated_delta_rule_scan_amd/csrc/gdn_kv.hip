@@ -3,92 +3,146 @@
 // A copy, with a block's scale and codes in between where the cache has 8 or 4
 // bits: memory-bound on both sides.  A thread moves eight channels of K and the
 // same of V; four neighbouring lanes hold a block of 32 channels.  A workgroup
-// takes a run of one sequence's tokens, all heads: on the rows' side that is
-// one contiguous piece, in the pools a piece of a page for every head.
+// takes 16 tokens of a few heads, head by head: rows in 8 or 4 bits are parts
+// of cache lines, and a wave's lie beside each other in the pool.
 #include "gdn_kv.h"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAtOnce = 2;     // places a thread has under way
+constexpr int kPlaces = 2;     // ... and in all
+constexpr int kTokenBits = 4;  // tokens of a workgroup
 
-template <typename MT, int FORMAT, bool WRITE, bool ALIGNED>
+// The scale bytes of a row, which every fourth lane holds, gathered in the
+// row's first lane of eight (two bytes) or of each sixteen (four): a lane's
+// value from 4, 8 and 12 lanes further in its row of 16.
+__device__ __forceinline__ unsigned two_bytes(unsigned s) {
+  return s | (unsigned)__builtin_amdgcn_mov_dpp((int)s, 0x104, 0xF, 0xF, true) << 8;
+}
+__device__ __forceinline__ unsigned four_bytes(unsigned s) {
+  const unsigned w = two_bytes(s);
+  return w | (unsigned)__builtin_amdgcn_mov_dpp((int)w, 0x108, 0xF, 0xF, true) << 16;
+}
+
+// ONCE: pools are read past the caches (see fetch)
+template <typename MT, int FORMAT, bool WRITE, bool ALIGNED, bool ONCE>
 __global__ __launch_bounds__(kThreads) void kv_kernel(KvArgs a) {
+  const unsigned shares = (unsigned)((a.Hk + a.heads - 1) / a.heads);
+  const int64_t item = blockIdx.x / shares;
+  const int h0 = (int)(blockIdx.x % shares) * a.heads;
   SeqItem s;
   if (a.off) {
-    s = find_packed(a.off, a.B, a.T, a.chunk, blockIdx.x);
+    s = find_packed(a.off, a.B, a.T, (int64_t)1 << a.chunk_bits, item);
   } else {
-    s.b = blockIdx.x / a.chunks;
-    s.chunk = blockIdx.x % a.chunks;
+    s.b = item / a.chunks;
+    s.chunk = item % a.chunks;
     s.row0 = 0;
     s.len = a.T;
   }
   // rows behind the last sequence
   const int64_t limit = !WRITE && a.zero_unused && s.b == a.B - 1 && a.off ? a.T - s.row0 : s.len;
-  const int64_t t0 = s.chunk * a.chunk;
+  const int64_t t0 = s.chunk << a.chunk_bits;
   if (t0 >= limit) return;
-  const int tokens = (int)(limit - t0 < a.chunk ? limit - t0 : a.chunk);
-  const int lanes = a.d / 8;  // of a row; a multiple of four
-  const unsigned per_token = (unsigned)(a.Hk * lanes);
+  const int lane_bits = __builtin_ctz(a.d) - 3;  // lanes of a row: 8, 16 or 32
+  const int heads = a.Hk - h0 < a.heads ? a.Hk - h0 : a.heads;
+  const unsigned places = (unsigned)heads << (a.chunk_bits + lane_bits);
   const int64_t first = a.start ? a.start[s.b] : 0;
   const int32_t* table = a.table + s.b * a.width;
-  const int64_t seq_k = a.off ? 0 : s.b * a.k_sb, seq_v = a.off ? 0 : s.b * a.v_sb;
-  for (int64_t i = threadIdx.x; i < (int64_t)tokens * per_token; i += kThreads) {
-    const unsigned t = (unsigned)(i / per_token), in = (unsigned)(i % per_token);
-    const int h = (int)(in / (unsigned)lanes), c = (int)(in % (unsigned)lanes);
-    const int64_t tok = t0 + t;
-    const int64_t row = tok < s.len ? kv_row(table, a.width, a.pages, a.page_bits, first + tok, a.Hk, h) : -1;
-    MT* k = static_cast<MT*>(a.k) + seq_k + (s.row0 + tok) * a.k_st + h * a.k_sh + 8 * c;
-    MT* v = static_cast<MT*>(a.v) + seq_v + (s.row0 + tok) * a.v_st + h * a.v_sh + 8 * c;
-    float x[2][8];
-    if constexpr (WRITE) {
-      // (the lanes of a row go the same way, so a block's four are all here)
-      if (row < 0) continue;
-      load8<MT, ALIGNED>(k, x[0]);
-      load8<MT, ALIGNED>(v, x[1]);
+  MT* k_rows = static_cast<MT*>(a.k) + (a.off ? 0 : s.b * a.k_sb) + s.row0 * a.k_st;
+  MT* v_rows = static_cast<MT*>(a.v) + (a.off ? 0 : s.b * a.v_sb) + s.row0 * a.v_st;
+
+  // places in order of head, token and channels
+  for (unsigned i0 = threadIdx.x; i0 < places; i0 += kAtOnce * kThreads) {
+    int64_t row[kAtOnce], tok[kAtOnce];
+    int c[kAtOnce], h[kAtOnce];
+    bool live[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        void* pool = j ? a.v_cache : a.k_cache;
-        if constexpr (FORMAT == GDN_KV_F32 || FORMAT == GDN_KV_BF16) {
-          store8<MT, true>(static_cast<MT*>(pool) + row * a.d + 8 * c, x[j]);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const unsigned i = i0 + u * kThreads;
+      c[u] = (int)(i & ((1u << lane_bits) - 1));
+      tok[u] = t0 + (i >> lane_bits & ((1u << a.chunk_bits) - 1));
+      h[u] = h0 + (int)(i >> (lane_bits + a.chunk_bits));
+      live[u] = i < places && tok[u] < limit;
+    }
+    float x[kAtOnce][2][8];
+    const auto rows_at = [&](int u, int j) {
+      return j ? v_rows + tok[u] * a.v_st + h[u] * a.v_sh + 8 * c[u] : k_rows + tok[u] * a.k_st + h[u] * a.k_sh + 8 * c[u];
+    };
+    if constexpr (WRITE)
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (live[u])
+#pragma unroll
+          for (int j = 0; j < 2; ++j) load8<MT, ALIGNED, true>(rows_at(u, j), x[u][j]);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      row[u] = live[u] && tok[u] < s.len ? kv_row(table, a.width, a.pages, a.page_bits, first + tok[u], a.Hk, h[u]) : -1;
+    if constexpr (!WRITE) {
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (row[u] >= 0) {
+          pool8<MT, FORMAT, ONCE>(a.k_cache, a.k_scales, row[u], a.d, c[u], x[u][0]);
+          pool8<MT, FORMAT, ONCE>(a.v_cache, a.v_scales, row[u], a.d, c[u], x[u][1]);
         } else {
-          const unsigned scale = block_scale<FORMAT>(block_top(x[j]));
-          unsigned w[2];
-          encode8<FORMAT>(x[j], scale, w);
-          if constexpr (FORMAT == GDN_KV_MXFP8)
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row * a.d + 8 * c) = make_uint2(w[0], w[1]);
-          else
-            *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(pool) + row * (a.d / 2) + 4 * c) = w[0];
-          if (c % 4 == 0) (j ? a.v_scales : a.k_scales)[row * (a.d / 32) + c / 4] = (uint8_t)scale;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[u][0][e] = x[u][1][e] = 0.0f;
         }
       }
-    } else {
-      if (row < 0) {
-        if (!a.zero_unused) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[0][e] = x[1][e] = 0.0f;
-      } else {
-        pool8<MT, FORMAT>(a.k_cache, a.k_scales, row, a.d, c, x[0]);
-        pool8<MT, FORMAT>(a.v_cache, a.v_scales, row, a.d, c, x[1]);
+      for (int u = 0; u < kAtOnce; ++u)
+        if (row[u] >= 0 || (a.zero_unused && live[u]))
+#pragma unroll
+          for (int j = 0; j < 2; ++j) store8<MT, ALIGNED>(rows_at(u, j), x[u][j]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        // (the lanes of a row go the same way, so a block's four are all here)
+        if (row[u] < 0) continue;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          void* pool = j ? a.v_cache : a.k_cache;
+          if constexpr (FORMAT == GDN_KV_F32 || FORMAT == GDN_KV_BF16) {
+            store8<MT, true>(static_cast<MT*>(pool) + row[u] * a.d + 8 * c[u], x[u][j]);
+          } else {
+            const unsigned scale = block_scale<FORMAT>(block_top(x[u][j]));
+            unsigned w[2];
+            encode8<FORMAT>(x[u][j], scale, w);
+            if constexpr (FORMAT == GDN_KV_MXFP8)
+              *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row[u] * a.d + 8 * c[u]) = make_uint2(w[0], w[1]);
+            else
+              *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(pool) + row[u] * (a.d / 2) + 4 * c[u]) = w[0];
+            uint8_t* to = (j ? a.v_scales : a.k_scales) + row[u] * (a.d / 32) + c[u] / 4;
+            if (lane_bits == 3) {
+              const unsigned two = two_bytes(scale);
+              if (c[u] % 8 == 0) *reinterpret_cast<uint16_t*>(to) = (uint16_t)two;
+            } else {
+              const unsigned four = four_bytes(scale);
+              if (c[u] % 16 == 0) *reinterpret_cast<unsigned*>(to) = four;
+            }
+          }
+        }
       }
-      store8<MT, ALIGNED>(k, x[0]);
-      store8<MT, ALIGNED>(v, x[1]);
     }
   }
 }
 
-template <typename MT, int FORMAT, bool WRITE>
-hipError_t kv_launch(const KvArgs& a, int64_t items, bool aligned, hipStream_t stream) {
+template <typename MT, int FORMAT, bool WRITE, bool ONCE>
+hipError_t kv_launch(const KvArgs& a, int64_t blocks, bool aligned, hipStream_t stream) {
   if (aligned)
-    hipLaunchKernelGGL((kv_kernel<MT, FORMAT, WRITE, true>), dim3((unsigned)items), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((kv_kernel<MT, FORMAT, WRITE, true, ONCE>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
   else
-    hipLaunchKernelGGL((kv_kernel<MT, FORMAT, WRITE, false>), dim3((unsigned)items), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((kv_kernel<MT, FORMAT, WRITE, false, ONCE>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename MT, int FORMAT>
-hipError_t kv_for(const KvArgs& a, int64_t items, bool write, bool aligned, hipStream_t stream) {
-  return write ? kv_launch<MT, FORMAT, true>(a, items, aligned, stream) : kv_launch<MT, FORMAT, false>(a, items, aligned, stream);
+hipError_t kv_for(const KvArgs& a, int64_t blocks, bool write, bool aligned, hipStream_t stream) {
+  if (write) return kv_launch<MT, FORMAT, true, false>(a, blocks, aligned, stream);
+  const int64_t bytes = 2 * (a.off ? a.T : a.B * a.T) * a.Hk * row_bytes(FORMAT, a.d);
+  return bytes >= kOnceBytes ? kv_launch<MT, FORMAT, false, true>(a, blocks, aligned, stream)
+                             : kv_launch<MT, FORMAT, false, false>(a, blocks, aligned, stream);
 }
 
 }  // namespace
@@ -96,17 +150,19 @@ hipError_t kv_for(const KvArgs& a, int64_t items, bool write, bool aligned, hipS
 template <typename MT>
 hipError_t launch_kv(const KvArgs& given, int format, bool write, bool aligned, hipStream_t stream) {
   KvArgs a = given;
-  // about eight vectors of K and as many of V a thread
-  const int64_t per_token = (int64_t)a.Hk * (a.d / 8);
-  a.chunk = (8 * kThreads + per_token - 1) / per_token;
-  if (!a.off && a.chunk > a.T) a.chunk = a.T;
-  a.chunks = (a.T + a.chunk - 1) / a.chunk;
-  const int64_t items = a.off ? a.T / a.chunk + a.B : a.B * a.chunks;
-  if (!grid_fits(items, kThreads)) return hipErrorNotSupported;
+  // tokens and heads of a workgroup: kPlaces places a thread, of 16 tokens where there are
+  a.chunk_bits = 0;
+  while (a.chunk_bits < kTokenBits && ((int64_t)1 << a.chunk_bits) < a.T) ++a.chunk_bits;
+  a.heads = (kPlaces * kThreads * 8 >> a.chunk_bits) / a.d;
+  a.heads = a.heads < 1 ? 1 : a.heads > a.Hk ? a.Hk : a.heads;
+  a.chunks = (a.T + ((int64_t)1 << a.chunk_bits) - 1) >> a.chunk_bits;
+  const int64_t items = a.off ? (a.T >> a.chunk_bits) + a.B : a.B * a.chunks;
+  const int64_t blocks = items * ((a.Hk + a.heads - 1) / a.heads);
+  if (items > 0x7FFFFFFF || !grid_fits(blocks, kThreads)) return hipErrorNotSupported;
   switch (format) {
-    case GDN_KV_MXFP8: return kv_for<MT, GDN_KV_MXFP8>(a, items, write, aligned, stream);
-    case GDN_KV_MXFP4: return kv_for<MT, GDN_KV_MXFP4>(a, items, write, aligned, stream);
-    default: return kv_for<MT, sizeof(MT) == 4 ? GDN_KV_F32 : GDN_KV_BF16>(a, items, write, aligned, stream);
+    case GDN_KV_MXFP8: return kv_for<MT, GDN_KV_MXFP8>(a, blocks, write, aligned, stream);
+    case GDN_KV_MXFP4: return kv_for<MT, GDN_KV_MXFP4>(a, blocks, write, aligned, stream);
+    default: return kv_for<MT, sizeof(MT) == 4 ? GDN_KV_F32 : GDN_KV_BF16>(a, blocks, write, aligned, stream);
   }
 }
 

@@ -114,8 +114,9 @@ struct KvArgs {
   int Hk, d;
   int page_bits;         // log2 of the tokens of a page
   int zero_unused;
-  int64_t chunk;         // tokens per workgroup
-  int64_t chunks;        // workgroups per sequence (not packed)
+  int chunk_bits;        // log2 of the tokens per workgroup
+  int heads;             // heads per workgroup
+  int64_t chunks;        // runs of tokens per sequence (not packed)
 };
 
 struct AttendArgs {
@@ -133,6 +134,7 @@ struct AttendArgs {
   int64_t window, sinks;
   int Hq, Hk, d, page_bits;
   int q_aligned;         // every row of q starts on 16 bytes
+  int once;              // pools are read past the caches
   float scale;
   int64_t items;         // runs of tiles; the workspace, or null where no sequence can be split:
   int32_t* plan;         // [B][2] first item and items of a sequence
