@@ -31,7 +31,14 @@ namespace {
 constexpr int kTile = 32;          // tokens
 constexpr int kWaves = 4;
 constexpr int kLeast = kWaves;     // tiles of an item: one a wave
-constexpr int kTarget = 1024;      // workgroups that a call is cut into, where it is long enough
+// Sequences are not cut where they have at most 16 tiles (8 heads, 512 tokens: 1
+// sequence 9.1 us against 10.5, 32 sequences 10.9 against 16.5; 1024 tokens: 13.7
+// against 10.5), or at most 64 and there are workgroups for most compute units
+// without (2048 tokens: 8 sequences 22.9 against 15.9, 32 33.1 against 35.5, 128
+// 105 against 115).
+constexpr int kShort = 16, kWhole = 64;
+constexpr int kTarget = 768;       // workgroups that a call is cut into, where it is long enough: as many as run at once
+constexpr int kCuts = 4;           // ... and items for every sequence, as they are of unequal length
 
 // What of a sequence is visible: [0, sinks) and [lo, len), as `tiles` tiles, the
 // first `first` of them from position 0 on, the others from tile `from` on.
@@ -84,8 +91,39 @@ __device__ __forceinline__ int64_t of_lane(int64_t x, int l) {
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// a / b for a >= 0, b > 0; a division of 64 bits only where it takes one
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((unsigned)a / (unsigned)b) : a / b;
+}
+
+// A word that is the same for the whole wave, by a scalar load.
+__device__ __forceinline__ int uniform_word(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int*)(uintptr_t)p;
+}
+
 __device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t i) {
   const int lane = threadIdx.x & 63;
+  if (!a.plan) {  // whole sequences
+    Item it;
+    it.b = i;
+    it.chunk = 0;
+    it.chunks = it.C = 1;
+    it.len = uniform_word(a.lengths + i);
+    it.any = true;
+    return it;
+  }
+  if (a.B == 1) {
+    Item it;
+    it.b = 0;
+    it.chunk = i;
+    it.len = uniform_word(a.lengths);
+    const int64_t tiles = seen_of(a, it.len).tiles, most = a.items - 1;
+    it.C = quotient(tiles + most - 1, most);
+    if (it.C < kLeast) it.C = kLeast;
+    it.chunks = tiles ? quotient(tiles + it.C - 1, it.C) : 1;
+    it.any = i < it.chunks;
+    return it;
+  }
   const int rounds = (int)((a.B + 63) / 64);
   int64_t total = 0;
   unsigned n = 0, before = 0;  // tiles of the lane's sequence, and before it in this round
@@ -99,7 +137,7 @@ __device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t i) {
   }
   Item it;
   const int64_t most = a.items - a.B;
-  it.C = (total + most - 1) / most;
+  it.C = quotient(total + most - 1, most);
   if (it.C < kLeast) it.C = kLeast;
   int64_t run = 0;
   it.b = 0;
@@ -111,7 +149,7 @@ __device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t i) {
       before = wave_scan(n) - n;
     }
     const int64_t at = run + before;
-    const int64_t first = (((at | it.C) >> 32) == 0 ? (int64_t)((unsigned)at / (unsigned)it.C) : at / it.C) + b;
+    const int64_t first = quotient(at, it.C) + b;
     const unsigned long long in = __ballot(b < a.B && first <= i);
     if (in == 0) break;
     const int l = 63 - __builtin_clzll(in);
@@ -119,7 +157,7 @@ __device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t i) {
     it.chunk = i - of_lane(first, l);
     it.len = of_lane(len, l);
     const int64_t tiles = (unsigned)__builtin_amdgcn_readlane((int)n, l);
-    it.chunks = tiles ? (tiles + it.C - 1) / it.C : 1;
+    it.chunks = tiles ? quotient(tiles + it.C - 1, it.C) : 1;
     if (in != ~0ull) break;
     run += (int64_t)(unsigned)__builtin_amdgcn_readlane((int)before, 63) + (unsigned)__builtin_amdgcn_readlane((int)n, 63);
   }
@@ -188,20 +226,36 @@ struct Shape {
   }
 };
 
-template <typename MT, int FORMAT, int D, int QT, bool ONCE>
-__global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
+template <typename MT, int FORMAT, int D, int QT, int WAVES, bool ONCE>
+__global__ __launch_bounds__(WAVES * 64) void attend_kernel(AttendArgs a) {
   typedef Shape<FORMAT, D> F;
   constexpr bool kWide = F::kWide, kCodes = F::kCodes;
   constexpr int kQTerms = kWide || sizeof(MT) == 2 ? 1 : 3, kPTerms = kWide ? 1 : sizeof(MT) == 2 ? 2 : 3;
-  __shared__ f32x4 dump[2][QT * F::kCols * 64];
-  __shared__ float stat[2][kWaves][QT * 16];
+  __shared__ f32x4 dump[WAVES / 2][QT * F::kCols * 64];
+  __shared__ float stat[2][WAVES][QT * 16];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, n = lane & 15;
   const int G = a.Hq / a.Hk, shares = (G + 16 * QT - 1) / (16 * QT);
   const int kh = (int)(blockIdx.x % a.Hk), share = (int)(blockIdx.x / a.Hk % shares);
-  const Item it = find_item(a, blockIdx.x / ((unsigned)a.Hk * shares));
   const int64_t item = blockIdx.x / ((unsigned)a.Hk * shares);
+  // Page numbers of a tile's halves, from its position, as the table has them:
+  // they are looked at where they are used, a tile later (see below).
+  struct Pages { int p[2]; };
+  auto pages_at = [&](const int32_t* table, int64_t pos) {
+    Pages r;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int64_t i = (pos + 16 * s) >> a.page_bits;
+      r.p[s] = uniform_word(table + (i < a.width ? i : a.width - 1));
+    }
+    return r;
+  };
+  // one sequence, or whole ones, without a window: where the first tile lies does not wait for the length
+  const bool known = (a.B == 1 || !a.plan) && !a.window;
+  Pages now = {};
+  if (known) now = a.plan ? pages_at(a.table, (item * WAVES + wave) * kTile) : pages_at(a.table + item * a.width, wave * kTile);
+  const Item it = find_item(a, item);
   if (!it.any) return;
   const int64_t b = it.b;
   const Seen seen = seen_of(a, it.len);
@@ -210,70 +264,41 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
     a.plan[2 * b + 1] = (int)it.chunks;
   }
 
-  // queries, by the channels that the keys come in
+  // queries, by the channels that the keys come in: loaded here, used after the
+  // first tile's loads are under way
   const int heads = G - share * 16 * QT < 16 * QT ? G - share * 16 * QT : 16 * QT;  // of this workgroup
   const int head0 = kh * G + share * 16 * QT;
-  bf16x8 qb[kWide ? 1 : QT][kQTerms][kWide ? 1 : D / 32];
-  f32x4 qw[kWide ? QT : 1][kWide ? D / 16 : 1];
+  constexpr int kChans = kWide ? 4 : 8, kProducts = D / (4 * kChans);  // channels of a lane, loads
+  MT qr[QT][kProducts][kChans];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    const bool mine = t * 16 + n < heads;
-    const MT* q = static_cast<const MT*>(a.q) + b * a.q_sb + (head0 + (mine ? t * 16 + n : 0)) * a.q_sh;
-    if constexpr (kWide) {
+    const MT* q = static_cast<const MT*>(a.q) + b * a.q_sb + (head0 + (t * 16 + n < heads ? t * 16 + n : 0)) * a.q_sh;
 #pragma unroll
-      for (int m = 0; m < D / 16; ++m) {
-        if (a.q_aligned) {
-          qw[t][m] = *reinterpret_cast<const f32x4*>(q + F::channel(m, g));
-        } else {
+    for (int m = 0; m < kProducts; ++m) {
+      if (a.q_aligned) {
+        __builtin_memcpy(qr[t][m], __builtin_assume_aligned(q + F::channel(m, g), 16), sizeof(qr[t][m]));
+      } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) qw[t][m][e] = q[F::channel(m, g) + e];
-        }
-        if (!mine) qw[t][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-    } else {
-#pragma unroll
-      for (int m = 0; m < D / 32; ++m) {
-        float x[8];
-        if (a.q_aligned) load8<MT, true, false>(q + F::channel(m, g), x);
-        else load8<MT, false, false>(q + F::channel(m, g), x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float rest = mine ? x[e] : 0.0f;
-#pragma unroll
-          for (int k = 0; k < kQTerms; ++k) {
-            qb[t][k][m][e] = (bf16)rest;
-            rest -= (float)qb[t][k][m][e];
-          }
-        }
+        for (int e = 0; e < kChans; ++e) qr[t][m][e] = q[F::channel(m, g) + e];
       }
     }
   }
 
   // tiles of this wave: the items of a sequence take turns, a tile a wave
-  const int64_t end = seen.tiles, step = it.chunks * kWaves;
-  int64_t tile = it.chunk * kWaves + wave;
+  const int64_t end = seen.tiles, step = it.chunks * WAVES;
+  int64_t tile = it.chunk * WAVES + wave;
   const int32_t* table = a.table + b * a.width;
   const uint8_t* pools[2] = {static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache)};
   const int64_t mask = ((int64_t)1 << a.page_bits) - 1;
   const unsigned k_off = n * F::kRow + g * (F::kRun * F::kBits / 8), v_off = 4 * g * F::kRow + n * F::kPieceBytes;
 
   auto place = [&](int64_t t) { return (t < seen.first ? t : t - seen.first + seen.from) * kTile; };
-  // page numbers of a tile's halves; no page: -1
-  struct Pages { int p[2]; };
-  auto pages_of = [&](int64_t t) {
-    Pages r;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int64_t i = (place(t) + 16 * s) >> a.page_bits;
-      const int64_t at = t < end && i < a.width ? i : 0;
-      const int v = *(const __attribute__((address_space(4))) int*)(uintptr_t)(table + at);
-      r.p[s] = i < a.width && v >= 0 && v < a.pages ? v : -1;
-    }
-    return r;
-  };
+  auto pages_of = [&](int64_t t) { return pages_at(table, t < end ? place(t) : 0); };
+  // (positions beyond the table are beyond the length too)
+  auto has_page = [&](const Pages& p, int s) { return p.p[s] >= 0 && p.p[s] < a.pages; };
   // first row in the pools of half s of a tile (page 0 where there is none)
   auto row_of = [&](int64_t t, const Pages& p, int s) {
-    const int64_t page = p.p[s] < 0 ? 0 : p.p[s];
+    const int64_t page = has_page(p, s) ? p.p[s] : 0;
     return ((page * a.Hk + kh) << a.page_bits) + ((place(t) + 16 * s) & mask);
   };
 
@@ -323,17 +348,34 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
   }
   const float scale2 = a.scale * kLog2e;
 
-  Pages now = {}, next = {};
+  Pages next = {};
   if (tile < end) {
-    now = pages_of(tile);
+    if (!known) now = pages_of(tile);
     load_k(tile, now);
     load_v(tile, now);
     next = pages_of(tile + step);
   }
-  for (; tile < end; tile += step) {
-    const bool more = tile + step < end;
-    // scores
-    f32x4 s[QT][2];
+  bf16x8 qb[kWide ? 1 : QT][kQTerms][kWide ? 1 : kProducts];
+  float qw[kWide ? QT : 1][kWide ? kProducts : 1][4];
+#pragma unroll
+  for (int t = 0; t < QT; ++t)
+#pragma unroll
+    for (int m = 0; m < kProducts; ++m)
+#pragma unroll
+      for (int e = 0; e < kChans; ++e) {
+        float rest = t * 16 + n < heads ? (float)qr[t][m][e] : 0.0f;
+        if constexpr (kWide) {
+          qw[t][m][e] = rest;
+        } else {
+#pragma unroll
+          for (int k = 0; k < kQTerms; ++k) {
+            qb[t][k][m][e] = (bf16)rest;
+            rest -= (float)qb[t][k][m][e];
+          }
+        }
+      }
+  f32x4 s[QT][2];
+  auto scores = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -376,22 +418,29 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
         }
       }
     }
-    Pages after = {};
-    if (more) {
-      after = pages_of(tile + 2 * step);
-      load_k(tile + step, next);
-    }
+  };
+  // weights of the tile's tokens, and their values added
+  auto values = [&]() {
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) s[t][h] *= scale2;
     // a tile that is not visible as a whole: which of the lane's tokens are
     const int64_t p0 = place(tile);
-    const bool whole = p0 + kTile <= seen.len && (p0 >= seen.lo || p0 + kTile <= seen.sinks) && now.p[0] >= 0 && now.p[1] >= 0;
+    const bool whole = p0 + kTile <= seen.len && (p0 >= seen.lo || p0 + kTile <= seen.sinks) && has_page(now, 0) && has_page(now, 1);
     unsigned ok = 0xFF;
     if (!whole) {
+      asm volatile("");  // (a branch: whole tiles are spared the selections)
       ok = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t p = p0 + 16 * (i / 4) + 4 * g + i % 4;
-        if (p < seen.len && (p >= seen.lo || p < seen.sinks) && now.p[i / 4] >= 0) ok |= 1u << i;
+        if (p < seen.len && (p >= seen.lo || p < seen.sinks) && has_page(now, i / 4)) ok |= 1u << i;
       }
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[t][i / 4][i % 4] = (ok >> i) & 1 ? s[t][i / 4][i % 4] : -INFINITY;
     }
     bf16x8 pb[kWide ? 1 : QT][kPTerms];
     float pw[QT][8];
@@ -400,8 +449,7 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
       float x[8], most = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[i] = s[t][i / 4][i % 4] * scale2;
-        if (!whole) x[i] = (ok >> i) & 1 ? x[i] : -INFINITY;
+        x[i] = s[t][i / 4][i % 4];
         most = fmaxf(most, x[i]);
       }
       most = fmaxf(top[t], over_groups_max(most));
@@ -445,6 +493,7 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
       }
     }
     if (!whole) {
+      asm volatile("");
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (!((ok >> i) & 1)) {
@@ -492,9 +541,24 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
               acc[t][c + o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[o], pb[t][k], acc[t][c + o], 0, 0, 0);
       }
     }
-    if (more) load_v(tile + step, next);
-    now = next;
-    next = after;
+  };
+  // The next tile's keys set out as soon as this one's are used, its values
+  // likewise, each without a branch: where one of the two might not have set
+  // out, waiting for one would be waiting for both.
+  if (tile < end) {
+    while (tile + step < end) {
+      scores();
+      load_k(tile + step, next);
+      values();
+      load_v(tile + step, next);
+      // scalar loads come back in any order, so a wait for one is a wait for
+      // all: the next ones set out here, and have come by when they are used
+      tile += step;
+      now = next;
+      next = pages_of(tile + step);
+    }
+    scores();
+    values();
   }
 
   // the waves' parts, brought to one maximum and added by twos
@@ -511,10 +575,10 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
   for (int t = 0; t < QT; ++t) {
     float most = -INFINITY, all = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) most = fmaxf(most, stat[0][w][t * 16 + n]);
+    for (int w = 0; w < WAVES; ++w) most = fmaxf(most, stat[0][w][t * 16 + n]);
     const float ref = most == -INFINITY ? 0.0f : most;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) all += hw_exp2(stat[0][w][t * 16 + n] - ref) * stat[1][w][t * 16 + n];
+    for (int w = 0; w < WAVES; ++w) all += hw_exp2(stat[0][w][t * 16 + n] - ref) * stat[1][w][t * 16 + n];
     const float f = hw_exp2(top[t] - ref);
 #pragma unroll
     for (int c = 0; c < F::kCols; ++c) acc[t][c] *= f;
@@ -522,7 +586,7 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
     sum[t] = all;
   }
 #pragma unroll
-  for (int half = kWaves / 2; half >= 1; half /= 2) {
+  for (int half = WAVES / 2; half >= 1; half /= 2) {
     if (wave >= half && wave < 2 * half)
 #pragma unroll
       for (int t = 0; t < QT; ++t)
@@ -564,63 +628,92 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(AttendArgs a) {
 }
 
 // The items of a sequence that was split, joined: a workgroup per sequence and
-// query head, its waves every fourth item, D / 64 channels a lane.
+// query head, its waves every eighth item, D / 64 channels a lane; a lane
+// works out the weight of one of 64 items.  A chain of load latencies: the
+// values' loads are under way before the maxima are known.
+constexpr int kJoinWaves = 8;
+
 template <typename MT, int D>
-__global__ __launch_bounds__(kWaves * 64) void join_kernel(AttendArgs a) {
-  constexpr int N = D / 64;
-  __shared__ float part[kWaves][D + 1];
+__global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a) {
+  constexpr int N = D / 64, U = 64 / kJoinWaves;
+  __shared__ float part[kJoinWaves][D];
   const int64_t b = blockIdx.x / a.Hq;
   const int h = (int)(blockIdx.x % a.Hq);
-  const int64_t first = a.plan[2 * b], chunks = a.plan[2 * b + 1];
+  const int first = a.plan[2 * b], chunks = a.plan[2 * b + 1];
   if (chunks == 1) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const float* stats = a.stats + 2 * (first * a.Hq + h);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const float* stats = a.stats + 2 * ((int64_t)first * a.Hq + h);
+  const float* parts = a.parts + ((int64_t)first * a.Hq + h) * D + lane * N;
+  float v[U][N];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = base + wave + u * kJoinWaves;
+      if (c < chunks) {
+        __builtin_memcpy(v[u], __builtin_assume_aligned(parts + (int64_t)c * a.Hq * D, N * 4), N * 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[u][i] = 0.0f;
+      }
+    }
+  };
+  load(0);
   float most = -INFINITY;
-  for (int64_t c = lane; c < chunks; c += 64) most = fmaxf(most, stats[2 * c * a.Hq]);
+  for (int c = lane; c < chunks; c += 64) most = fmaxf(most, stats[2 * (int64_t)c * a.Hq]);
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) most = fmaxf(most, __shfl_xor(most, m, 64));
   const float ref = most == -INFINITY ? 0.0f : most;
   float sum = 0.0f, o[N] = {};
-#pragma unroll 4
-  for (int64_t c = wave; c < chunks; c += kWaves) {
-    const float f = hw_exp2(stats[2 * c * a.Hq] - ref);
-    sum = fmaf(f, stats[2 * c * a.Hq + 1], sum);
-    const float* from = a.parts + ((first + c) * a.Hq + h) * D + lane * N;
+  for (int base = 0; base < chunks; base += 64) {
+    float f = 0.0f;
+    if (base + lane < chunks) {
+      const float* s = stats + 2 * (int64_t)(base + lane) * a.Hq;
+      f = hw_exp2(s[0] - ref);
+      sum = fmaf(f, s[1], sum);
+    }
+    float w[U][N];
+    __builtin_memcpy(w, v, sizeof(w));
+    if (base + 64 < chunks) load(base + 64);
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fmaf(f, from[i], o[i]);
+    for (int u = 0; u < U; ++u) {
+      const float k = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), wave + u * kJoinWaves));
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = fmaf(k, w[u][i], o[i]);
+    }
   }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) sum += __shfl_xor(sum, m, 64);
 #pragma unroll
   for (int i = 0; i < N; ++i) part[wave][lane * N + i] = o[i];
-  if (lane == 0) part[wave][D] = sum;
   __syncthreads();
-  if (wave != 0) return;
-  sum = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) sum += part[w][D];
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  MT* to = static_cast<MT*>(a.out) + b * a.o_sb + h * a.o_sh + lane * N;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
+  if (threadIdx.x < D) {
     float x = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) x += part[w][lane * N + i];
-    to[i] = (MT)(x * inv);
+    for (int w = 0; w < kJoinWaves; ++w) x += part[w][threadIdx.x];
+    static_cast<MT*>(a.out)[b * a.o_sb + h * a.o_sh + threadIdx.x] = (MT)(x * inv);
   }
-  if (lane == 0 && a.lse) a.lse[b * a.Hq + h] = sum == 0.0f ? -INFINITY : (most + log2f(sum)) * 0.6931471805599453f;
+  if (threadIdx.x == 0 && a.lse) a.lse[b * a.Hq + h] = sum == 0.0f ? -INFINITY : (most + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename MT, int FORMAT, int D, int QT>
 hipError_t attend_launch(const AttendArgs& a, hipStream_t stream) {
   const int64_t shares = (a.Hq / a.Hk + 16 * QT - 1) / (16 * QT);
   const int64_t blocks = a.items * a.Hk * shares;
-  if (!grid_fits(blocks, kWaves * 64) || !grid_fits(a.B * a.Hq, kWaves * 64)) return hipErrorNotSupported;
+  if (!grid_fits(blocks, 8 * 64) || !grid_fits(a.B * a.Hq, kJoinWaves * 64)) return hipErrorNotSupported;
+  if (!a.plan) {
+    // eight waves where their registers allow it
+    constexpr int W = D < 256 && D * QT * sizeof(MT) <= 512 ? 8 : 4;
+    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, W, false>), dim3((unsigned)blocks), dim3(W * 64), 0, stream, a);
+    return hipGetLastError();
+  }
   if (a.once)
-    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, true>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
+    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, kWaves, true>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
   else
-    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, false>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
+    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, kWaves, false>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.plan) return e;
-  hipLaunchKernelGGL((join_kernel<MT, D>), dim3((unsigned)(a.B * a.Hq)), dim3(kWaves * 64), 0, stream, a);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((join_kernel<MT, D>), dim3((unsigned)(a.B * a.Hq)), dim3(kJoinWaves * 64), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -652,17 +745,20 @@ AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, int64_t rea
   int64_t most = reach;
   if (window && window + sinks < reach) most = window + sinks + 2 * kTile;
   const int64_t tiles = (most + kTile - 1) / kTile;
+  // not cut: one kernel and no workspace
+  if (tiles <= kShort || (tiles <= kWhole && B * Hk * shares >= 3 * tiles)) {
+    p.items = B;
+    return p;
+  }
   int64_t whole = (kTarget + Hk * shares - 1) / (Hk * shares);
-  if (whole < 1) whole = 1;
+  if (whole < kCuts * B) whole = kCuts * B;
   // no more than all of them make
   const int64_t all = (tiles + kLeast - 1) / kLeast;
   if (all < (whole + B - 1) / B) whole = all * B;
   p.items = whole + B;
-  if (tiles > kLeast && p.items < ((int64_t)1 << 31)) {
-    p.plan_bytes = padded((size_t)B * 8);
-    p.parts_bytes = padded((size_t)p.items * Hq * d * 4);
-    p.total_bytes = p.plan_bytes + p.parts_bytes + padded((size_t)p.items * Hq * 8);
-  }
+  p.plan_bytes = padded((size_t)B * 8);
+  p.parts_bytes = padded((size_t)p.items * Hq * d * 4);
+  p.total_bytes = p.plan_bytes + p.parts_bytes + padded((size_t)p.items * Hq * 8);
   return p;
 }
 
