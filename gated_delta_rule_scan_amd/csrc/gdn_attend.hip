@@ -37,8 +37,12 @@ constexpr int kLeast = kWaves;     // tiles of an item: one a wave
 // without (2048 tokens: 8 sequences 22.9 against 15.9, 32 33.1 against 35.5, 128
 // 105 against 115).
 constexpr int kShort = 16, kWhole = 64;
-constexpr int kTarget = 768;       // workgroups that a call is cut into, where it is long enough: as many as run at once
-constexpr int kCuts = 4;           // ... and items for every sequence, as they are of unequal length
+constexpr int kCuts = 4;           // items for every sequence, where there are many of unequal length
+
+// Workgroups of four waves that a compute unit runs at once, by their registers.
+constexpr int at_once(int D, int QT, size_t size) {
+  return D * QT <= 64 ? (size == 4 ? 3 : 4) : D * QT <= 128 ? (size == 4 ? 2 : 3) : D * QT <= 256 ? (size == 4 ? 1 : 2) : 1;
+}
 
 // What of a sequence is visible: [0, sinks) and [lo, len), as `tiles` tiles, the
 // first `first` of them from position 0 on, the others from tile `from` on.
@@ -227,7 +231,7 @@ struct Shape {
 };
 
 template <typename MT, int FORMAT, int D, int QT, int WAVES, bool ONCE>
-__global__ __launch_bounds__(WAVES * 64) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : at_once(D, QT, sizeof(MT))) void attend_kernel(AttendArgs a) {
   typedef Shape<FORMAT, D> F;
   constexpr bool kWide = F::kWide, kCodes = F::kCodes;
   constexpr int kQTerms = kWide || sizeof(MT) == 2 ? 1 : 3, kPTerms = kWide ? 1 : sizeof(MT) == 2 ? 2 : 3;
@@ -738,9 +742,11 @@ size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
 
-AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, int64_t reach, int64_t window, int64_t sinks) {
+AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, bool half, int64_t reach, int64_t window, int64_t sinks) {
   AttendPlan p = {};
-  const int64_t G = Hq / Hk, shares = G <= 16 ? 1 : (G + 31) / 32;
+  const int64_t G = Hq / Hk;
+  const int QT = G <= 16 || (!half && d == 256) ? 1 : 2;
+  const int64_t shares = (G + 16 * QT - 1) / (16 * QT);
   // tiles that a sequence can have
   int64_t most = reach;
   if (window && window + sinks < reach) most = window + sinks + 2 * kTile;
@@ -750,8 +756,10 @@ AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, int64_t rea
     p.items = B;
     return p;
   }
-  int64_t whole = (kTarget + Hk * shares - 1) / (Hk * shares);
-  if (whole < kCuts * B) whole = kCuts * B;
+  // as many as run at once, each sequence's last one counted; or where those
+  // are few for every sequence, more, in several turns
+  const int64_t slots = 256 * at_once((int)d, QT, half ? 2 : 4) / (Hk * shares);
+  int64_t whole = slots >= 2 * B ? slots - B : kCuts * B;
   // no more than all of them make
   const int64_t all = (tiles + kLeast - 1) / kLeast;
   if (all < (whole + B - 1) / B) whole = all * B;

@@ -141,7 +141,7 @@ gdn_status_t attention_sizes(const gdn_attention_problem_t* p) {
 }
 
 AttendPlan plan_of(const gdn_attention_problem_t* p) {
-  return attend_plan(p->B, p->Hq, p->Hk, p->d, p->table_width * p->page, p->window, p->window ? p->sinks : 0);
+  return attend_plan(p->B, p->Hq, p->Hk, p->d, p->dtype == GDN_DTYPE_BF16, p->table_width * p->page, p->window, p->window ? p->sinks : 0);
 }
 
 gdn_status_t norm_sizes(const gdn_norm_problem_t* p) {

@@ -147,7 +147,7 @@ struct AttendPlan {
   int64_t items;
   size_t plan_bytes, parts_bytes, total_bytes;
 };
-AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, int64_t reach, int64_t window, int64_t sinks);
+AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, bool half, int64_t reach, int64_t window, int64_t sinks);
 
 struct NormArgs {
   const void* x;
