@@ -20,9 +20,10 @@
 // are its maximum, sum and rescaling.
 //
 // Rounding: queries and values of 16 bits or fewer enter bf16 products exactly;
-// weights enter as two bf16 terms (2^-17 of themselves), with fp32 queries both
-// as three (2^-25); a cache in fp32 goes through fp32 products.  Everything
-// else is fp32.
+// weights enter as two bf16 terms (off by 2^-16 of themselves: the first is cut,
+// not rounded, and the second, at most 2^-7, rounds by 2^-9), with fp32 queries
+// both as three; a cache in fp32 goes through fp32 products.  Everything else
+// is fp32.
 #include "gdn_kv.h"
 
 namespace gdn {
@@ -475,9 +476,16 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : at_once(D, QT, sizeof(
       if constexpr (!kWide)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float rest = pw[t][i];
+          // the first term: the weight cut to bf16, or the next below where that
+          // is the weight itself, so that what is left is above zero (an infinite
+          // value times both terms stays infinite; a weight that vanished counts
+          // as the least normal number for the same reason)
+          const float w = fmaxf(pw[t][i], 1.17549435e-38f);
+          const float cut = __builtin_bit_cast(float, (__builtin_bit_cast(unsigned, w) - 1u) & 0xFFFF0000u);
+          pb[t][0][i] = (bf16)cut;
+          float rest = w - cut;
 #pragma unroll
-          for (int k = 0; k < kPTerms; ++k) {
+          for (int k = 1; k < kPTerms; ++k) {
             pb[t][k][i] = (bf16)rest;
             rest -= (float)pb[t][k][i];
           }

@@ -46,7 +46,9 @@ def attend(q, k, v, scale, short):
 
     A score is a product of d terms and a scale: (d + 4) U of the magnitudes.  A weight e^(s - m) takes that error, the
     rounding of its exponent's argument (2 U |s - m|, twice) and 8 U; ``short`` (rows in 16 bits) carries weights as two
-    16-bit terms, off by 2^-17.  The sums over n tokens round at most n + 64 times."""
+    16-bit terms: the first is the weight cut to 8 bits (or one step below), so the second is above zero and at most
+    2^-7 of the weight, and rounds by 2^-9 of itself: 2^-16.  (fp32 rows: a third term, 2^-24 and less.)  The sums over n
+    tokens round at most n + 64 times."""
     G, d = q.shape
     if len(k) == 0:
         return (np.zeros((G, d)), np.zeros((G, d))), (np.full(G, -np.inf), np.zeros(G))
@@ -56,7 +58,7 @@ def attend(q, k, v, scale, short):
     z = w.sum(1, keepdims=True)
     w = w / z
     ds = (d + 4) * U * sm
-    rel = ds + (4 * np.abs(s - m) + 8) * U + (2.0 ** -17 if short else 2.0 ** -22)
+    rel = ds + (4 * np.abs(s - m) + 8) * U + (2.0 ** -16 if short else 2.0 ** -22)
     n = len(k) + 64
     zerr = (w * rel).sum(1, keepdims=True) + n * U
     out = w @ v

@@ -376,32 +376,52 @@ def test_attention_of_far_scores(kind):
     _check_attention(y, lse, _expect(q, table, lens, kv, vv, 2.0, 0, 0, kind), kind)
 
 
-def test_attention_of_nan_and_infinite_tokens():
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_attention_of_nan_and_infinite_tokens(kind):
     import gated_delta_rule_scan_amd as gdn
 
     torch = _torch()
-    lens = [50, 50, 50, 50]
-    q, cache, table, kv, vv = _attention_case("f32", "f32", lens, 2, 1, 64, 16, 0, 0, 6)
+    lens = [50, 50, 50, 50, 1]
+    q, cache, table, kv, vv = _attention_case(kind, kind, lens, 2, 1, 64, 16, 0, 0, 6)
     at = [place(table[b], len(kv), 16, 20) for b in range(4)]
     cache[0][at[0][0], 0, at[0][1]] = float("nan")      # a key: the whole row is NaN
     cache[1][at[1][0], 0, at[1][1], 5] = float("nan")   # a value: its channel
     cache[1][at[2][0], 0, at[2][1], 7] = float("inf")
+    cache[1][at[2][0], 0, at[2][1], 8] = -float("inf")
     cache[0][at[3][0], 0, at[3][1]] = 0                 # a key of minus infinity's score: weight zero
     cache[0][at[3][0], 0, at[3][1], 0] = -float("inf")
-    q[3, :, 0] = q[3, :, 0].abs() + 0.1
-    lse = torch.empty((4, 2), device="cuda")
+    cache[1][table[4, 0], 0, 0, 9] = float("inf")       # a weight of exactly one
+    q[:, :, 0] = q[:, :, 0].abs() + 0.1
+    lse = torch.empty((5, 2), device="cuda")
     y = gdn.attention_step(q, cache, i32(table), i32(lens), lse=lse)
     got = n(y)
-    assert np.isnan(got[0]).all()
+    assert np.isnan(got[0]).all() and np.isnan(n(lse)[0]).all()
     assert np.isnan(got[1, :, 5]).all() and np.isfinite(np.delete(got[1], 5, 1)).all()
-    assert np.isposinf(got[2, :, 7]).all() and np.isfinite(np.delete(got[2], 7, 1)).all()
+    assert np.isposinf(got[2, :, 7]).all() and np.isneginf(got[2, :, 8]).all()
+    assert np.isfinite(np.delete(got[2], [7, 8], 1)).all()
+    assert np.isposinf(got[4, :, 9]).all() and np.isfinite(np.delete(got[4], 9, 1)).all()
     kk, vals = n(cache[0]), n(cache[1])
     keep = [p for p in range(50) if p != 20]
     pg = np.array([table[3, p // 16] for p in keep])
     rw = np.array([p % 16 for p in keep])
-    (o, oe), (l, le) = oracle.attend(n(q)[3], kk[pg, 0, rw], vals[pg, 0, rw], 0.125, False)
-    check(got[3], o, oe, "f32")
+    (o, oe), (l, le) = oracle.attend(n(q)[3], kk[pg, 0, rw], vals[pg, 0, rw], 0.125, kind == "bf16")
+    check(got[3], o, oe, kind)
     check(n(lse)[3], l, le, "f32")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_attention_of_scores_that_are_all_minus_infinity(kind):
+    """The sum of weights is zero, as where nothing is visible."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    q, cache, table, kv, vv = _attention_case(kind, kind, [40, 3], 2, 1, 64, 16, 0, 0, 6)
+    cache[0].zero_()
+    cache[0][..., 0] = -float("inf")
+    q[:, :, 0] = 1
+    lse = torch.empty((2, 2), device="cuda")
+    y = gdn.attention_step(q, cache, i32(table), i32([40, 3]), lse=lse)
+    assert not n(y).any() and np.isneginf(n(lse)).all()
 
 
 def test_attention_of_a_pool_beyond_4_gib():
