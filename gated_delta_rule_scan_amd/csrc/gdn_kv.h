@@ -113,33 +113,34 @@ inline int64_t row_bytes(int format, int d) {
   return format == GDN_KV_F32 ? 4 * d : format == GDN_KV_BF16 ? 2 * d : (format == GDN_KV_MXFP8 ? d : d / 2) + d / 32;
 }
 
-// Eight channels of a row, in whole vectors or one by one.
+// Eight channels of a row, in vectors of 16 bytes; not ALIGNED to them, at any
+// address of the type.
+template <typename MT, bool ALIGNED>
+struct Vec {
+  static constexpr int kSize = 16 / sizeof(MT);
+  typedef MT type __attribute__((ext_vector_type(16 / sizeof(MT)), aligned(ALIGNED ? 16 : sizeof(MT))));
+};
+
 template <typename MT, bool ALIGNED, bool ONCE>
 __device__ __forceinline__ void load8(const MT* p, float (&x)[8]) {
-  if constexpr (ALIGNED) {
-    typedef MT vec __attribute__((ext_vector_type(16 / sizeof(MT))));
+  typedef Vec<MT, ALIGNED> V;
 #pragma unroll
-    for (int i = 0; i < 8; i += 16 / sizeof(MT)) {
-      const vec v = fetch<ONCE>(reinterpret_cast<const vec*>(p + i));
+  for (int i = 0; i < 8; i += V::kSize) {
+    const typename V::type v = fetch<ONCE>(reinterpret_cast<const typename V::type*>(p + i));
 #pragma unroll
-      for (int e = 0; e < (int)(16 / sizeof(MT)); ++e) x[i + e] = (float)v[e];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)p[i];
+    for (int e = 0; e < V::kSize; ++e) x[i + e] = (float)v[e];
   }
 }
 
 template <typename MT, bool ALIGNED>
 __device__ __forceinline__ void store8(MT* p, const float (&x)[8]) {
-  MT v[8];
+  typedef Vec<MT, ALIGNED> V;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (MT)x[i];
-  if constexpr (ALIGNED) {
-    __builtin_memcpy(__builtin_assume_aligned(p, 16), v, sizeof(v));
-  } else {
+  for (int i = 0; i < 8; i += V::kSize) {
+    typename V::type v;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = v[i];
+    for (int e = 0; e < V::kSize; ++e) v[e] = (MT)x[i + e];
+    *reinterpret_cast<typename V::type*>(p + i) = v;
   }
 }
 

@@ -38,13 +38,23 @@ constexpr int waves_at_once(int waves, int E, size_t size, bool backward) {
   return E == 16 ? (size == 4 ? 12 : 16) : 20;
 }
 
-// WAVES waves per row, E channels per lane in vectors of VEC.
-template <typename MT, int WAVES, int E, int VEC>
+// Threads of a workgroup: waves that have a row each come by four.
+constexpr int threads_of(int waves) { return (waves == 1 ? 4 : waves) * 64; }
+
+// WAVES waves per row, E channels per lane in vectors of 16 bytes.
+// Rows that are not WHOLE (off 16 bytes, or not of whole vectors) are moved in
+// vectors too, which the memory takes at any address; the last one of a row ends
+// with the row, so that its first channels are the neighbour's as well: both
+// compute and write the same, and sums leave one out.  bf16 in microseconds, so
+// against channel by channel: forward 8000 x 4003 51 and 88, 20000 x 1001 29 and
+// 49; backward 102 and 124, 59 and 67.
+template <typename MT, int WAVES, int E, bool WHOLE>
 struct Lanes {
+  static constexpr int VEC = 16 / sizeof(MT) < E ? 16 / sizeof(MT) : E;
   static_assert(WAVES == 1 || WAVES >= 4, "waves that share a row have the workgroup's barriers to themselves");
   static constexpr int kRows = WAVES == 1 ? 4 : 1;  // rows of a workgroup at a time
-  static constexpr int kThreads = WAVES * kRows * 64;
-  static constexpr int kAlign = VEC * sizeof(MT) < 16 ? VEC * sizeof(MT) : 16;
+  static constexpr int kThreads = threads_of(WAVES);
+  static constexpr int kAlign = WHOLE ? VEC * sizeof(MT) : sizeof(MT);
   // a lane's channels of a row as they lie in memory: what is in flight for the next row
   struct Raw {
     MT v[E];
@@ -57,7 +67,34 @@ struct Lanes {
   int phase = 0;
   mutable int sums_taken = 0;
 
-  __device__ __forceinline__ int col(int v) const { return v * WAVES * 64 * VEC + col0; }
+  // a vector's first channel, were it not moved back; whether the lane has it at all; how far it is moved
+  __device__ __forceinline__ int place(int v) const { return v * WAVES * 64 * VEC + col0; }
+  __device__ __forceinline__ bool live(int v) const { return place(v) < D; }
+  __device__ __forceinline__ int col(int v) const {
+    if constexpr (WHOLE) return place(v);
+    return live(v) && place(v) + VEC > D && !narrow() ? (int)D - VEC : place(v);
+  }
+  // the row has not one whole vector (wider kernels than the narrowest have no such rows)
+  __device__ __forceinline__ bool narrow() const { return !WHOLE && WAVES * E == 4 && D < VEC; }
+  __device__ __forceinline__ int twice(int v) const { return place(v) - col(v); }
+  // sum over the lane's own channels of a b; `some_twice`: the wave has a vector that was moved
+  __device__ __forceinline__ float dot(const float (&a)[E], const float (&b)[E], bool some_twice) const {
+    float s = 0.0f;
+    if (!WHOLE && some_twice) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) s = i % VEC >= twice(i / VEC) ? fmaf(a[i], b[i], s) : s;
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) s = fmaf(a[i], b[i], s);
+    }
+    return s;
+  }
+  __device__ __forceinline__ bool has_twice() const {
+    bool any = false;
+#pragma unroll
+    for (int v = 0; v < E / VEC; ++v) any = any || twice(v) != 0;
+    return !WHOLE && __any(any);
+  }
 
   __device__ __forceinline__ void load(const MT* p, Raw& x) const {
 #pragma unroll
@@ -65,7 +102,13 @@ struct Lanes {
       // (rows are read once: with the hint for that the backward call of 32760 x 2048 took 160 us, without 175)
       typedef MT vec __attribute__((ext_vector_type(VEC), aligned(kAlign)));
       vec q = (vec)(MT)0.0f;
-      if (col(v) < D) q = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p + col(v)));
+      if (narrow()) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (col(v) + e < D) q[e] = p[col(v) + e];
+      } else if (live(v)) {
+        q = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p + col(v)));
+      }
 #pragma unroll
       for (int e = 0; e < VEC; ++e) x.v[v * VEC + e] = q[e];
     }
@@ -82,35 +125,49 @@ struct Lanes {
   __device__ __forceinline__ void param(const float* p, float (&x)[E]) const {
 #pragma unroll
     for (int v = 0; v < E / VEC; ++v) {
-      if (p && col(v) < D) {
+      if (p && live(v) && !narrow()) {
         __builtin_memcpy(x + v * VEC, p + col(v), VEC * 4);
       } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[v * VEC + e] = 1.0f;
+        for (int e = 0; e < VEC; ++e) x[v * VEC + e] = narrow() && p && col(v) + e < D ? p[col(v) + e] : 1.0f;
       }
     }
   }
+  // In LDS a vector's pieces of 16 bytes lie WAVES * 64 pieces apart, so that a
+  // wave's lanes read side by side: [v][piece][lane].
   static constexpr int kStage = kOnce ? WAVES * 64 * E : 4;
+  static constexpr int kPiece = VEC < 4 ? VEC : 4;
   __device__ __forceinline__ void stage(const float* p, float* to) const {
     if constexpr (kOnce)
-      for (int i = threadIdx.x; i < kStage; i += kThreads) to[i] = p && i < D ? p[i] : 1.0f;
+      for (int i = threadIdx.x; i < kStage; i += kThreads) {
+        const int at = i / (WAVES * 64 * VEC) * (WAVES * 64 * VEC) + i / kPiece % (WAVES * 64) * VEC;  // its vector's place
+        int c = at + i / (WAVES * 64 * kPiece) % (VEC / kPiece) * kPiece + i % kPiece;
+        if (!WHOLE && at < D && at + VEC > D && !narrow()) c -= at + VEC - (int)D;
+        to[i] = p && c < D ? p[c] : 1.0f;
+      }
   }
   __device__ __forceinline__ void param(const float* p, const float* staged, float (&x)[E]) const {
     if constexpr (!kOnce) return param(p, x);
 #pragma unroll
-    for (int v = 0; v < E / VEC; ++v)
-      __builtin_memcpy(x + v * VEC, __builtin_assume_aligned(staged + col(v), VEC * 4 < 16 ? VEC * 4 : 16), VEC * 4);
+    for (int i = 0; i < E; i += kPiece)
+      __builtin_memcpy(x + i, __builtin_assume_aligned(staged + i * WAVES * 64 + col0 / VEC * kPiece, kPiece * 4), kPiece * 4);
   }
   template <typename T>
   __device__ __forceinline__ void store(T* p, const float (&x)[E]) const {
-    constexpr int kTo = VEC * sizeof(T) < 16 ? VEC * sizeof(T) : 16;
+    // (partial sums, fp32, lie at rows of D words)
+    typedef T vec __attribute__((ext_vector_type(VEC), aligned(sizeof(T) == sizeof(MT) ? kAlign : 4)));
 #pragma unroll
     for (int v = 0; v < E / VEC; ++v) {
-      if (col(v) >= D) continue;
-      T t[VEC];
+      if (narrow()) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) t[e] = (T)x[v * VEC + e];
-      __builtin_memcpy(__builtin_assume_aligned(p + col(v), sizeof(T) == 4 && sizeof(MT) != 4 ? 4 : kTo), t, sizeof(t));
+        for (int e = 0; e < VEC; ++e)
+          if (col(v) + e < D) p[col(v) + e] = (T)x[v * VEC + e];
+      } else if (live(v)) {
+        vec q;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) q[e] = (T)x[v * VEC + e];
+        *reinterpret_cast<vec*>(p + col(v)) = q;
+      }
     }
   }
   // K sums over the row, in all its lanes.  Several waves join theirs in LDS;
@@ -212,12 +269,12 @@ __device__ __forceinline__ Run run_of(const NormArgs& a, int sub) {
   return r;
 }
 
-template <typename MT, int WAVES, int E, int VEC>
-__global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_once(WAVES, E, sizeof(MT), false) / 4)) void norm_kernel(NormArgs a) {
-  typedef Lanes<MT, WAVES, E, VEC> L;
+template <typename MT, int WAVES, int E, bool WHOLE>
+__global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(MT), false) / 4)) void norm_kernel(NormArgs a) {
+  typedef Lanes<MT, WAVES, E, WHOLE> L;
   __shared__ float red[4 * WAVES];
   const int sub = L::kRows > 1 ? threadIdx.x / (64 * WAVES) : 0;
-  L lanes{a.D, (int)(threadIdx.x % (64 * WAVES)) * VEC, red};
+  L lanes{a.D, (int)(threadIdx.x % (64 * WAVES)) * L::VEC, red};
   const Run r = run_of<L::kRows>(a, sub);
   const int64_t b = a.off ? 0 : r.b;
   const MT* x_rows = static_cast<const MT*>(a.x) + b * a.x_sb;
@@ -232,6 +289,7 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_onc
     if (a.y) lanes.load(y_rows + (r.row0 + t) * a.y_st, ry);
   }
   const float inv_d = 1.0f / (float)a.D;
+  const bool twice = lanes.has_twice();
   const float* gate = a.gate ? a.gate + r.b * a.gate_sb : nullptr;
   float x[E], y[E], g[E], pw[E], w[E];
   if (L::kOnce) {
@@ -252,9 +310,7 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_onc
     asm volatile("" ::: "memory");  // (the loads are issued here, not where they are used)
     if (a.y) {
       if (a.post) {
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int i = 0; i < E; ++i) s[0] = fmaf(y[i], y[i], s[0]);
+        float s[1] = {lanes.dot(y, y, twice)};
         lanes.sum(s);
         const float inv = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
         if (!L::kOnce) lanes.param(a.post, pw);
@@ -267,9 +323,7 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_onc
     }
     if (a.h) lanes.store(h_rows + row * a.h_st, x);
     if (a.n) {
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int i = 0; i < E; ++i) s[0] = fmaf(x[i], x[i], s[0]);
+      float s[1] = {lanes.dot(x, x, twice)};
       lanes.sum(s);
       const float inv = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
       if (!L::kOnce) lanes.param(a.weight, w);
@@ -287,12 +341,12 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_onc
   }
 }
 
-template <typename MT, int WAVES, int E, int VEC>
-__global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_once(WAVES, E, sizeof(MT), true) / 4)) void norm_back_kernel(NormArgs a) {
-  typedef Lanes<MT, WAVES, E, VEC> L;
+template <typename MT, int WAVES, int E, bool WHOLE>
+__global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(MT), true) / 4)) void norm_back_kernel(NormArgs a) {
+  typedef Lanes<MT, WAVES, E, WHOLE> L;
   __shared__ float red[4 * WAVES];
   const int sub = L::kRows > 1 ? threadIdx.x / (64 * WAVES) : 0;
-  L lanes{a.D, (int)(threadIdx.x % (64 * WAVES)) * VEC, red};
+  L lanes{a.D, (int)(threadIdx.x % (64 * WAVES)) * L::VEC, red};
   const Run r = run_of<L::kRows>(a, sub);
   const int64_t b = a.off ? 0 : r.b;
   const MT* x_rows = static_cast<const MT*>(a.x) + b * a.x_sb;
@@ -311,6 +365,7 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_onc
   int64_t t = r.t;
   if (t < r.len) load(r.row0 + t);
   const float inv_d = 1.0f / (float)a.D;
+  const bool twice = lanes.has_twice();
   const float* gate = a.gate ? a.gate + r.b * a.gate_sb : nullptr;
   __shared__ __align__(16) float params[3][L::kStage];
   lanes.stage(gate, params[0]);
@@ -335,9 +390,7 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_onc
     if (L::kAhead && t + r.step < r.len) load(row + r.step);
     float ry_ = 1.0f;
     if (a.post) {
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int i = 0; i < E; ++i) s[0] = fmaf(y[i], y[i], s[0]);
+      float s[1] = {lanes.dot(y, y, twice)};
       lanes.sum(s);
       ry_ = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
     }
@@ -349,13 +402,11 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_onc
       h[i] = fmaf(g[i], y[i] * pw[i], a.alpha * h[i]);
     }
     if (a.n) {
-      float s[2] = {0.0f, 0.0f}, w[E];
+      float w[E];  // weight, then weight dn
       lanes.param(a.weight, params[2], w);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        s[0] = fmaf(h[i], h[i], s[0]);
-        s[1] = fmaf(w[i] * dn[i], h[i], s[1]);
-      }
+      for (int i = 0; i < E; ++i) w[i] *= dn[i];
+      float s[2] = {lanes.dot(h, h, twice), lanes.dot(w, h, twice)};
       lanes.sum(s);
       const float rh = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
       const float c = s[1] * rh * inv_d;  // mean(w dn h^)
@@ -363,7 +414,7 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_onc
       for (int i = 0; i < E; ++i) {
         const float hh = h[i] * rh;
         dw[i] = fmaf(dn[i], hh, dw[i]);
-        d[i] = fmaf(rh, fmaf(-hh, c, w[i] * dn[i]), d[i]);
+        d[i] = fmaf(rh, fmaf(-hh, c, w[i]), d[i]);
       }
     }
     if (a.dx) {
@@ -383,14 +434,13 @@ __global__ __launch_bounds__((Lanes<MT, WAVES, E, VEC>::kThreads), (waves_at_onc
     }
     if (a.dgate) dg.add(u);
     if (a.post) {
-      float s[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         u[i] = d[i] * y[i];
         d[i] *= pw[i];
-        s[0] = fmaf(d[i], y[i], s[0]);
       }
       if (a.dpost) dpw.add(u);
+      float s[1] = {lanes.dot(d, y, twice)};
       lanes.sum(s);
       const float c = s[0] * inv_d;
 #pragma unroll
@@ -506,24 +556,23 @@ constexpr Width kWidths[] = {{256, 1, 4},
                              {8192, BACKWARD ? 16 : 8, BACKWARD ? 8 : 16},
                              {16384, 16, 16}};
 
-template <typename MT, int VEC, bool BACKWARD, int I = 0>
+template <typename MT, bool WHOLE, bool BACKWARD, int I = 0>
 hipError_t norm_by_width(const NormArgs& a, hipStream_t stream) {
   constexpr Width w = kWidths<BACKWARD>[I];
   if constexpr (w.D < 16384)
-    if (a.D > w.D) return norm_by_width<MT, VEC, BACKWARD, I + 1>(a, stream);
-  constexpr int kVec = VEC < w.E ? VEC : w.E;
-  constexpr int kThreads = Lanes<MT, w.waves, w.E, kVec>::kThreads;
+    if (a.D > w.D) return norm_by_width<MT, WHOLE, BACKWARD, I + 1>(a, stream);
+  constexpr int kThreads = threads_of(w.waves);
   if (!grid_fits(a.items, kThreads)) return hipErrorNotSupported;
   if constexpr (BACKWARD)
-    hipLaunchKernelGGL((norm_back_kernel<MT, w.waves, w.E, kVec>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((norm_back_kernel<MT, w.waves, w.E, WHOLE>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
   else
-    hipLaunchKernelGGL((norm_kernel<MT, w.waves, w.E, kVec>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((norm_kernel<MT, w.waves, w.E, WHOLE>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename MT, bool BACKWARD>
 hipError_t norm_for(const NormArgs& a, bool aligned, hipStream_t stream) {
-  return aligned ? norm_by_width<MT, 16 / sizeof(MT), BACKWARD>(a, stream) : norm_by_width<MT, 1, BACKWARD>(a, stream);
+  return aligned ? norm_by_width<MT, true, BACKWARD>(a, stream) : norm_by_width<MT, false, BACKWARD>(a, stream);
 }
 
 }  // namespace
