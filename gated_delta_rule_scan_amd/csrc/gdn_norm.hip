@@ -10,8 +10,8 @@
 //   dy  = r(y) (b - y^ mean(b y^)), b = wp g dH (or dy = g dH),  dwp = sum g dH y^
 //
 // Memory-bound: four rows a token forward, six backward.  A row stays in
-// registers between its reductions, 8 or 16 channels a lane over one, four or
-// sixteen waves; parameters and the sums over rows stay in registers over all
+// registers between its reductions, 4 to 16 channels a lane over a quarter of a
+// wave to sixteen waves; parameters and the sums over rows stay in registers over all
 // of a workgroup's rows.  Those sums go to the workspace, one partial each per
 // workgroup, and a second kernel adds them in a fixed order.
 #include "gdn_layer.h"
@@ -19,15 +19,21 @@
 namespace gdn {
 namespace {
 
-// Sum over a wave, in every lane: quads, eights and sixteens by row
-// permutations, then pairs of rows and the halves swapped.
+// Sum over LANES lanes of a wave (16, 32 or 64), in each of them: quads, eights
+// and sixteens by row permutations, then pairs of rows and the halves swapped.
+template <int LANES>
 __device__ __forceinline__ float wave_sum(float x) {
   auto add = [](float v, int moved) { return v + __builtin_bit_cast(float, moved); };
   x = add(x, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0xB1, 0xF, 0xF, true));   // quad: 1 0 3 2
   x = add(x, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x4E, 0xF, 0xF, true));   // quad: 2 3 0 1
   x = add(x, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x141, 0xF, 0xF, true));  // half row mirrored
   x = add(x, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x140, 0xF, 0xF, true));  // row mirrored
-  return over_groups(x, [](float a, float b) { return a + b; });
+  if constexpr (LANES == 16) return x;
+  if constexpr (LANES == 64) return over_groups(x, [](float a, float b) { return a + b; });
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned a = r[0], b = r[1];
+  return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
 }
 
 // Waves of a compute unit at a time, by registers and LDS.  A call has
@@ -38,47 +44,51 @@ constexpr int waves_at_once(int waves, int E, size_t size, bool backward) {
   return E == 16 ? (size == 4 ? 12 : 16) : 20;
 }
 
-// Threads of a workgroup: waves that have a row each come by four.
-constexpr int threads_of(int waves) { return (waves == 1 ? 4 : waves) * 64; }
+// Threads of a workgroup: rows of up to a wave come by four waves.
+constexpr int threads_of(int lanes) { return lanes <= 64 ? 256 : lanes; }
 
-// WAVES waves per row, E channels per lane in vectors of 16 bytes.
+// LANES lanes per row, E channels per lane in vectors of 16 bytes.
 // Rows that are not WHOLE (off 16 bytes, or not of whole vectors) are moved in
 // vectors too, which the memory takes at any address; the last one of a row ends
-// with the row, so that its first channels are the neighbour's as well: both
-// compute and write the same, and sums leave one out.  bf16 in microseconds, so
+// with the row, so that its first channels are the neighbour's as well.  Those are
+// left out of sums, and written twice they are the same; in a call in place the
+// waves wait for each other's loads, since a neighbour could have written them
+// before they are read.  bf16 in microseconds, so
 // against channel by channel: forward 8000 x 4003 51 and 88, 20000 x 1001 29 and
-// 49; backward 102 and 124, 59 and 67.
-template <typename MT, int WAVES, int E, bool WHOLE>
+// 49; backward 101 and 124, 55 and 67.
+template <typename MT, int LANES, int E, bool WHOLE>
 struct Lanes {
   static constexpr int VEC = 16 / sizeof(MT) < E ? 16 / sizeof(MT) : E;
+  static constexpr int WAVES = LANES <= 64 ? 1 : LANES / 64;
   static_assert(WAVES == 1 || WAVES >= 4, "waves that share a row have the workgroup's barriers to themselves");
-  static constexpr int kRows = WAVES == 1 ? 4 : 1;  // rows of a workgroup at a time
-  static constexpr int kThreads = threads_of(WAVES);
+  static constexpr int kRows = WAVES == 1 ? 256 / LANES : 1;  // rows of a workgroup at a time
+  static constexpr int kThreads = threads_of(LANES);
   static constexpr int kAlign = WHOLE ? VEC * sizeof(MT) : sizeof(MT);
   // a lane's channels of a row as they lie in memory: what is in flight for the next row
   struct Raw {
     MT v[E];
   };
   // whether a row's loads are under way while the one before is worked on
-  static constexpr bool kAhead = WAVES * 64 * E <= 8192;
+  static constexpr bool kAhead = LANES * E <= 8192;
   int64_t D;
   int col0;  // the lane's first channel
   float* red;
   int phase = 0;
   mutable int sums_taken = 0;
+  bool some_twice = false;  // the wave has a vector that was moved
 
   // a vector's first channel, were it not moved back; whether the lane has it at all; how far it is moved
-  __device__ __forceinline__ int place(int v) const { return v * WAVES * 64 * VEC + col0; }
+  __device__ __forceinline__ int place(int v) const { return v * LANES * VEC + col0; }
   __device__ __forceinline__ bool live(int v) const { return place(v) < D; }
   __device__ __forceinline__ int col(int v) const {
     if constexpr (WHOLE) return place(v);
     return live(v) && place(v) + VEC > D && !narrow() ? (int)D - VEC : place(v);
   }
   // the row has not one whole vector (wider kernels than the narrowest have no such rows)
-  __device__ __forceinline__ bool narrow() const { return !WHOLE && WAVES * E == 4 && D < VEC; }
+  __device__ __forceinline__ bool narrow() const { return !WHOLE && LANES == 16 && D < VEC; }
   __device__ __forceinline__ int twice(int v) const { return place(v) - col(v); }
-  // sum over the lane's own channels of a b; `some_twice`: the wave has a vector that was moved
-  __device__ __forceinline__ float dot(const float (&a)[E], const float (&b)[E], bool some_twice) const {
+  // sum over the lane's own channels of a b
+  __device__ __forceinline__ float dot(const float (&a)[E], const float (&b)[E]) const {
     float s = 0.0f;
     if (!WHOLE && some_twice) {
 #pragma unroll
@@ -89,11 +99,18 @@ struct Lanes {
     }
     return s;
   }
-  __device__ __forceinline__ bool has_twice() const {
+  // before a row is written, in a call in place: every wave of it has its loads, of this row and the next
+  __device__ __forceinline__ void loaded(bool in_place) const {
+    if (WHOLE || WAVES == 1 || !in_place) return;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  }
+  // (by the whole wave, before anything else)
+  __device__ __forceinline__ void begin() {
     bool any = false;
 #pragma unroll
     for (int v = 0; v < E / VEC; ++v) any = any || twice(v) != 0;
-    return !WHOLE && __any(any);
+    some_twice = !WHOLE && __any(any);
   }
 
   __device__ __forceinline__ void load(const MT* p, Raw& x) const {
@@ -121,7 +138,7 @@ struct Lanes {
   // channels they are loaded once: the forward kernel keeps them in registers,
   // the backward one, which has sums there, in LDS (in LDS the forward call of
   // 65520 x 2048 took 215 us, in registers 194).
-  static constexpr bool kOnce = WAVES * 64 * E <= 8192;
+  static constexpr bool kOnce = LANES * E <= 8192;
   __device__ __forceinline__ void param(const float* p, float (&x)[E]) const {
 #pragma unroll
     for (int v = 0; v < E / VEC; ++v) {
@@ -133,15 +150,15 @@ struct Lanes {
       }
     }
   }
-  // In LDS a vector's pieces of 16 bytes lie WAVES * 64 pieces apart, so that a
+  // In LDS a vector's pieces of 16 bytes lie LANES pieces apart, so that a
   // wave's lanes read side by side: [v][piece][lane].
-  static constexpr int kStage = kOnce ? WAVES * 64 * E : 4;
+  static constexpr int kStage = kOnce ? LANES * E : 4;
   static constexpr int kPiece = VEC < 4 ? VEC : 4;
   __device__ __forceinline__ void stage(const float* p, float* to) const {
     if constexpr (kOnce)
       for (int i = threadIdx.x; i < kStage; i += kThreads) {
-        const int at = i / (WAVES * 64 * VEC) * (WAVES * 64 * VEC) + i / kPiece % (WAVES * 64) * VEC;  // its vector's place
-        int c = at + i / (WAVES * 64 * kPiece) % (VEC / kPiece) * kPiece + i % kPiece;
+        const int at = i / (LANES * VEC) * (LANES * VEC) + i / kPiece % LANES * VEC;  // its vector's place
+        int c = at + i / (LANES * kPiece) % (VEC / kPiece) * kPiece + i % kPiece;
         if (!WHOLE && at < D && at + VEC > D && !narrow()) c -= at + VEC - (int)D;
         to[i] = p && c < D ? p[c] : 1.0f;
       }
@@ -150,7 +167,7 @@ struct Lanes {
     if constexpr (!kOnce) return param(p, x);
 #pragma unroll
     for (int i = 0; i < E; i += kPiece)
-      __builtin_memcpy(x + i, __builtin_assume_aligned(staged + i * WAVES * 64 + col0 / VEC * kPiece, kPiece * 4), kPiece * 4);
+      __builtin_memcpy(x + i, __builtin_assume_aligned(staged + i * LANES + col0 / VEC * kPiece, kPiece * 4), kPiece * 4);
   }
   template <typename T>
   __device__ __forceinline__ void store(T* p, const float (&x)[E]) const {
@@ -175,7 +192,7 @@ struct Lanes {
   template <int K>
   __device__ __forceinline__ void sum(float (&s)[K]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) s[k] = wave_sum(s[k]);
+    for (int k = 0; k < K; ++k) s[k] = wave_sum<(LANES < 64 ? LANES : 64)>(s[k]);
     if constexpr (WAVES > 1) {
       float* buf = red + phase * (2 * WAVES);
       phase ^= 1;
@@ -269,12 +286,12 @@ __device__ __forceinline__ Run run_of(const NormArgs& a, int sub) {
   return r;
 }
 
-template <typename MT, int WAVES, int E, bool WHOLE>
-__global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(MT), false) / 4)) void norm_kernel(NormArgs a) {
-  typedef Lanes<MT, WAVES, E, WHOLE> L;
-  __shared__ float red[4 * WAVES];
-  const int sub = L::kRows > 1 ? threadIdx.x / (64 * WAVES) : 0;
-  L lanes{a.D, (int)(threadIdx.x % (64 * WAVES)) * L::VEC, red};
+template <typename MT, int LANES, int E, bool WHOLE>
+__global__ __launch_bounds__(threads_of(LANES), (waves_at_once(LANES / 64, E, sizeof(MT), false) / 4)) void norm_kernel(NormArgs a) {
+  typedef Lanes<MT, LANES, E, WHOLE> L;
+  __shared__ float red[4 * L::WAVES];
+  const int sub = L::kRows > 1 ? threadIdx.x / LANES : 0;
+  L lanes{a.D, (int)(threadIdx.x % LANES) * L::VEC, red};
   const Run r = run_of<L::kRows>(a, sub);
   const int64_t b = a.off ? 0 : r.b;
   const MT* x_rows = static_cast<const MT*>(a.x) + b * a.x_sb;
@@ -289,7 +306,7 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
     if (a.y) lanes.load(y_rows + (r.row0 + t) * a.y_st, ry);
   }
   const float inv_d = 1.0f / (float)a.D;
-  const bool twice = lanes.has_twice();
+  lanes.begin();
   const float* gate = a.gate ? a.gate + r.b * a.gate_sb : nullptr;
   float x[E], y[E], g[E], pw[E], w[E];
   if (L::kOnce) {
@@ -308,9 +325,10 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
       if (a.y) lanes.load(y_rows + (row + r.step) * a.y_st, ry);
     }
     asm volatile("" ::: "memory");  // (the loads are issued here, not where they are used)
+    lanes.loaded(a.h == a.x);
     if (a.y) {
       if (a.post) {
-        float s[1] = {lanes.dot(y, y, twice)};
+        float s[1] = {lanes.dot(y, y)};
         lanes.sum(s);
         const float inv = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
         if (!L::kOnce) lanes.param(a.post, pw);
@@ -323,7 +341,7 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
     }
     if (a.h) lanes.store(h_rows + row * a.h_st, x);
     if (a.n) {
-      float s[1] = {lanes.dot(x, x, twice)};
+      float s[1] = {lanes.dot(x, x)};
       lanes.sum(s);
       const float inv = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
       if (!L::kOnce) lanes.param(a.weight, w);
@@ -341,12 +359,12 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
   }
 }
 
-template <typename MT, int WAVES, int E, bool WHOLE>
-__global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(MT), true) / 4)) void norm_back_kernel(NormArgs a) {
-  typedef Lanes<MT, WAVES, E, WHOLE> L;
-  __shared__ float red[4 * WAVES];
-  const int sub = L::kRows > 1 ? threadIdx.x / (64 * WAVES) : 0;
-  L lanes{a.D, (int)(threadIdx.x % (64 * WAVES)) * L::VEC, red};
+template <typename MT, int LANES, int E, bool WHOLE>
+__global__ __launch_bounds__(threads_of(LANES), (waves_at_once(LANES / 64, E, sizeof(MT), true) / 4)) void norm_back_kernel(NormArgs a) {
+  typedef Lanes<MT, LANES, E, WHOLE> L;
+  __shared__ float red[4 * L::WAVES];
+  const int sub = L::kRows > 1 ? threadIdx.x / LANES : 0;
+  L lanes{a.D, (int)(threadIdx.x % LANES) * L::VEC, red};
   const Run r = run_of<L::kRows>(a, sub);
   const int64_t b = a.off ? 0 : r.b;
   const MT* x_rows = static_cast<const MT*>(a.x) + b * a.x_sb;
@@ -365,7 +383,7 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
   int64_t t = r.t;
   if (t < r.len) load(r.row0 + t);
   const float inv_d = 1.0f / (float)a.D;
-  const bool twice = lanes.has_twice();
+  lanes.begin();
   const float* gate = a.gate ? a.gate + r.b * a.gate_sb : nullptr;
   __shared__ __align__(16) float params[3][L::kStage];
   lanes.stage(gate, params[0]);
@@ -388,9 +406,10 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
     if (a.h) L::open(rdh, d);
     if (a.n) L::open(rdn, dn);
     if (L::kAhead && t + r.step < r.len) load(row + r.step);
+    lanes.loaded(a.dx == a.h);
     float ry_ = 1.0f;
     if (a.post) {
-      float s[1] = {lanes.dot(y, y, twice)};
+      float s[1] = {lanes.dot(y, y)};
       lanes.sum(s);
       ry_ = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
     }
@@ -406,7 +425,7 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
       lanes.param(a.weight, params[2], w);
 #pragma unroll
       for (int i = 0; i < E; ++i) w[i] *= dn[i];
-      float s[2] = {lanes.dot(h, h, twice), lanes.dot(w, h, twice)};
+      float s[2] = {lanes.dot(h, h), lanes.dot(w, h)};
       lanes.sum(s);
       const float rh = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
       const float c = s[1] * rh * inv_d;  // mean(w dn h^)
@@ -440,7 +459,7 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
         d[i] *= pw[i];
       }
       if (a.dpost) dpw.add(u);
-      float s[1] = {lanes.dot(d, y, twice)};
+      float s[1] = {lanes.dot(d, y)};
       lanes.sum(s);
       const float c = s[0] * inv_d;
 #pragma unroll
@@ -462,17 +481,17 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
   float* part = a.parts + blockIdx.x * (int64_t)a.sums * a.D;
   auto put = [&](float (&x)[E]) {
     if constexpr (L::kRows > 1) {
-      __shared__ float side[L::kRows - 1][E * 64 * WAVES];
+      __shared__ float side[L::kRows - 1][E * LANES];
       __syncthreads();
       if (sub > 0)
 #pragma unroll
-        for (int i = 0; i < E; ++i) side[sub - 1][i * 64 * WAVES + threadIdx.x % (64 * WAVES)] = x[i];
+        for (int i = 0; i < E; ++i) side[sub - 1][i * LANES + threadIdx.x % LANES] = x[i];
       __syncthreads();
       if (sub == 0)
 #pragma unroll
         for (int i = 0; i < E; ++i)
 #pragma unroll
-          for (int k = 0; k < L::kRows - 1; ++k) x[i] += side[k][i * 64 * WAVES + threadIdx.x];
+          for (int k = 0; k < L::kRows - 1; ++k) x[i] += side[k][i * LANES + threadIdx.x];
     }
     if (sub == 0) lanes.store(part, x);
     part += a.D;
@@ -488,14 +507,14 @@ __global__ __launch_bounds__(threads_of(WAVES), (waves_at_once(WAVES, E, sizeof(
   if (a.dweight) put(dw);
 }
 
-// Partial sums [parts][sums][D] to gradients: a workgroup takes 64 channels of
-// one gradient (of one sequence's, where the gate is per sequence), its waves
-// every sixteenth partial, joined in order.
+// Partial sums [parts][sums][D] to gradients: a workgroup takes 32 channels of
+// one gradient (of one sequence's, where the gate is per sequence), its half
+// waves every 32nd partial, joined in order.
 __global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a) {
-  __shared__ float red[16][64];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t tiles = (a.D + 63) / 64;
-  const int64_t c = (blockIdx.x % tiles) * 64 + lane;
+  __shared__ float red[32][32];
+  const int half = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t tiles = (a.D + 31) / 32;
+  const int64_t c = (blockIdx.x % tiles) * 32 + lane;
   int64_t which = blockIdx.x / tiles;  // gates, then the others
   const int64_t gates = a.dgate ? (a.gate_sb ? a.B : 1) : 0;
   int64_t first = 0, last = a.items;
@@ -518,55 +537,57 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a) {
     kind = (a.dgate ? 1 : 0) + (int)which;
     to = which == 0 && a.dpost ? a.dpost : a.dweight;
   }
-  // (sixteen loads under way at a time: the sum is a chain of their latencies)
+  // (sixteen loads under way at a time, the last ones too: the sum is a chain of their latencies)
   float s = 0.0f;
   if (c < a.D) {
     const float* from = a.parts + kind * a.D + c;
     const int64_t step = a.sums * a.D;
-    int64_t p = first + wave;
-    for (; p + 15 * 16 < last; p += 16 * 16) {
+    for (int64_t p = first + half; p < last; p += 16 * 32) {
       float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = from[(p + 16 * i) * step];
+      for (int i = 0; i < 16; ++i) v[i] = from[(p + 32 * i < last ? p + 32 * i : p) * step];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s += v[i];
+      for (int i = 0; i < 16; ++i) s = p + 32 * i < last ? s + v[i] : s;
     }
-    for (; p < last; p += 16) s += from[p * step];
   }
-  red[wave][lane] = s;
+  red[half][lane] = s;
   __syncthreads();
-  if (wave != 0 || c >= a.D) return;
+  if (half != 0 || c >= a.D) return;
   s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s += red[i][lane];
+  for (int i = 0; i < 32; ++i) s += red[i][lane];
   to[c] = s;
 }
 
-// A row's waves and a lane's channels, by the row's width.
+// A row's lanes and a lane's channels, by the row's width.  Rows up to 256
+// channels share a wave: a row alone has too few bytes under way (with a wave
+// per row 93750 x 64 took 30 us in bf16 and 29 in fp32, so 12 and 18).
 struct Width {
   int64_t D;
-  int waves, E;
+  int lanes, E;
 };
-template <bool BACKWARD>
-constexpr Width kWidths[] = {{256, 1, 4},
-                             {512, 1, 8},
-                             {1024, 1, 16},
-                             {2048, 4, 8},
-                             {4096, BACKWARD ? 8 : 4, BACKWARD ? 8 : 16},
-                             {8192, BACKWARD ? 16 : 8, BACKWARD ? 8 : 16},
-                             {16384, 16, 16}};
+template <bool HALF, bool BACKWARD>
+constexpr Width kWidths[] = {{64, 16, 4},
+                             {128, 32, 4},
+                             {256, HALF ? 32 : 64, HALF ? 8 : 4},
+                             {512, 64, 8},
+                             {1024, 64, 16},
+                             {2048, 256, 8},
+                             {4096, BACKWARD ? 512 : 256, BACKWARD ? 8 : 16},
+                             {8192, BACKWARD ? 1024 : 512, BACKWARD ? 8 : 16},
+                             {16384, 1024, 16}};
 
 template <typename MT, bool WHOLE, bool BACKWARD, int I = 0>
 hipError_t norm_by_width(const NormArgs& a, hipStream_t stream) {
-  constexpr Width w = kWidths<BACKWARD>[I];
+  constexpr Width w = kWidths<sizeof(MT) == 2, BACKWARD>[I];
   if constexpr (w.D < 16384)
     if (a.D > w.D) return norm_by_width<MT, WHOLE, BACKWARD, I + 1>(a, stream);
-  constexpr int kThreads = threads_of(w.waves);
+  constexpr int kThreads = threads_of(w.lanes);
   if (!grid_fits(a.items, kThreads)) return hipErrorNotSupported;
   if constexpr (BACKWARD)
-    hipLaunchKernelGGL((norm_back_kernel<MT, w.waves, w.E, WHOLE>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((norm_back_kernel<MT, w.lanes, w.E, WHOLE>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
   else
-    hipLaunchKernelGGL((norm_kernel<MT, w.waves, w.E, WHOLE>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((norm_kernel<MT, w.lanes, w.E, WHOLE>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -579,11 +600,11 @@ hipError_t norm_for(const NormArgs& a, bool aligned, hipStream_t stream) {
 
 NormPlan norm_plan(int64_t B, int64_t T, int64_t D, bool half, bool packed, bool backward) {
   NormPlan p;
-  const Width* widths = backward ? kWidths<true> : kWidths<false>;
+  const Width* widths = half ? (backward ? kWidths<true, true> : kWidths<true, false>) : backward ? kWidths<false, true> : kWidths<false, false>;
   while (D > widths->D && widths->D < 16384) ++widths;
   const Width& w = *widths;
-  const int64_t at_once = w.waves == 1 ? 4 : 1;
-  int64_t workgroups = 256 * (waves_at_once(w.waves, w.E, half ? 2 : 4, backward) / (w.waves * at_once));
+  const int64_t at_once = w.lanes <= 64 ? 256 / w.lanes : 1;
+  int64_t workgroups = 256 * (waves_at_once(w.lanes / 64, w.E, half ? 2 : 4, backward) * 64 / threads_of(w.lanes));
   if (workgroups < 256) workgroups = 256;
   const int64_t rows = packed ? T : B * T;
   // (a packed batch has up to a workgroup a sequence more)
@@ -609,7 +630,7 @@ hipError_t launch_norm_back(const NormArgs& a, bool aligned, hipStream_t stream)
   }
   const int64_t outs = (a.dgate ? (a.gate_sb ? a.B : 1) : 0) + (a.dpost ? 1 : 0) + (a.dweight ? 1 : 0);
   if (!outs) return hipSuccess;
-  const int64_t blocks = outs * ((a.D + 63) / 64);
+  const int64_t blocks = outs * ((a.D + 31) / 32);
   if (!grid_fits(blocks, 1024)) return hipErrorNotSupported;
   hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)blocks), dim3(1024), 0, stream, a);
   return hipGetLastError();

@@ -475,6 +475,15 @@ SEAM = [
     ("bf16", [3000, 1500], 1100, True, "sequence", True, True, 1.0, "odd"),
     ("bf16", (2, 0), 64, True, "sequence", True, True, 1.0, "plain"),
 ]
+# rows off 16 bytes and of no whole vectors, in every kernel's widths: the last vector of a row is moved back into it
+SEAM += [(kind, lens, D, True, gate, True, True, 1.0, layout)
+         for D in [1, 2, 3, 4, 5, 7, 9, 63, 65, 67, 127, 129, 150, 250, 257, 501, 1001, 1025, 2001, 4003, 7001, 9001]
+         for kind, lens, gate, layout in [("bf16", (2, 19), "sequence", "plain"), ("f32", [5, 0, 31, 1], "sequence", "odd")]]
+SEAM += [("bf16", [200, 0, 33, 1], 64, True, "sequence", True, True, 1.0, "odd"),
+         ("bf16", [200, 0, 33, 1], 128, True, "sequence", False, True, 1.0, "slices"),
+         ("bf16", [200, 0, 33, 1], 256, True, "sequence", True, True, 1.0, "plain"),
+         ("f32", (3, 90), 128, True, "channel", True, True, 1.0, "plain"),
+         ("bf16", (1, 9000), 64, True, "channel", True, True, 1.0, "plain")]
 
 
 class SeamCase:
@@ -586,6 +595,26 @@ def test_residual_norm_in_place_and_given_outputs(kind):
     want = c.expect_backward(dh=False)
     check(c.flat(got[0]), *want["dx"], kind, "dx")
     check(n(got[2]), *want["dgate"], "f32", "dgate")
+
+
+@pytest.mark.parametrize("kind,D,layout", [("bf16", 2001, "plain"), ("bf16", 1100, "odd"), ("f32", 1027, "plain"), ("bf16", 4003, "plain"),
+                                           ("f32", 8190, "odd"), ("bf16", 16381, "plain"), ("bf16", 1001, "plain"), ("f32", 67, "odd")])
+@pytest.mark.parametrize("post,weight", [(False, False), (True, False), (False, True)])
+def test_residual_norm_in_place_of_odd_widths(kind, D, layout, post, weight):
+    """Rows of no whole vectors over several waves that do not wait for each other: no wave reads what another wrote."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    c = SeamCase(kind, (2, 400), D, True, "sequence", post, weight, 0.5, layout)
+    h0, n0 = gdn.residual_norm(c.x, c.y, **c.args())
+    g0 = gdn.residual_norm_backward(c.dh, c.dn, c.x, c.y, **c.args())
+    (eh, ehb), _ = c.expect()
+    check(c.flat(h0), eh, ehb, kind, "h")
+    dh = c.dh.clone()
+    gdn.residual_norm_backward(dh, c.dn, c.x, c.y, **c.args(), dx=dh)
+    assert torch.equal(dh, g0[0])
+    _, nn = gdn.residual_norm(c.x, c.y, **c.args(), out=c.x)
+    assert torch.equal(c.x, h0) and (not weight or torch.equal(nn, n0))
 
 
 def test_residual_norm_gradients_against_differences():
