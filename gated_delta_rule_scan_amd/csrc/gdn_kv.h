@@ -100,8 +100,11 @@ __device__ __forceinline__ void decode8(const unsigned (&w)[2], float scale, flo
 }
 
 // A vector that is read `once`: non-temporal.  That is faster where the data
-// comes from memory (%s) and slower where it waits in the cache (%s), so a
-// call that reads less than kOnceBytes of a cache does without.
+// comes from memory (64 ragged sequences' attention, 1092 MB: 199 us against 212;
+// 143 MB out of a cache in 4 bits: 150 against 158) and slower where it waits in
+// the cache (fp32 attention over a window, 38 MB: 18.0 against 16.1; 11 MB out of
+// a cache in 4 bits: 27.9 against 19.9), so a call that reads less than kOnceBytes
+// of a cache does without.
 constexpr int64_t kOnceBytes = (int64_t)64 << 20;
 template <bool ONCE, typename T>
 __device__ __forceinline__ T fetch(const T* p) {

@@ -553,8 +553,10 @@ gdn_status_t gdn_kv_read(const gdn_kv_problem_t* p, const void* k_cache, const v
  * lengths[b], and with window > 0 only p >= lengths[b] - window or p < sinks)
  *   s_p = scale q . k_p,  out = sum_p exp(s_p) v_p / sum_p exp(s_p),
  *   lse = log(sum_p exp(s_p))
- * No visible position: out is zero, lse minus infinity.  What lies in places
- * that are not visible, NaN included, has no influence.  lengths beyond the table's
+ * Where no weight is above zero (no visible position, or every score minus
+ * infinity) out is zero and lse minus infinity; a score of plus infinity or NaN
+ * makes its row and lse NaN.  What lies in places that are not visible, NaN
+ * included, has no influence.  lengths beyond the table's
  * reach count as that.
  *   q, out  head h of sequence b at b * stride_b + h * stride_h, d contiguous
  *           channels (dtype)
