@@ -44,6 +44,12 @@ constexpr int kLeast = kWaves;     // tiles of an item: one a wave
 // without (2048 tokens: 8 sequences 22.9 against 15.9, 32 33.1 against 35.5, 128
 // 105 against 115).
 constexpr int kShort = 16, kWhole = 64;
+// Where they are not cut, eight waves take each (if the registers allow it) for
+// up to kFew workgroups or beyond kLong tiles, else four, of which a compute unit
+// holds more: 512 tokens, 128 sequences of 8 heads 39 us with eight, 33 with four;
+// 64 tokens 20 and 11; 2048 tokens 105 and 113; 24 windows of 793 in fp32 on 4
+// heads 15.5 and 15.9.
+constexpr int kFew = 128, kLong = 32;
 constexpr int kCuts = 4;           // items for every sequence, where there are many of unequal length
 
 // Workgroups of four waves that a compute unit runs at once, by their registers.
@@ -719,18 +725,17 @@ hipError_t attend_launch(const AttendArgs& a, hipStream_t stream) {
   const int64_t shares = (a.Hq / a.Hk + 16 * QT - 1) / (16 * QT);
   const int64_t blocks = a.items * a.Hk * shares;
   if (!grid_fits(blocks, 8 * 64) || !grid_fits(a.B * a.Hq, kJoinWaves * 64)) return hipErrorNotSupported;
-  if (!a.plan) {
-    // eight waves where their registers allow it
-    constexpr int W = D < 256 && D * QT * sizeof(MT) <= 512 ? 8 : 4;
-    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, W, false>), dim3((unsigned)blocks), dim3(W * 64), 0, stream, a);
-    return hipGetLastError();
-  }
-  if (a.once)
+  if constexpr (D < 256 && D * QT * sizeof(MT) <= 512)
+    if (!a.plan && a.tiles > kWaves && (blocks <= kFew || a.tiles > kLong)) {
+      hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, 8, false>), dim3((unsigned)blocks), dim3(8 * 64), 0, stream, a);
+      return hipGetLastError();
+    }
+  if (a.plan && a.once)
     hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, kWaves, true>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
   else
     hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, kWaves, false>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || !a.plan) return e;
   hipLaunchKernelGGL((join_kernel<MT, D>), dim3((unsigned)(a.B * a.Hq)), dim3(kJoinWaves * 64), 0, stream, a);
   return hipGetLastError();
 }
@@ -789,6 +794,7 @@ hipError_t launch_attend(const AttendArgs& given, int format, hipStream_t stream
   AttendArgs a = given;
   // (what can be visible: how much is, only the device knows)
   const int64_t reach = a.width << a.page_bits, tokens = a.window && a.window + a.sinks < reach ? a.window + a.sinks : reach;
+  a.tiles = (tokens + kTile - 1) / kTile;
   a.once = 2 * a.B * tokens >= kOnceBytes / (a.Hk * row_bytes(format, a.d));
   switch (format) {
     case GDN_KV_MXFP8: return attend_for<MT, GDN_KV_MXFP8>(a, stream);

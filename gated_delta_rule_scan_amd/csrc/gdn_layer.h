@@ -132,6 +132,7 @@ struct AttendArgs {
   int64_t B, width, pages;
   int64_t q_sb, q_sh, o_sb, o_sh;
   int64_t window, sinks;
+  int64_t tiles;         // that a sequence may have (about)
   int Hq, Hk, d, page_bits;
   int q_aligned;         // every row of q starts on 16 bytes
   int once;              // pools are read past the caches

@@ -48,7 +48,12 @@ def attend(q, k, v, scale, short):
     rounding of its exponent's argument (2 U |s - m|, twice) and 8 U; ``short`` (rows in 16 bits) carries weights as two
     16-bit terms: the first is the weight cut to 8 bits (or one step below), so the second is above zero and at most
     2^-7 of the weight, and rounds by 2^-9 of itself: 2^-16.  (fp32 rows: a third term, 2^-24 and less.)  The sums over n
-    tokens round at most n + 64 times."""
+    tokens round at most n + 64 times.
+
+    Below the least normal number, 2^-126, fp32 gives up digits.  A weight (at most 1, the largest is 1, so z >= 1) that
+    lies there is taken for something between zero and 2^-126, so it is off by 2^-126 at most; so are the two factors,
+    at most 1, by which waves' and items' parts come to one maximum: 3 * 2^-126 sum |v| in all.  A product with a value
+    that lies there may vanish: another 2^-126 a token."""
     G, d = q.shape
     if len(k) == 0:
         return (np.zeros((G, d)), np.zeros((G, d))), (np.full(G, -np.inf), np.zeros(G))
@@ -62,7 +67,7 @@ def attend(q, k, v, scale, short):
     n = len(k) + 64
     zerr = (w * rel).sum(1, keepdims=True) + n * U
     out = w @ v
-    err = (w * (rel + zerr + n * U)) @ np.abs(v)
+    err = (w * (rel + zerr + n * U)) @ np.abs(v) + 2.0 ** -126 * (3 * np.abs(v).sum(0) + n)
     lse = (m + np.log(z))[:, 0]
     return (out, err), (lse, zerr[:, 0] + ds.max(1) + 4 * U * (np.abs(m[:, 0]) + np.abs(lse) + 1))
 

@@ -262,6 +262,12 @@ ATTEND = [
     ("bf16", "bf16", [37] * 300, 2, 1, 64, 16, 0, 0),        # more sequences than a wave has lanes
     ("bf16", "bf16", [4000] + [3] * 70, 4, 2, 64, 32, 0, 0),
 ]
+# many sequences, none cut: with few tiles, up to 32, and more than 32
+ATTEND += [(kind, form, lens, Hq, Hk, d, page, window, 0)
+           for kind, form, Hq, Hk, d, page in [("bf16", "bf16", 8, 4, 128, 16), ("f32", "f32", 16, 8, 64, 32),
+                                               ("bf16", "mxfp8", 34, 2, 128, 64), ("f32", "mxfp4", 6, 6, 64, 16)]
+           for lens, window in [([2, 0, 63, 128] * 20, 0), ([300, 1, 129, 0, 1000] * 16, 90), ([33, 500] * 35, 0),
+                                ([0, 1100, 700, 20] * 15, 0)]]
 
 
 def _attention_case(kind, form, lens, Hq, Hk, d, page, window, sinks, seed, width=None):
