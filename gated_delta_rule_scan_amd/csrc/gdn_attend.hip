@@ -143,7 +143,7 @@ __device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t i) {
   }
   const int rounds = (int)((a.B + 63) / 64);
   int64_t total = 0;
-  unsigned n = 0, before = 0;  // tiles of the lane's sequence, and before it in this round
+  unsigned n = 0, before = 0;  // tiles of the lane's sequence, and before it among these 64
   int64_t len = 0;
   for (int r = 0; r < rounds; ++r) {
     const int64_t b = r * 64 + lane;

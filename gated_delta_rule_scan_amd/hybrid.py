@@ -109,7 +109,7 @@ def residual_norm_backward(dh, dn, x, y=None, gate=None, post_weight=None, weigh
 def register_ops() -> None:
     """The calls as torch.library custom ops (torch.ops.gdn.kv_write, kv_read, attention_step, residual_norm,
     residual_norm_backward) with fake implementations for tracing; kv_write mutates the cache.  residual_norm's op
-    needs y and weight."""
+    needs y and weight.  None has an autograd formula: residual_norm_backward is called by name."""
     op = torch.library.custom_op
     cache = "Tensor k_cache, Tensor v_cache, Tensor? k_scales, Tensor? v_scales"
 
