@@ -8,7 +8,7 @@
 // to 8192 tokens, 32 query heads on 8 of 128, bf16: 1092 MB in 178 + 7 us (6.0
 // TB/s); one of 131072 tokens in 8 bits: 277 MB in 48 + 4 (5.8 TB/s).  A cache in
 // 4 bits is bound by the vector instructions that turn codes into operands: 128
-// sequences of up to 8192, 16 query heads on one, 72 MB in 31 us (cached).
+// sequences of up to 8192, 16 query heads on one, 72 MB in 32 us (cached).
 // A few short sequences end at the latency of one tile's chain and two launches:
 // 1560 tokens of 12 heads 6.2 + 2.8 us.
 //
@@ -25,11 +25,12 @@
 // lanes but the maximum over groups.  Query n is the lane's in both results, as
 // are its maximum, sum and rescaling.
 //
-// Rounding: queries and values of 16 bits or fewer enter bf16 products exactly;
-// weights enter as two bf16 terms (off by 2^-16 of themselves: the first is cut,
-// not rounded, and the second, at most 2^-7, rounds by 2^-9), with fp32 queries
-// both as three; a cache in fp32 goes through fp32 products.  Everything else
-// is fp32.
+// Rounding: queries and values of 16 bits or fewer enter bf16 products exactly,
+// weights as three bf16 terms that add up to them (two are off by 2^-15 at most
+// and turn one output in two thousand to its other neighbour, for 1.1 us less of 32.3
+// where products bound it: 128 sequences of up to 8192, 16 query heads on one, in
+// 4 bits), fp32 queries as three (off by 2^-24 at most); a cache in fp32 goes
+// through fp32 products.  Everything else is fp32.
 #include "gdn_kv.h"
 
 namespace gdn {
@@ -247,7 +248,7 @@ template <typename MT, int FORMAT, int D, int QT, int WAVES, bool ONCE>
 __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : at_once(D, QT, sizeof(MT))) void attend_kernel(AttendArgs a) {
   typedef Shape<FORMAT, D> F;
   constexpr bool kWide = F::kWide, kCodes = F::kCodes;
-  constexpr int kQTerms = kWide || sizeof(MT) == 2 ? 1 : 3, kPTerms = kWide ? 1 : sizeof(MT) == 2 ? 2 : 3;
+  constexpr int kQTerms = kWide || sizeof(MT) == 2 ? 1 : 3, kPTerms = kWide ? 1 : 3;
   __shared__ f32x4 dump[WAVES / 2][QT * F::kCols * 64];
   __shared__ float stat[2][WAVES][QT * 16];
 
@@ -488,18 +489,16 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : at_once(D, QT, sizeof(
       if constexpr (!kWide)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          // the first term: the weight cut to bf16, or the next below where that
-          // is the weight itself, so that what is left is above zero (an infinite
-          // value times both terms stays infinite; a weight that vanished counts
-          // as the least normal number for the same reason)
-          const float w = fmaxf(pw[t][i], 1.17549435e-38f);
-          const float cut = __builtin_bit_cast(float, (__builtin_bit_cast(unsigned, w) - 1u) & 0xFFFF0000u);
-          pb[t][0][i] = (bf16)cut;
-          float rest = w - cut;
+          // the first two terms: what is left cut to bf16, or the next below where
+          // that is all of it, so that every term is above zero (an infinite value
+          // times each stays infinite; a weight that vanished counts as the least
+          // normal number for the same reason).  Three times eight bits hold all 24.
+          float rest = fmaxf(pw[t][i], 1.17549435e-38f);
 #pragma unroll
-          for (int k = 1; k < kPTerms; ++k) {
-            pb[t][k][i] = (bf16)rest;
-            rest -= (float)pb[t][k][i];
+          for (int k = 0; k < kPTerms; ++k) {
+            const float cut = __builtin_bit_cast(float, (__builtin_bit_cast(unsigned, rest) - 1u) & 0xFFFF0000u);
+            pb[t][k][i] = (bf16)(k + 1 < kPTerms ? cut : rest);
+            rest -= cut;
           }
         }
     }
