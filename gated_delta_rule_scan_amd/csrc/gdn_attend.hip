@@ -490,13 +490,14 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : at_once(D, QT, sizeof(
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           // the first two terms: what is left cut to bf16, or the next below where
-          // that is all of it, so that every term is above zero (an infinite value
-          // times each stays infinite; a weight that vanished counts as the least
-          // normal number for the same reason).  Three times eight bits hold all 24.
-          float rest = fmaxf(pw[t][i], 1.17549435e-38f);
+          // that is all of it, so that no term of a weight above 2^-100 is zero (an
+          // infinite value times each stays infinite) and all of zero are.  Three
+          // times eight bits hold all 24.
+          float rest = pw[t][i];
 #pragma unroll
           for (int k = 0; k < kPTerms; ++k) {
-            const float cut = __builtin_bit_cast(float, (__builtin_bit_cast(unsigned, rest) - 1u) & 0xFFFF0000u);
+            const unsigned bits = __builtin_bit_cast(unsigned, rest);
+            const float cut = __builtin_bit_cast(float, ((bits > 1u ? bits : 1u) - 1u) & 0xFFFF0000u);
             pb[t][k][i] = (bf16)(k + 1 < kPTerms ? cut : rest);
             rest -= cut;
           }
@@ -639,13 +640,15 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : at_once(D, QT, sizeof(
         a.stats[2 * (item * a.Hq + h) + 1] = sum[t];
       }
     } else {
-      const float inv = sum[t] == 0.0f ? 0.0f : 1.0f / sum[t];
+      // (zero, whatever 2^-inf made of the values)
+      const bool none = sum[t] == 0.0f;
+      const float inv = 1.0f / sum[t];
       MT* to = static_cast<MT*>(a.out) + b * a.o_sb + h * a.o_sh;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < F::kCols; ++c) to[F::out_channel(c, g, i)] = (MT)(acc[t][c][i] * inv);
-      if (g == 0 && a.lse) a.lse[b * a.Hq + h] = sum[t] == 0.0f ? -INFINITY : (top[t] + log2f(sum[t])) * 0.6931471805599453f;
+        for (int c = 0; c < F::kCols; ++c) to[F::out_channel(c, g, i)] = (MT)(none ? 0.0f : acc[t][c][i] * inv);
+      if (g == 0 && a.lse) a.lse[b * a.Hq + h] = none ? -INFINITY : (top[t] + log2f(sum[t])) * 0.6931471805599453f;
     }
   }
 }
@@ -709,14 +712,15 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a) {
 #pragma unroll
   for (int i = 0; i < N; ++i) part[wave][lane * N + i] = o[i];
   __syncthreads();
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const bool none = sum == 0.0f;
+  const float inv = 1.0f / sum;
   if (threadIdx.x < D) {
     float x = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJoinWaves; ++w) x += part[w][threadIdx.x];
-    static_cast<MT*>(a.out)[b * a.o_sb + h * a.o_sh + threadIdx.x] = (MT)(x * inv);
+    static_cast<MT*>(a.out)[b * a.o_sb + h * a.o_sh + threadIdx.x] = (MT)(none ? 0.0f : x * inv);
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[b * a.Hq + h] = sum == 0.0f ? -INFINITY : (most + log2f(sum)) * 0.6931471805599453f;
+  if (threadIdx.x == 0 && a.lse) a.lse[b * a.Hq + h] = none ? -INFINITY : (most + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename MT, int FORMAT, int D, int QT>

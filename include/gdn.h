@@ -555,9 +555,13 @@ gdn_status_t gdn_kv_read(const gdn_kv_problem_t* p, const void* k_cache, const v
  *   lse = log(sum_p exp(s_p))
  * Where no weight is above zero (no visible position, or every score minus
  * infinity) out is zero and lse minus infinity; a score of plus infinity or NaN
- * makes its row and lse NaN.  What lies in places that are not visible, NaN
- * included, has no influence.  lengths beyond the table's
- * reach count as that.
+ * makes its row and lse NaN.  A channel with an infinite visible value is infinite
+ * in a cache of the rows' own type if that token's weight is 2^-100 of the largest
+ * or more; else, as in quantised caches, infinite or NaN.  Weights below 2^-126 of
+ * the largest count as zero.  Sums are fp32 and divided last: finite values of
+ * 2^127 / lengths[b] or more may overflow.  What lies in places that are not
+ * visible, NaN included, has no influence.  lengths beyond the table's reach
+ * count as that.
  *   q, out  head h of sequence b at b * stride_b + h * stride_h, d contiguous
  *           channels (dtype)
  *   lengths [B] int32; lse [B, Hq] fp32, or NULL

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import hybrid_oracle as oracle
-from layer_oracle import U
+from layer_oracle import U, check
 from test_gpu_hybrid import i32, n, to_pool
 from test_gpu_layer import Rng, _dtype, _torch
 
@@ -56,3 +56,85 @@ def test_attention_weights_keep_their_digits(form):
     got = n(y)
     off = (got < np.minimum(lo, hi)) | (got > np.maximum(lo, hi))
     assert not off.any(), f"{off.sum()} of {off.size} outputs are not the nearest"
+
+
+def spread(B, L, Hk, page, d):
+    """Pages of B sequences of up to L tokens, one after the other: (a table, k and v of zeros)."""
+    width = -(-L // page)
+    return np.arange(B * width).reshape(B, width), *(np.zeros((B * width, Hk, page, d)) for _ in range(2))
+
+
+FAR = [(40, 2, 35), (40, 35, 2), (200, 7, 8), (200, 150, 149), (5000, 3, 4200), (5000, 4200, 3), (5000, 1000, 1001)]
+
+
+@pytest.mark.parametrize("kind,form", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "mxfp8"), ("f32", "mxfp8"), ("bf16", "mxfp4")])
+def test_attention_of_far_values_whose_weight_vanishes(kind, form):
+    """A value near the type's end at a token whose weight is zero in 32 bits adds nothing, wherever the largest score
+    lies: before it, behind it, in another wave or another run of tiles."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    rng = Rng(22)
+    Hk, d, page = 2, 64, 64
+    for L, top, far in FAR:
+        table, k, v = spread(1, L, Hk, page, d)
+        k[top // page, :, top % page, 0] = 18.75  # a score of 300 (288 in 8 or 4 bits): other weights are e^-288 at most
+        v[top // page, :, top % page] = rng.g.integers(-3, 4, (Hk, d))
+        v[far // page, :, far % page, ::2] = 1.75 * 2.0 ** 126
+        cache, kk, vv = cache_of(k, v, form)
+        q = torch.zeros((1, 4, d), dtype=_dtype(kind), device="cuda")
+        q[..., 0] = 16
+        lse = torch.empty((1, 4), device="cuda")
+        y = gdn.attention_step(q, cache, i32(table), i32([L]), scale=1.0, lse=lse)
+        want = np.repeat(vv[top // page, :, top % page], 2, 0)[None]  # one weight of exactly one
+        check(n(y), want, np.zeros_like(want), kind, f"{L} {top} {far}")
+        score = np.full((1, 4), 16 * kk[top // page, 0, top % page, 0])
+        check(n(lse), score, 4 * U * score, "f32", "lse")  # (log2 e, its product, ln 2 and its product)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_attention_of_infinite_values_beside_far_scores(kind):
+    """An infinite value's channel is infinite while its weight is above 2^-100 of the largest, and no number where it is
+    smaller; the other channels are as ever."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    rng = Rng(23)
+    Hk, d, page, c = 2, 64, 64, 9
+    for L, top, far in FAR:
+        for score in (40.0, 300.0):  # weights of e^-40 = 2^-58 and of zero in 32 bits
+            table, k, v = spread(1, L, Hk, page, d)
+            v[:] = rng.g.standard_normal(v.shape)
+            k[top // page, :, top % page, 0] = score / 16
+            v[far // page, 0, far % page, c] = np.inf
+            v[far // page, 1, far % page, c] = -np.inf
+            cache, kk, vv = cache_of(k, v, kind)
+            q = torch.zeros((1, 2, d), dtype=_dtype(kind), device="cuda")
+            q[..., 0] = 16
+            y = n(gdn.attention_step(q, cache, i32(table), i32([L]), scale=1.0))[0]
+            if score == 40.0:
+                assert np.isposinf(y[0, c]) and np.isneginf(y[1, c]), (L, top, far)
+            else:
+                assert not np.isfinite(y[:, c]).any() and not np.isneginf(y[0, c]) and not np.isposinf(y[1, c])
+            rest = np.delete(np.arange(d), c)
+            for h in range(Hk):
+                rows = vv[:, h].reshape(-1, d)[:L][:, rest]
+                (o, oe), _ = oracle.attend(n(q)[0, h: h + 1, :1], kk[:, h].reshape(-1, d)[:L, :1], rows, 1.0, False)
+                check(y[h: h + 1, rest], o, oe, kind, f"{L} {top} {far} {score}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [3, 200, 5000])
+def test_attention_of_infinite_values_without_a_weight(kind, L):
+    """Every score minus infinity: zero, infinite values or not."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    table, k, v = spread(2, L, 1, 32, 64)
+    k[..., 0] = -np.inf
+    v[..., 3], v[..., 4] = np.inf, -np.inf
+    cache, _, _ = cache_of(k, v, kind)
+    q = torch.ones((2, 2, 64), dtype=_dtype(kind), device="cuda")
+    lse = torch.empty((2, 2), device="cuda")
+    y = gdn.attention_step(q, cache, i32(table), i32([L, L // 2]), lse=lse)
+    assert not n(y).any() and np.isneginf(n(lse)).all()
