@@ -32,7 +32,7 @@ __device__ __forceinline__ unsigned four_bytes(unsigned s) {
 template <typename MT, int FORMAT, bool WRITE, bool ALIGNED, bool ONCE>
 __global__ __launch_bounds__(kThreads) void kv_kernel(KvArgs a) {
   const unsigned shares = (unsigned)((a.Hk + a.heads - 1) / a.heads);
-  const int64_t item = blockIdx.x / shares;
+  const int64_t item = a.first + blockIdx.x / shares;
   const int h0 = (int)(blockIdx.x % shares) * a.heads;
   SeqItem s;
   if (a.off) {
@@ -131,20 +131,23 @@ __global__ __launch_bounds__(kThreads) void kv_kernel(KvArgs a) {
 }
 
 template <typename MT, int FORMAT, bool WRITE, bool ONCE>
-hipError_t kv_launch(const KvArgs& a, int64_t blocks, bool aligned, hipStream_t stream) {
-  if (aligned)
-    hipLaunchKernelGGL((kv_kernel<MT, FORMAT, WRITE, true, ONCE>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((kv_kernel<MT, FORMAT, WRITE, false, ONCE>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
+hipError_t kv_launch(const KvArgs& given, int64_t items, bool aligned, hipStream_t stream) {
+  KvArgs a = given;
+  return in_launches(items, (a.Hk + a.heads - 1) / a.heads, kThreads, [&](int64_t first, dim3 blocks) {
+    a.first = first;
+    if (aligned)
+      hipLaunchKernelGGL((kv_kernel<MT, FORMAT, WRITE, true, ONCE>), blocks, dim3(kThreads), 0, stream, a);
+    else
+      hipLaunchKernelGGL((kv_kernel<MT, FORMAT, WRITE, false, ONCE>), blocks, dim3(kThreads), 0, stream, a);
+  });
 }
 
 template <typename MT, int FORMAT>
-hipError_t kv_for(const KvArgs& a, int64_t blocks, bool write, bool aligned, hipStream_t stream) {
-  if (write) return kv_launch<MT, FORMAT, true, false>(a, blocks, aligned, stream);
+hipError_t kv_for(const KvArgs& a, int64_t items, bool write, bool aligned, hipStream_t stream) {
+  if (write) return kv_launch<MT, FORMAT, true, false>(a, items, aligned, stream);
   const int64_t bytes = 2 * (a.off ? a.T : a.B * a.T) * a.Hk * row_bytes(FORMAT, a.d);
-  return bytes >= kOnceBytes ? kv_launch<MT, FORMAT, false, true>(a, blocks, aligned, stream)
-                             : kv_launch<MT, FORMAT, false, false>(a, blocks, aligned, stream);
+  return bytes >= kOnceBytes ? kv_launch<MT, FORMAT, false, true>(a, items, aligned, stream)
+                             : kv_launch<MT, FORMAT, false, false>(a, items, aligned, stream);
 }
 
 }  // namespace
@@ -159,12 +162,10 @@ hipError_t launch_kv(const KvArgs& given, int format, bool write, bool aligned, 
   a.heads = a.heads < 1 ? 1 : a.heads > a.Hk ? a.Hk : a.heads;
   a.chunks = (a.T + ((int64_t)1 << a.chunk_bits) - 1) >> a.chunk_bits;
   const int64_t items = a.off ? (a.T >> a.chunk_bits) + a.B : a.B * a.chunks;
-  const int64_t blocks = items * ((a.Hk + a.heads - 1) / a.heads);
-  if (items > 0x7FFFFFFF || !grid_fits(blocks, kThreads)) return hipErrorNotSupported;
   switch (format) {
-    case GDN_KV_MXFP8: return kv_for<MT, GDN_KV_MXFP8>(a, blocks, write, aligned, stream);
-    case GDN_KV_MXFP4: return kv_for<MT, GDN_KV_MXFP4>(a, blocks, write, aligned, stream);
-    default: return kv_for<MT, sizeof(MT) == 4 ? GDN_KV_F32 : GDN_KV_BF16>(a, blocks, write, aligned, stream);
+    case GDN_KV_MXFP8: return kv_for<MT, GDN_KV_MXFP8>(a, items, write, aligned, stream);
+    case GDN_KV_MXFP4: return kv_for<MT, GDN_KV_MXFP4>(a, items, write, aligned, stream);
+    default: return kv_for<MT, sizeof(MT) == 4 ? GDN_KV_F32 : GDN_KV_BF16>(a, items, write, aligned, stream);
   }
 }
 

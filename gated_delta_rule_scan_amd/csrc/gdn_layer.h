@@ -117,6 +117,7 @@ struct KvArgs {
   int chunk_bits;        // log2 of the tokens per workgroup
   int heads;             // heads per workgroup
   int64_t chunks;        // runs of tokens per sequence (not packed)
+  int64_t first;         // of the launch's runs
 };
 
 struct AttendArgs {
@@ -137,6 +138,7 @@ struct AttendArgs {
   int q_aligned;         // every row of q starts on 16 bytes
   int once;              // pools are read past the caches
   float scale;
+  int64_t first;         // of the launch's items (sequences, in the join)
   int64_t items;         // runs of tiles; the workspace, or null where no sequence can be split:
   int32_t* plan;         // [B][2] first item and items of a sequence
   float* parts;          // [items][Hq][d] sums of weighted values
@@ -169,6 +171,7 @@ struct NormArgs {
   int64_t chunk;         // rows per workgroup
   int64_t chunks;        // workgroups per sequence (not packed)
   int64_t items;         // workgroups
+  int64_t first;         // of the launch's (of the gradients, in their sums)
   // backward: the sums over a workgroup's rows [item][sums][D], and where
   // the gradients' sums go (null: not wanted)
   float* parts;
@@ -209,6 +212,19 @@ hipError_t launch_step(const StepArgs& a, int dk, hipStream_t stream);
 // Blocks of `threads` that one launch may have (the launch's work items are
 // counted in 32 bits).
 inline bool grid_fits(int64_t blocks, int threads) { return blocks <= (((int64_t)1 << 32) - 1) / threads && blocks <= 0x7FFFFFFF; }
+
+// Work of `count` parts, each of `blocks` blocks, in as many launches as that
+// takes: launch(first part, its blocks).
+template <typename Launch>
+hipError_t in_launches(int64_t count, int64_t blocks, int threads, Launch launch) {
+  const int64_t most = (((int64_t)1 << 32) - 1) / threads / blocks;
+  for (int64_t at = 0; at < count; at += most) {
+    launch(at, dim3((unsigned)((count - at < most ? count - at : most) * blocks)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 // ---- small device helpers ----
 

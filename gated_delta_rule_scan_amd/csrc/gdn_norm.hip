@@ -267,12 +267,13 @@ struct Run {
 
 template <int R>
 __device__ __forceinline__ Run run_of(const NormArgs& a, int sub) {
+  const int64_t item = a.first + blockIdx.x;
   SeqItem s;
   if (a.off) {
-    s = find_packed(a.off, a.B, a.T, a.chunk, blockIdx.x);
+    s = find_packed(a.off, a.B, a.T, a.chunk, item);
   } else {
-    s.b = blockIdx.x / a.chunks;
-    s.chunk = blockIdx.x % a.chunks;
+    s.b = item / a.chunks;
+    s.chunk = item % a.chunks;
     s.row0 = 0;
     s.len = a.T;
   }
@@ -481,7 +482,7 @@ __global__ __launch_bounds__(threads_of(LANES), (waves_at_once(LANES / 64, E, si
   }
   // the sums over these rows: zero where the run is empty.  Rows that were
   // taken side by side are added first.
-  float* part = a.parts + blockIdx.x * (int64_t)a.sums * a.D;
+  float* part = a.parts + (a.first + blockIdx.x) * a.sums * a.D;
   auto put = [&](float (&x)[E]) {
     if constexpr (L::kRows > 1) {
       __shared__ float side[L::kRows - 1][E * LANES];
@@ -519,7 +520,7 @@ __global__ __launch_bounds__(512) void norm_sums_kernel(NormArgs a) {
   const int half = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t tiles = (a.D + 31) / 32;
   const int64_t c = (blockIdx.x % tiles) * 32 + lane;
-  int64_t which = blockIdx.x / tiles;  // gates, then the others
+  int64_t which = a.first + blockIdx.x / tiles;  // gates, then the others
   const int64_t gates = a.dgate ? (a.gate_sb ? a.B : 1) : 0;
   int64_t first = 0, last = a.items;
   int kind = 0;
@@ -587,12 +588,14 @@ hipError_t norm_by_width(const NormArgs& a, hipStream_t stream) {
   if constexpr (w.D < 16384)
     if (a.D > w.D) return norm_by_width<MT, WHOLE, BACKWARD, I + 1>(a, stream);
   constexpr int kThreads = threads_of(w.lanes);
-  if (!grid_fits(a.items, kThreads)) return hipErrorNotSupported;
-  if constexpr (BACKWARD)
-    hipLaunchKernelGGL((norm_back_kernel<MT, w.lanes, w.E, WHOLE>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((norm_kernel<MT, w.lanes, w.E, WHOLE>), dim3((unsigned)a.items), dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
+  NormArgs part = a;
+  return in_launches(a.items, 1, kThreads, [&](int64_t first, dim3 blocks) {
+    part.first = first;
+    if constexpr (BACKWARD)
+      hipLaunchKernelGGL((norm_back_kernel<MT, w.lanes, w.E, WHOLE>), blocks, dim3(kThreads), 0, stream, part);
+    else
+      hipLaunchKernelGGL((norm_kernel<MT, w.lanes, w.E, WHOLE>), blocks, dim3(kThreads), 0, stream, part);
+  });
 }
 
 template <typename MT, bool BACKWARD>
@@ -623,21 +626,19 @@ NormPlan norm_plan(int64_t B, int64_t T, int64_t D, bool half, bool packed, bool
 
 template <typename MT>
 hipError_t launch_norm(const NormArgs& a, bool aligned, hipStream_t stream) {
-  return a.items ? norm_for<MT, false>(a, aligned, stream) : hipSuccess;
+  return norm_for<MT, false>(a, aligned, stream);
 }
 
 template <typename MT>
 hipError_t launch_norm_back(const NormArgs& a, bool aligned, hipStream_t stream) {
-  if (a.items) {
-    const hipError_t e = norm_for<MT, true>(a, aligned, stream);
-    if (e != hipSuccess) return e;
-  }
+  const hipError_t e = norm_for<MT, true>(a, aligned, stream);
+  if (e != hipSuccess) return e;
   const int64_t outs = (a.dgate ? (a.gate_sb ? a.B : 1) : 0) + (a.dpost ? 1 : 0) + (a.dweight ? 1 : 0);
-  if (!outs) return hipSuccess;
-  const int64_t blocks = outs * ((a.D + 31) / 32);
-  if (!grid_fits(blocks, 512)) return hipErrorNotSupported;
-  hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)blocks), dim3(512), 0, stream, a);
-  return hipGetLastError();
+  NormArgs part = a;
+  return in_launches(outs, (a.D + 31) / 32, 512, [&](int64_t first, dim3 blocks) {
+    part.first = first;
+    hipLaunchKernelGGL(norm_sums_kernel, blocks, dim3(512), 0, stream, part);
+  });
 }
 
 template hipError_t launch_norm<float>(const NormArgs&, bool, hipStream_t);

@@ -519,7 +519,7 @@ gdn_status_t gdn_step(const gdn_step_problem_t* p, const void* q, const void* k,
  * that round to 2^128 read back as infinities.  A pool of zero bytes holds zeros.
  *
  * Supported: d 64, 128 or 256; page a power of two, 16 to 1024; Hk <= 65536;
- * B * T < 2^31. */
+ * B * T and B * table_width < 2^31. */
 typedef enum { GDN_KV_F32 = 0, GDN_KV_BF16 = 1, GDN_KV_MXFP8 = 2, GDN_KV_MXFP4 = 3 } gdn_kv_format_t;
 
 /* Rows of K and V into the cache, and back out of it.
@@ -565,7 +565,7 @@ gdn_status_t gdn_kv_read(const gdn_kv_problem_t* p, const void* k_cache, const v
  *   q, out  head h of sequence b at b * stride_b + h * stride_h, d contiguous
  *           channels (dtype)
  *   lengths [B] int32; lse [B, Hq] fp32, or NULL
- * Supported: as above, Hk divides Hq, Hq <= 65536. */
+ * Supported: as above, Hk divides Hq, Hq <= 65536, B * Hq < 2^31. */
 typedef struct {
   int64_t B, Hq, Hk, d;
   int64_t pages, page, table_width;
