@@ -44,7 +44,13 @@ constexpr int kLeast = kWaves;     // tiles of an item: one a wave
 // against 10.5), or at most 64 and there are workgroups for most compute units
 // without (2048 tokens: 8 sequences 22.9 against 15.9, 32 33.1 against 35.5, 128
 // 105 against 115).
-constexpr int kShort = 16, kWhole = 64;
+// Nor from 1024 sequences on: each workgroup of a cut call goes through all
+// lengths, which alone keep the card busy (to 4096 tokens, 32 query heads on 8:
+// 1024 sequences 1202 against 1886, 4096 4645 against 12664; to 256 tokens in a
+// table for 32768: 193 against 859.  One long sequence among short ones would
+// rather be cut below that: 32768 among 512 of up to 256, 4 query heads on one,
+// 280 against 46; among 2048 281 against 392).
+constexpr int kShort = 16, kWhole = 64, kMany = 1024;
 // Where they are not cut, eight waves take each (if the registers allow it) for
 // up to kFew workgroups or beyond kLong tiles, else four, of which a compute unit
 // holds more: 512 tokens, 128 sequences of 8 heads 39 us with eight, 33 with four;
@@ -774,7 +780,7 @@ AttendPlan attend_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t d, bool half, 
   if (window && window + sinks < reach) most = window + sinks + 2 * kTile;
   const int64_t tiles = (most + kTile - 1) / kTile;
   // not cut: one kernel and no workspace
-  if (tiles <= kShort || (tiles <= kWhole && B * Hk * shares >= 3 * tiles)) {
+  if (B >= kMany || tiles <= kShort || (tiles <= kWhole && B * Hk * shares >= 3 * tiles)) {
     p.items = B;
     return p;
   }

@@ -3,6 +3,7 @@ in calls that need fewer."""
 import pytest
 
 from layer_oracle import U
+from test_gpu_hybrid import _attention_case, _check_attention, _expect, i32
 from test_gpu_layer import _torch
 
 pytestmark = pytest.mark.gpu
@@ -69,3 +70,16 @@ def test_cache_rows_of_more_sequences_than_a_launch_takes():
     assert not cache.k.view(-1, d)[B:].any()
     back = gdn.kv_read(cache, table, 1, start)
     assert torch.equal(back[0][:, 0], k) and torch.equal(back[1][:, 0], v)
+
+
+@pytest.mark.parametrize("kind,form", [("bf16", "bf16"), ("f32", "mxfp8")])
+def test_attention_of_a_thousand_sequences_in_a_wide_table(kind, form):
+    """Not cut, short ones and one long one."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    lens = [3, 40, 0, 17] * 256 + [4100, 700]
+    q, cache, table, kv, vv = _attention_case(kind, form, lens, 4, 2, 64, 64, 0, 0, 31, width=100)
+    lse = torch.empty((len(lens), 4), device="cuda")
+    y = gdn.attention_step(q, cache, i32(table), i32(lens), lse=lse)
+    _check_attention(y, lse, _expect(q, table, lens, kv, vv, 0.125, 0, 0, kind), kind)
