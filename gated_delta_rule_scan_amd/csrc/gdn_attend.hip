@@ -262,7 +262,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : at_once(D, QT, sizeof(
   const int g = lane >> 4, n = lane & 15;
   const int G = a.Hq / a.Hk, shares = (G + 16 * QT - 1) / (16 * QT);
   const int kh = (int)(blockIdx.x % a.Hk), share = (int)(blockIdx.x / a.Hk % shares);
-  const int64_t item = blockIdx.x / ((unsigned)a.Hk * shares);
+  const int64_t item = a.first + blockIdx.x / ((unsigned)a.Hk * shares);
   // Page numbers of a tile's halves, from its position, as the table has them:
   // they are looked at where they are used, a tile later (see below).
   struct Pages { int p[2]; };
@@ -669,7 +669,7 @@ template <typename MT, int D>
 __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a) {
   constexpr int N = D / 64, U = 64 / kJoinWaves;
   __shared__ float part[kJoinWaves][D];
-  const int64_t b = blockIdx.x / a.Hq;
+  const int64_t b = a.first + blockIdx.x / a.Hq;
   const int h = (int)(blockIdx.x % a.Hq);
   const int first = a.plan[2 * b], chunks = a.plan[2 * b + 1];
   if (chunks == 1) return;
@@ -730,23 +730,25 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a) {
 }
 
 template <typename MT, int FORMAT, int D, int QT>
-hipError_t attend_launch(const AttendArgs& a, hipStream_t stream) {
+hipError_t attend_launch(const AttendArgs& given, hipStream_t stream) {
+  AttendArgs a = given;
   const int64_t shares = (a.Hq / a.Hk + 16 * QT - 1) / (16 * QT);
-  const int64_t blocks = a.items * a.Hk * shares;
-  if (!grid_fits(blocks, 8 * 64) || !grid_fits(a.B * a.Hq, kJoinWaves * 64)) return hipErrorNotSupported;
+  const auto launch = [&](auto kernel, int waves) {
+    return in_launches(a.items, a.Hk * shares, waves * 64, [&](int64_t first, dim3 blocks) {
+      a.first = first;
+      hipLaunchKernelGGL(kernel, blocks, dim3(waves * 64), 0, stream, a);
+    });
+  };
   if constexpr (D < 256 && D * QT * sizeof(MT) <= 512)
-    if (!a.plan && a.tiles > kWaves && (blocks <= kFew || a.tiles > kLong)) {
-      hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, 8, false>), dim3((unsigned)blocks), dim3(8 * 64), 0, stream, a);
-      return hipGetLastError();
-    }
-  if (a.plan && a.once)
-    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, kWaves, true>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
-  else
-    hipLaunchKernelGGL((attend_kernel<MT, FORMAT, D, QT, kWaves, false>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, a);
-  const hipError_t e = hipGetLastError();
+    if (!a.plan && a.tiles > kWaves && (a.items * a.Hk * shares <= kFew || a.tiles > kLong))
+      return launch(attend_kernel<MT, FORMAT, D, QT, 8, false>, 8);
+  const hipError_t e = a.plan && a.once ? launch(attend_kernel<MT, FORMAT, D, QT, kWaves, true>, kWaves)
+                                        : launch(attend_kernel<MT, FORMAT, D, QT, kWaves, false>, kWaves);
   if (e != hipSuccess || !a.plan) return e;
-  hipLaunchKernelGGL((join_kernel<MT, D>), dim3((unsigned)(a.B * a.Hq)), dim3(kJoinWaves * 64), 0, stream, a);
-  return hipGetLastError();
+  return in_launches(a.B, a.Hq, kJoinWaves * 64, [&](int64_t first, dim3 blocks) {
+    a.first = first;
+    hipLaunchKernelGGL((join_kernel<MT, D>), blocks, dim3(kJoinWaves * 64), 0, stream, a);
+  });
 }
 
 // 32 query heads a workgroup where more than 16 share a head of the cache; 16

@@ -1,5 +1,5 @@
-"""The largest batches of the cache and the seam on the GPU: more workgroups than one launch takes, against the same rows
-in calls that need fewer."""
+"""The largest batches of the cache, its attention and the seam on the GPU: more workgroups than one launch takes,
+against the same rows in calls that need fewer; more sequences than are cut."""
 import pytest
 
 from layer_oracle import U
@@ -70,6 +70,24 @@ def test_cache_rows_of_more_sequences_than_a_launch_takes():
     assert not cache.k.view(-1, d)[B:].any()
     back = gdn.kv_read(cache, table, 1, start)
     assert torch.equal(back[0][:, 0], k) and torch.equal(back[1][:, 0], v)
+
+
+def test_attention_of_more_heads_than_a_launch_takes():
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    H, d, page = 128, 64, 16
+    B = MOST // H + 30
+    q = randn(1, B, H, d)
+    cache = gdn.KVCache(randn(2, 5, H, page, d), randn(3, 5, H, page, d))
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None] % 5
+    lens = torch.arange(B, dtype=torch.int32, device="cuda") % 17
+    lse = torch.empty((B, H), device="cuda")
+    y = gdn.attention_step(q, cache, table.contiguous(), lens, lse=lse)
+    for i in (slice(0, B // 2), slice(B // 2, B)):
+        part = torch.empty_like(lse[i])
+        assert torch.equal(y[i], gdn.attention_step(q[i], cache, table[i].contiguous(), lens[i], lse=part))
+        assert torch.equal(lse[i], part)
 
 
 @pytest.mark.parametrize("kind,form", [("bf16", "bf16"), ("f32", "mxfp8")])
