@@ -207,7 +207,8 @@ __device__ __forceinline__ void words(const uint8_t* p, unsigned (&w)[N]) {
   for (int i = 0; i < N; ++i) w[i] = v[i];
 }
 
-// Two channels from codes, as two bf16 values.
+// Two channels from codes, as two bf16 values.  The instructions take the
+// exponent of `scale` alone, the scale byte as it is: 0 is 2^-127 and 255 NaN.
 template <int FORMAT, int AT>  // AT: which pair of the word
 __device__ __forceinline__ unsigned two(unsigned w, float scale) {
   if constexpr (FORMAT == GDN_KV_BF16)

@@ -25,8 +25,10 @@ __device__ __forceinline__ int64_t kv_row(const int32_t* table, int64_t width, i
   return ((page * Hk + h) << page_bits) + (pos & (((int64_t)1 << page_bits) - 1));
 }
 
-// a scale byte as a float; 255 is NaN
-__device__ __forceinline__ float kv_scale(unsigned s) { return __builtin_bit_cast(float, s == 255 ? 0x7FC00000u : s << 23); }
+// a scale byte s as a float, 2^(s - 127): below the least normal number for 0; 255 is NaN
+__device__ __forceinline__ float kv_scale(unsigned s) {
+  return __builtin_bit_cast(float, s == 255 ? 0x7FC00000u : s == 0 ? 0x00400000u : s << 23);
+}
 
 // Bits of max|x| over 8 channels (NaN and infinities largest), then over the
 // four lanes of a quad, which hold a block.

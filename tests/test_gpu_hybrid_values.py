@@ -138,3 +138,72 @@ def test_attention_of_infinite_values_without_a_weight(kind, L):
     lse = torch.empty((2, 2), device="cuda")
     y = gdn.attention_step(q, cache, i32(table), i32([L, L // 2]), lse=lse)
     assert not n(y).any() and np.isneginf(n(lse)).all()
+
+
+MX = [("bf16", "mxfp8"), ("f32", "mxfp8"), ("bf16", "mxfp4"), ("f32", "mxfp4")]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind,form", MX)
+def test_attention_of_visible_blocks_that_are_nan(kind, form, d):
+    """Scale byte 255 in a key makes the rows that see it NaN, in a value its 32 channels; whatever the codes are."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    rng = Rng(24)
+    B, L, Hk, page = 8, 150, 2, 64
+    table, k, v = spread(B, L, Hk, page, d)
+    k[:], v[:] = rng.g.standard_normal(k.shape), rng.g.standard_normal(v.shape)
+    k[0, 0, 5], v[3, 0, 5] = 0, 0  # codes of zero
+    cache, kk, vv = cache_of(k, v, form)
+    blocks = [0, d // 32 - 1, 1, 0]
+    bad = [(b, [5, 17, 70, 149][b % 4], blocks[b % 4]) for b in range(B)]  # sequence, position, block; head 0
+    for b, at, block in bad:
+        cache[2 if b < 4 else 3][table[b, at // page], 0, at % page, block] = 255
+    q = rng.t(B, 4, d, kind=kind)
+    lse = torch.empty((B, 4), device="cuda")
+    y, lse_ = n(gdn.attention_step(q, cache, i32(table), i32([L] * B), lse=lse)), n(lse)
+    for b, at, block in bad:
+        nan = np.zeros((4, d), bool)
+        nan[:2, slice(None) if b < 4 else slice(32 * block, 32 * block + 32)] = True
+        assert np.array_equal(np.isnan(y[b]), nan), (b, at, block)
+        assert np.array_equal(np.isnan(lse_[b]), [b < 4, b < 4, False, False])
+        for h in range(2):
+            rows = [a[table[b], h].reshape(-1, d)[:L] for a in (kk, vv)]
+            (o, oe), _ = oracle.attend(n(q)[b, 2 * h: 2 * h + 2], *rows, d ** -0.5, False)
+            keep = ~nan[2 * h: 2 * h + 2]
+            check(y[b, 2 * h: 2 * h + 2][keep], o[keep], oe[keep], kind, f"{b} {h}")
+    gk, gv = gdn.kv_read(cache, i32(table), L)
+    assert np.isnan(n(gk)).sum() == np.isnan(n(gv)).sum() == 4 * 32
+
+
+@pytest.mark.parametrize("kind,form", MX)
+def test_blocks_of_the_least_scales(kind, form):
+    """Scale bytes 0 to 16, which kv_write does not choose: 2^-127 to 2^-111."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    d, page = 64, 32
+    codes = np.zeros((1, 1, page, d), np.uint8)
+    top = {"mxfp8": 126, "mxfp4": 7}[form]  # 448, 6
+    codes[0, 0, :, 0] = top
+    codes[0, 0, :, 1:32] = np.arange(1, 32) * (4 if form == "mxfp8" else 1) % (top + 1)
+    codes[0, 0, :, 32] = top
+    scales = np.full((1, 1, page, 2), 127, np.uint8)
+    scales[0, 0, :, 0] = np.arange(page) % 17
+    pool = to_pool(codes, form)
+    cache = (pool, pool, *(torch.from_numpy(scales).cuda() for _ in range(2)))
+    want = oracle.decode(codes, scales, form)[0, 0]
+    for dtype in (torch.float32, torch.bfloat16):
+        got = gdn.kv_read(cache, i32([[0]]), page, dtype=dtype)
+        for t in got:
+            assert torch.equal(t[0, :, 0].cpu(), torch.from_numpy(want).to(dtype)), dtype  # (exact in fp32)
+    # attention of the one token of each byte (a window of one): lse is its score, of ordinary size by query and scale
+    q = torch.zeros((1, 1, d), dtype=_dtype(kind), device="cuda")
+    q[..., 0] = 2.0 ** 120
+    lse = torch.empty((1, 1), device="cuda")
+    for s in range(page):
+        scale = 2.0 ** -(s % 17)
+        gdn.attention_step(q, cache, i32([[0]]), i32([s + 1]), scale=scale, window=1, lse=lse)
+        x = scale * 2.0 ** 120 * want[s, 0]
+        check(n(lse), np.array([[x]]), np.array([[8 * U * x]]), "f32", f"byte {s % 17}")
