@@ -774,6 +774,20 @@ PyObject* residual_norm(PyObject* const* a) {
   return pair(h.defined() ? h : q.x, n);
 }
 
+// A gradient, as autograd hands them on: one whose rows are not contiguous (that
+// of a sum is one value, expanded) is copied.
+Tensor gradient(const Stream& s, const Tensor& t, const Tensor& x, const char* name) {
+  const bool fits = t.scalar_type() == x.scalar_type() && t.sizes() == x.sizes() && t.device() == x.device();
+  if (!fits || !t.numel() || t.size(-1) == 1 || t.stride(-1) == 1) {
+    rows(t, x.sizes(), x, name);
+    return t;
+  }
+  const c10::DeviceGuard device(x.device());
+  if (!s.other) return t.contiguous();
+  const c10::StreamGuard guard(s.stream);
+  return t.contiguous();
+}
+
 // dh, dn, then x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets, then dx, dy, workspace, stream
 PyObject* residual_norm_backward(PyObject* const* a) {
   Seam q(a + 2);
@@ -781,11 +795,12 @@ PyObject* residual_norm_backward(PyObject* const* a) {
   const Tensor *dh = tensor(a[0], "dh"), *dn = tensor(a[1], "dn"), *dx = tensor(a[10], "dx"), *dy = tensor(a[11], "dy");
   if (!dn != !q.weight) refuse("dn and weight go together");
   if (!dh && !dn) refuse("dh or dn must be given");
-  if (dh) rows(*dh, q.x.sizes(), q.x, "dh"), q.stride(*dh, &p.h_stride_b, &p.h_stride_t);
-  if (dn) rows(*dn, q.x.sizes(), q.x, "dn"), q.stride(*dn, &p.n_stride_b, &p.n_stride_t);
   if (dy && !q.y) refuse("dy without y");
   if (q.y && !dx != !dy && q.off) refuse("dx and dy go together in a packed batch");
   const Stream s(a[13], q.x);
+  Tensor gh, gn;
+  if (dh) gh = gradient(s, *dh, q.x, "dh"), q.stride(gh, &p.h_stride_b, &p.h_stride_t);
+  if (dn) gn = gradient(s, *dn, q.x, "dn"), q.stride(gn, &p.n_stride_b, &p.n_stride_t);
   const Tensor gx = output(s, dx, q.x, "dx");
   q.stride(gx, &p.dx_stride_b, &p.dx_stride_t);
   Tensor gy, gg, gp, gw;
@@ -801,9 +816,9 @@ PyObject* residual_norm_backward(PyObject* const* a) {
   p.workspace = workspace(a[12], s, (int64_t)f_norm_workspace(&p), q.x, &mine, &p.workspace_bytes);
   p.stream = s.raw;
   const c10::DeviceGuard guard(q.x.device());
+  auto rows_of = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
   auto at = [](const Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; };
-  check(f_norm_backward(&p, q.x.data_ptr(), ptr(q.y), ptr(dh), ptr(dn), gx.data_ptr(), gy.defined() ? gy.data_ptr() : nullptr,
-                        at(gg), at(gp), at(gw)));
+  check(f_norm_backward(&p, q.x.data_ptr(), ptr(q.y), rows_of(gh), rows_of(gn), gx.data_ptr(), rows_of(gy), at(gg), at(gp), at(gw)));
   return Py_BuildValue("(NNNNN)", THPVariable_Wrap(gx), none_or(gy), none_or(gg), none_or(gp), none_or(gw));
 }
 

@@ -99,7 +99,8 @@ def residual_norm(x, y=None, gate=None, post_weight=None, weight=None, residual_
 def residual_norm_backward(dh, dn, x, y=None, gate=None, post_weight=None, weight=None, residual_scale: float = 1.0,
                            eps: float = 1e-6, seq_offsets=None, dx=None, dy=None, workspace=None, stream=None) -> Tuple:
     """The gradients of ``residual_norm``: dh, dn those of its outputs (dh None: zero; dn goes with ``weight``), the
-    others its arguments.  ``dx`` may be dh.  ``workspace``: a uint8 tensor (``gdn_norm_workspace_bytes``); a smaller
+    others its arguments; where their rows are not contiguous (a sum's gradient is one value, expanded) they are copied
+    first.  ``dx`` may be dh.  ``workspace``: a uint8 tensor (``gdn_norm_workspace_bytes``); a smaller
     one, or None, is replaced by one allocated here.  Returns (dx, dy, dgate, dpost_weight, dweight), each None where the
     argument was; the last three float32."""
     return _native().residual_norm_backward(dh, dn, x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets, dx,
