@@ -6,6 +6,7 @@
 // position; the entry points' addresses come from the loaded library (init).
 #include <ATen/core/Tensor.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -747,11 +748,24 @@ struct Seam {
   }
 };
 
-// x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets, out, norm_out, stream
+// (for autograd, which may have kept the tensor's values for a gradient)
+void written(const Tensor* t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
+// x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets, out, norm_out, stream; None where a graph is
+// wanted: an argument requires gradients, and they are enabled
 PyObject* residual_norm(PyObject* const* a) {
   Seam q(a);
   gdn_norm_problem_t& p = q.p;
   const Tensor *out = tensor(a[8], "out"), *nout = tensor(a[9], "norm_out");
+  if (c10::AutogradState::get_tls_state().get_grad_mode()) {
+    bool graph = false;
+    for (const Tensor* t : {&q.x, q.y, q.gate, q.post, q.weight}) graph = graph || (t && t->requires_grad());
+    if (graph && (out || nout || a[10] != Py_None))
+      refuse("out, norm_out and stream do not go with gradients (under torch.no_grad they do; torch.cuda.stream sets a stream)");
+    if (graph) Py_RETURN_NONE;
+  }
   if (nout && !q.weight) refuse("norm_out without weight");
   // without a block's output and a scale the residual stream stays what it is
   const bool moves = q.y || out || p.residual_scale != 1.0f;
@@ -771,6 +785,7 @@ PyObject* residual_norm(PyObject* const* a) {
   p.stream = s.raw;
   const c10::DeviceGuard guard(q.x.device());
   check(f_norm_forward(&p, q.x.data_ptr(), ptr(q.y), h.defined() ? h.data_ptr() : nullptr, n.defined() ? n.data_ptr() : nullptr));
+  written(out), written(nout);
   return pair(h.defined() ? h : q.x, n);
 }
 
@@ -819,6 +834,7 @@ PyObject* residual_norm_backward(PyObject* const* a) {
   auto rows_of = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
   auto at = [](const Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; };
   check(f_norm_backward(&p, q.x.data_ptr(), ptr(q.y), rows_of(gh), rows_of(gn), gx.data_ptr(), rows_of(gy), at(gg), at(gp), at(gw)));
+  written(dx), written(dy);
   return Py_BuildValue("(NNNNN)", THPVariable_Wrap(gx), none_or(gy), none_or(gg), none_or(gp), none_or(gw));
 }
 

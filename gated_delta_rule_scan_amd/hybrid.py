@@ -5,7 +5,8 @@ residual, norm) with its gradients (layouts and rules of ``include/gdn.h``).
 
 Checked and launched in native code like the operators of ``layer.py``, whose
 rules for ``stream``, packed batches (``seq_offsets``), strided views and rows
-of no sequence hold here too.
+of no sequence hold here too.  ``residual_norm`` takes part in autograd; the
+cache and its attention serve, and their results have no graph.
 """
 from __future__ import annotations
 
@@ -92,8 +93,38 @@ def residual_norm(x, y=None, gate=None, post_weight=None, weight=None, residual_
 
     x, y [B, T, D], [B, D] (a token each) or [T, D] packed with ``seq_offsets``; ``gate`` [D], or [B, D] (a gate for
     every sequence), float32; ``weight``, ``post_weight`` [D] float32.  ``out`` (of h) may be x.  Returns (h, n), n None
-    without ``weight``; without y, out and a residual scale h is x itself."""
-    return _native().residual_norm(x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets, out, norm_out, stream)
+    without ``weight``; without y, out and a residual scale h is x itself.
+
+    Where x, y or a parameter requires gradients (and they are enabled) the results have a graph, whose backward pass is
+    ``residual_norm_backward``; ``out``, ``norm_out`` and ``stream`` are refused then."""
+    got = _native().residual_norm(x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets, out, norm_out, stream)
+    if got is not None:
+        return got
+    got = _ResidualNorm.apply(x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets)
+    return got if len(got) == 2 else (x, got[0]) if y is None and residual_scale == 1.0 else (got[0], None)
+
+
+class _ResidualNorm(torch.autograd.Function):
+    """h and n of ``residual_norm``, those of them that it computes."""
+
+    @staticmethod
+    def forward(ctx, x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets):
+        h, n = _native().residual_norm(x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets, None, None, None)
+        ctx.save_for_backward(x, y, gate, post_weight, weight, seq_offsets)
+        ctx.numbers, ctx.h = (residual_scale, eps), h is not x
+        ctx.set_materialize_grads(False)
+        return tuple(t for t in (h if ctx.h else None, n) if t is not None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        x, y, gate, post_weight, weight, seq_offsets = ctx.saved_tensors
+        dh = grads[0] if ctx.h else None
+        dn = None if weight is None else grads[-1]
+        if dh is None and dn is None:
+            return (None,) * 8
+        got = residual_norm_backward(dh, dn, x, y, gate, post_weight, None if dn is None else weight, *ctx.numbers, seq_offsets)
+        return (*(g if need else None for g, need in zip(got, ctx.needs_input_grad)), None, None, None)
 
 
 def residual_norm_backward(dh, dn, x, y=None, gate=None, post_weight=None, weight=None, residual_scale: float = 1.0,
@@ -110,7 +141,7 @@ def residual_norm_backward(dh, dn, x, y=None, gate=None, post_weight=None, weigh
 def register_ops() -> None:
     """The calls as torch.library custom ops (torch.ops.gdn.kv_write, kv_read, attention_step, residual_norm,
     residual_norm_backward) with fake implementations for tracing; kv_write mutates the cache.  residual_norm's op
-    needs y and weight.  None has an autograd formula: residual_norm_backward is called by name."""
+    needs y and weight; it alone has an autograd formula."""
     op = torch.library.custom_op
     cache = "Tensor k_cache, Tensor v_cache, Tensor? k_scales, Tensor? v_scales"
 
@@ -155,11 +186,23 @@ def register_ops() -> None:
         schema="(Tensor x, Tensor y, Tensor? gate, Tensor? post_weight, Tensor weight, float residual_scale, float eps, "
                "Tensor? seq_offsets) -> (Tensor, Tensor)")
     def _norm(x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets):
-        return residual_norm(x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets)
+        with torch.no_grad():  # (the graph is the op's)
+            return residual_norm(x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets)
 
     @_norm.register_fake
     def _(x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets):
         return x.new_empty(x.shape), x.new_empty(x.shape)
+
+    def _keep(ctx, inputs, output):
+        *tensors, ctx.residual_scale, ctx.eps, offsets = inputs
+        ctx.save_for_backward(*tensors, offsets)
+
+    def _gradients(ctx, dh, dn):
+        *tensors, offsets = ctx.saved_tensors
+        got = torch.ops.gdn.residual_norm_backward(dh, dn, *tensors, ctx.residual_scale, ctx.eps, offsets)
+        return (*(None if t is None else g for g, t in zip(got, tensors)), None, None, None)
+
+    _norm.register_autograd(_gradients, setup_context=_keep)
 
     @op("gdn::residual_norm_backward", mutates_args=(), device_types="cuda",
         schema="(Tensor? dh, Tensor dn, Tensor x, Tensor y, Tensor? gate, Tensor? post_weight, Tensor weight, "
