@@ -196,7 +196,7 @@ __device__ __forceinline__ float over_groups_sum(float x) {
   return over_groups(x, [](float a, float b) { return a + b; });
 }
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+constexpr float kMostBf16 = 0x1.FEp127f;
 
 // N words of a pool, aligned to `A` bytes, read ONCE (see fetch) or not.
 template <int N, int A, bool ONCE>
@@ -394,7 +394,9 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : at_once(D, QT, sizeof(
         } else {
 #pragma unroll
           for (int k = 0; k < kQTerms; ++k) {
-            qb[t][k][m][e] = (bf16)rest;
+            // (the type's largest where fp32 goes on: infinite first terms leave NaN; the last one carries an infinity)
+            const bool beyond = k + 1 < kQTerms && fabsf(rest) > kMostBf16;
+            qb[t][k][m][e] = (bf16)(beyond ? copysignf(kMostBf16, rest) : rest);
             rest -= (float)qb[t][k][m][e];
           }
         }

@@ -557,7 +557,8 @@ gdn_status_t gdn_kv_read(const gdn_kv_problem_t* p, const void* k_cache, const v
  * infinity) out is zero and lse minus infinity; a score of plus infinity or NaN
  * makes its row and lse NaN.  A channel with an infinite visible value is infinite
  * in a cache of the rows' own type if that token's weight is 2^-100 of the largest
- * or more; else, as in quantised caches, infinite or NaN.  Weights below 2^-126 of
+ * or more; else, as in quantised caches, infinite or NaN.  fp32 queries make NaN of
+ * a quantised key that reads back as an infinity.  Weights below 2^-126 of
  * the largest count as zero.  Sums are fp32 and divided last: finite values of
  * 2^127 / lengths[b] or more may overflow.  What lies in places that are not
  * visible, NaN included, has no influence.  lengths beyond the table's reach

@@ -207,3 +207,38 @@ def test_blocks_of_the_least_scales(kind, form):
         gdn.attention_step(q, cache, i32([[0]]), i32([s + 1]), scale=scale, window=1, lse=lse)
         x = scale * 2.0 ** 120 * want[s, 0]
         check(n(lse), np.array([[x]]), np.array([[8 * U * x]]), "f32", f"byte {s % 17}")
+
+
+@pytest.mark.parametrize("form", ["mxfp8", "mxfp4"])
+def test_attention_of_fp32_queries_beyond_16_bits(form):
+    """Over quantised keys: infinite queries, and the largest finite one, which lies above the largest bf16 value."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    rng = Rng(25)
+    L, d, page = 70, 64, 32
+    table, k, v = spread(1, L, 1, page, d)
+    k[:], v[:] = rng.g.standard_normal(k.shape), rng.g.standard_normal(v.shape)
+    k[..., 0] = rng.g.choice([1.0, 2.0, 3.0], k.shape[:-1])
+    k[..., 1] = rng.g.choice([-0.5, 0.25, 0.5], k.shape[:-1])
+    cache, kk, vv = cache_of(k, v, form)
+    keys, values = (a[table[0], 0].reshape(-1, d)[:L] for a in (kk, vv))
+    assert keys[:, 0].min() > 0
+
+    def attend(channel, value, scale):
+        q = torch.zeros((1, 1, d), device="cuda")
+        q[..., channel] = value
+        lse = torch.empty((1, 1), device="cuda")
+        y = gdn.attention_step(q, cache, i32(table), i32([L]), scale=scale, lse=lse)
+        return n(q)[0], n(y)[0], n(lse)[0]
+
+    for scale in (1.0, 2.0 ** -126):
+        _, y, lse = attend(0, -float("inf"), scale)  # every score minus infinity
+        assert not y.any() and np.isneginf(lse).all()
+        _, y, lse = attend(0, float("inf"), scale)
+        assert np.isnan(y).all() and np.isnan(lse).all()
+    for sign in (1, -1):
+        q, y, lse = attend(1, sign * torch.finfo(torch.float32).max, 2.0 ** -126)  # scores of up to 2
+        (o, oe), (l, le) = oracle.attend(q[:, 1:2], keys[:, 1:2], values, 2.0 ** -126, False)
+        check(y, o, oe, "f32", f"{sign}")
+        check(lse, l, le, "f32", f"{sign}")
