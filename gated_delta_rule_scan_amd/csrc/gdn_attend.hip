@@ -405,17 +405,24 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 8 ? 2 : at_once(D, QT, sizeof(
   auto scores = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int t = 0; t < QT; ++t) s[t][h] = f32x4{0.f, 0.f, 0.f, 0.f};
       if constexpr (kWide) {
 #pragma unroll
-        for (int m = 0; m < D / 16; ++m)
+        for (int t = 0; t < QT; ++t) {
+          // (four sums, each a chain of a quarter of the products: one chain of all is off by twice as much, 8 sequences of
+          // 512 tokens with heads of 128 by 5.4e-7 of the outputs against 2.6e-7, in the same time)
+          f32x4 part[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e) part[e] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int t = 0; t < QT; ++t)
-              s[t][h] = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, kw[h][m][e]), qw[t][m][e], s[t][h], 0, 0, 0);
+          for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              part[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, kw[h][m][e]), qw[t][m][e], part[e], 0, 0, 0);
+          s[t][h] = (part[0] + part[1]) + (part[2] + part[3]);
+        }
       } else {
+#pragma unroll
+        for (int t = 0; t < QT; ++t) s[t][h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
           constexpr int per = F::kRun / 8, wpm = 8 / F::kPerWord;  // products of a load, words of a product

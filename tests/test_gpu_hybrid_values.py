@@ -242,3 +242,20 @@ def test_attention_of_fp32_queries_beyond_16_bits(form):
         (o, oe), (l, le) = oracle.attend(q[:, 1:2], keys[:, 1:2], values, 2.0 ** -126, False)
         check(y, o, oe, "f32", f"{sign}")
         check(lse, l, le, "f32", f"{sign}")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_fp32_scores_are_sums_of_four(d):
+    """One product of 1 and d - 1 of 0.1255 of its last digit: a sum that adds them to the one loses each, or rounds each
+    four of them up.  At most d / 4 meet it: off by no more than they are.  Then the scale, log2 e, ln 2 and three sums."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    term = 0.1255 * 2.0 ** -23
+    for at in (0, 1, 5, d // 2 + 2, d - 1):
+        k = torch.full((1, 1, 16, d), term, device="cuda")
+        k[..., at] = 1
+        lse = torch.empty((2, 1), device="cuda")
+        gdn.attention_step(torch.ones((2, 1, d), device="cuda"), (k, k), i32([[0], [0]]), i32([1, 1]), scale=1.0, lse=lse)
+        want = np.full((2, 1), 1 + (d - 1) * term)
+        check(n(lse), want, np.full((2, 1), (d / 4) * term + 7 * U), "f32", f"{at}")
