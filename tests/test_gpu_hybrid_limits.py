@@ -1,10 +1,12 @@
 """The largest batches of the cache, its attention and the seam on the GPU: more workgroups than one launch takes,
-against the same rows in calls that need fewer; more sequences than are cut."""
+against the same rows in calls that need fewer; more sequences than are cut; workspaces of exactly the size that a call
+asks for; lengths beyond a table whose pages are all there."""
 import pytest
 
 from layer_oracle import U
-from test_gpu_hybrid import _attention_case, _check_attention, _expect, i32
+from test_gpu_hybrid import SeamCase, _attention_case, _check_attention, _expect, i32
 from test_gpu_layer import _torch
+from test_gpu_layer_together import G, _guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +103,97 @@ def test_attention_of_a_thousand_sequences_in_a_wide_table(kind, form):
     lse = torch.empty((len(lens), 4), device="cuda")
     y = gdn.attention_step(q, cache, i32(table), i32(lens), lse=lse)
     _check_attention(y, lse, _expect(q, table, lens, kv, vv, 0.125, 0, 0, kind), kind)
+
+
+def _workspace(size):
+    """(exactly that many bytes that hold NaN, the buffer with their guard zones)."""
+    torch = _torch()
+    ws, whole = _guarded(torch.full((size,), 255, dtype=torch.uint8, device="cuda"))
+    assert ws.data_ptr() % 256 == 0
+    return ws, whole
+
+
+WORKSPACES = [
+    # kind, form, lens, Hq, Hk, d, page, window, sinks, width
+    ("bf16", "bf16", [1000], 12, 12, 128, 64, 0, 0, None),
+    ("f32", "f32", [700, 0, 3000], 6, 2, 64, 16, 0, 0, None),
+    ("bf16", "mxfp8", [5000, 1, 33, 600], 40, 1, 128, 64, 0, 0, 100),
+    ("f32", "mxfp4", [2000, 40], 8, 2, 256, 16, 0, 0, 200),
+    ("bf16", "bf16", [3000, 2500, 10], 34, 2, 256, 32, 900, 70, None),
+    ("f32", "f32", [9000], 4, 4, 64, 32, 2500, 0, 400),
+    ("bf16", "mxfp4", [600] * 70, 4, 2, 64, 64, 0, 0, 40),
+]
+
+
+@pytest.mark.parametrize("kind,form,lens,Hq,Hk,d,page,window,sinks,width", WORKSPACES)
+def test_attention_keeps_to_its_workspace(kind, form, lens, Hq, Hk, d, page, window, sinks, width):
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    q, cache, table, kv, vv = _attention_case(kind, form, lens, Hq, Hk, d, page, window, sinks, len(lens) + d, width)
+    forms = {"f32": 0, "bf16": 1, "mxfp8": 2, "mxfp4": 3}
+    size = gdn.gdn_attention_workspace_bytes(gdn.gdn_attention_problem_t(
+        B=len(lens), Hq=Hq, Hk=Hk, d=d, pages=len(kv), page=page, table_width=table.shape[1], window=window, sinks=sinks,
+        dtype=forms[kind], format=forms[form]))
+    assert size > 0
+    ws, whole = _workspace(size)
+    lse = torch.empty((len(lens), Hq), device="cuda")
+    for _ in range(2):  # (the second call finds the first one's remains)
+        y = gdn.attention_step(q, cache, i32(table), i32(lens), window=window, sinks=sinks, lse=lse, workspace=ws)
+        torch.cuda.synchronize()
+        assert (whole[:G] == 0x5A).all() and (whole[-G:] == 0x5A).all()
+        _check_attention(y, lse, _expect(q, table, lens, kv, vv, d ** -0.5, window, sinks, kind), kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,D", [((2, 300), 136), ((5000,), 64), ([700, 0, 130], 1001), ([1] * 300, 250), ((1, 2000), 4003), ((3, 5), 16384)])
+@pytest.mark.parametrize("gate,post,weight", [("sequence", True, True), ("channel", False, True), (None, True, False)])
+def test_residual_norm_backward_keeps_to_its_workspace(kind, lens, D, gate, post, weight):
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    c = SeamCase(kind, lens, D, True, gate, post, weight, 1.0, "plain")
+    packed = isinstance(lens, list)
+    p = gdn.gdn_norm_problem_t(B=len(c.each), T=c.x.shape[0] if packed else lens[1] if len(lens) == 2 else 1, D=D,
+                               gate_stride_b=D if gate == "sequence" else 0, dtype=int(kind == "bf16"), residual_scale=1.0, eps=1e-6)
+    p.gate, p.post_weight, p.weight, p.seq_offsets = (1 << 20 if t is not None else None for t in (c.gate, c.post, c.weight, c.off))
+    size = gdn.gdn_norm_workspace_bytes(p)
+    assert size > 0
+    want = gdn.residual_norm_backward(c.dh, c.dn, c.x, c.y, **c.args())
+    ws, whole = _workspace(size)
+    got = gdn.residual_norm_backward(c.dh, c.dn, c.x, c.y, **c.args(), workspace=ws)
+    torch.cuda.synchronize()
+    assert (whole[:G] == 0x5A).all() and (whole[-G:] == 0x5A).all() and not (ws == 255).all()
+    for a, b in zip(got, want):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+
+
+REACH = [
+    # kind, form, page, width (positions: page * width), window, sinks
+    ("bf16", "bf16", 16, 5, 0, 0),          # 80 positions: not cut
+    ("bf16", "bf16", 16, 5, 33, 7),
+    ("f32", "f32", 64, 20, 0, 0),           # 1280: cut
+    ("f32", "f32", 64, 20, 700, 40),
+    ("bf16", "mxfp8", 32, 100, 0, 0),
+    ("f32", "mxfp4", 16, 70, 900, 1),
+]
+
+
+@pytest.mark.parametrize("kind,form,page,width,window,sinks", REACH)
+def test_attention_of_lengths_beyond_a_full_table(kind, form, page, width, window, sinks):
+    """Every page of the table is there; lengths behind its end count as its end, and so does a window's."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    reach = page * width
+    full = [reach] * 5
+    q, cache, table, kv, vv = _attention_case(kind, form, full, 4, 2, 64, page, window, sinks, 41)
+    given = [reach, reach + 1, reach + 1000, 2 ** 31 - 1, reach - 1]
+    assert (table >= 0).all() and table.shape == (5, width)
+    lse = torch.empty((5, 4), device="cuda")
+    y = gdn.attention_step(q, cache, i32(table), i32(given), window=window, sinks=sinks, lse=lse)
+    # (of the last sequence one token more is hidden, and with a window another one seen: garbage there, so its own case)
+    want = _expect(q[:4], table[:4], full[:4], kv, vv, 0.125, window, sinks, kind)
+    _check_attention(y[:4], lse[:4], want, kind)
+    if not window:
+        _check_attention(y[4:], lse[4:], _expect(q[4:], table[4:], given[4:], kv, vv, 0.125, 0, 0, kind), kind)
