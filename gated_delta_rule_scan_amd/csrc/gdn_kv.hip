@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kThreads) void kv_kernel(KvArgs a) {
   // rows behind the last sequence
   const int64_t limit = !WRITE && a.zero_unused && s.b == a.B - 1 && a.off ? a.T - s.row0 : s.len;
   const int64_t t0 = s.chunk << a.chunk_bits;
-  if (t0 >= limit) return;
+  if (t0 < 0 || t0 >= limit) return;  // (below zero: rows in front of the first sequence)
   const int lane_bits = __builtin_ctz(a.d) - 3;  // lanes of a row: 8, 16 or 32
   const int heads = a.Hk - h0 < a.heads ? a.Hk - h0 : a.heads;
   const unsigned places = (unsigned)heads << (a.chunk_bits + lane_bits);

@@ -282,7 +282,7 @@ __device__ __forceinline__ Run run_of(const NormArgs& a, int sub) {
   r.row0 = s.row0;
   r.len = s.len;
   const int64_t runs = (s.len + a.chunk - 1) / a.chunk;
-  r.t = s.chunk < runs ? s.chunk * R + sub : s.len;
+  r.t = s.chunk >= 0 && s.chunk < runs ? s.chunk * R + sub : s.len;  // (below zero: in front of the first sequence)
   r.step = runs * R;
   const int64_t all = a.off && a.zero_unused && s.b == a.B - 1 ? a.T - s.row0 : s.len;
   r.u0 = s.chunk * a.chunk > s.len ? s.chunk * a.chunk : s.len;

@@ -597,7 +597,8 @@ gdn_status_t gdn_attention_step(const gdn_attention_problem_t* p, const void* q,
  *   u = post_weight * y / sqrt(mean(y^2) + eps)     (post_weight NULL: u = y)
  *   h = residual_scale * x + gate * u               (gate NULL: 1)
  *   n = weight * h / sqrt(mean(h^2) + eps)          (weight NULL: no n)
- * n is computed from h before h is rounded.
+ * n is computed from h before h is rounded.  Squares and their sums are fp32: a
+ * row whose sum passes 2^128 norms to zero, squares below 2^-149 are lost.
  *   x, y, h, n   rows of D channels (dtype), strided, packed with seq_offsets;
  *                y may be NULL (then h = residual_scale * x; gate and
  *                post_weight NULL); h may be NULL, or x (in place)

@@ -197,3 +197,36 @@ def test_attention_of_lengths_beyond_a_full_table(kind, form, page, width, windo
     _check_attention(y[:4], lse[:4], want, kind)
     if not window:
         _check_attention(y[4:], lse[4:], _expect(q[4:], table[4:], given[4:], kv, vv, 0.125, 0, 0, kind), kind)
+
+
+def test_offsets_that_do_not_start_at_zero():
+    """Rows in front of the first sequence are of no sequence: not written to the cache, not read into, not normed, and
+    in no sum."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    T, H, d, page, first = 330, 2, 64, 16, 200
+    off, table, start = i32([first, 240, 320]), i32([list(range(20)), list(range(20, 40))]), i32([250, 5])
+    k, v = randn(1, T, H, d), randn(2, T, H, d)
+    cache, want = gdn.kv_cache(40, H, page, d), gdn.kv_cache(40, H, page, d)
+    gdn.kv_write(k, v, cache, table, start, seq_offsets=off)
+    gdn.kv_write(k[first:].contiguous(), v[first:].contiguous(), want, table, start, seq_offsets=off - first)
+    assert torch.equal(cache.k, want.k) and torch.equal(cache.v, want.v)
+    ko, vo = torch.full_like(k, 7), torch.full_like(v, 7)
+    gdn.kv_read(cache, table, T, start, seq_offsets=off, k_out=ko, v_out=vo)
+    assert (ko[:first] == 7).all() and torch.equal(ko[first:320], k[first:320]) and torch.equal(vo[first:320], v[first:320])
+    D = 136
+    x, y, dh, dn = (randn(s, T, D) for s in range(4))
+    w, gate = torch.linspace(0.5, 1.5, D, device="cuda"), torch.randn(2, D, device="cuda")
+    args = dict(gate=gate, weight=w, post_weight=w)
+    h, nn = torch.full_like(x, 7), torch.full_like(x, 7)
+    gdn.residual_norm(x, y, **args, seq_offsets=off, out=h, norm_out=nn)
+    cut = [t[first:].contiguous() for t in (x, y, dh, dn)]
+    eh, en = gdn.residual_norm(*cut[:2], **args, seq_offsets=off - first)
+    assert (h[:first] == 7).all() and (nn[:first] == 7).all()
+    assert torch.equal(h[first:320], eh[:120]) and torch.equal(nn[first:320], en[:120])
+    got = gdn.residual_norm_backward(dh, dn, x, y, **args, seq_offsets=off)
+    want = gdn.residual_norm_backward(*cut[2:], *cut[:2], **args, seq_offsets=off - first)
+    assert torch.equal(got[0][first:320], want[0][:120]) and torch.equal(got[1][first:320], want[1][:120])
+    for g, e in zip(got[2:], want[2:]):  # (sums over 120 rows in two orders)
+        assert torch.allclose(g, e, rtol=0, atol=240 * U * 120 * 64)
