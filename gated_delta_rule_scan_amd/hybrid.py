@@ -101,7 +101,7 @@ def residual_norm(x, y=None, gate=None, post_weight=None, weight=None, residual_
     if got is not None:
         return got
     got = _ResidualNorm.apply(x, y, gate, post_weight, weight, residual_scale, eps, seq_offsets)
-    return got if len(got) == 2 else (x, got[0]) if y is None and residual_scale == 1.0 else (got[0], None)
+    return got if len(got) == 2 else (*got, None) if weight is None else (x, *got)
 
 
 class _ResidualNorm(torch.autograd.Function):

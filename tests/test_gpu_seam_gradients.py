@@ -169,6 +169,19 @@ def test_what_does_not_go_with_gradients():
         nn.sum().backward()
 
 
+@pytest.mark.parametrize("scale", [1.0, 1.0 + 1e-10, 1])
+def test_a_scale_of_one_in_32_bits(scale):
+    """Without y the residual stream then stays what it is, with gradients and without."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    x, w = torch.randn(3, 64, device="cuda", requires_grad=True), torch.ones(64, device="cuda")
+    h, nn = gdn.residual_norm(x, weight=w, residual_scale=scale)
+    with torch.no_grad():
+        want = gdn.residual_norm(x, weight=w, residual_scale=scale)
+    assert h is x and want[0] is x and torch.equal(nn, want[1]) and nn.requires_grad
+
+
 def test_compiled_training_step():
     """The op's autograd formula, eagerly and traced."""
     import gated_delta_rule_scan_amd as gdn
