@@ -93,6 +93,20 @@ def test_attention_of_more_heads_than_a_launch_takes():
 
 
 @pytest.mark.parametrize("kind,form", [("bf16", "bf16"), ("f32", "mxfp8")])
+def test_attention_of_as_many_sequences_as_are_cut(kind, form):
+    """1000 in a wide table: lengths in sixteen rounds of 64, long sequences in the first, a middle and the last."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    lens = [3, 40, 0, 17] * 250
+    lens[5], lens[500], lens[999] = 3100, 2000, 5000
+    q, cache, table, kv, vv = _attention_case(kind, form, lens, 4, 2, 64, 64, 0, 0, 32, width=100)
+    lse = torch.empty((len(lens), 4), device="cuda")
+    y = gdn.attention_step(q, cache, i32(table), i32(lens), lse=lse)
+    _check_attention(y, lse, _expect(q, table, lens, kv, vv, 0.125, 0, 0, kind), kind)
+
+
+@pytest.mark.parametrize("kind,form", [("bf16", "bf16"), ("f32", "mxfp8")])
 def test_attention_of_a_thousand_sequences_in_a_wide_table(kind, form):
     """Not cut, short ones and one long one."""
     import gated_delta_rule_scan_amd as gdn
