@@ -203,3 +203,43 @@ def test_compiled_training_step():
     args, leaves = _leaves(c)
     torch.ops.gdn.residual_norm(leaves[0], leaves[1], None, None, leaves[4], 1.0, 1e-6, None)[1].sum().backward()
     assert leaves[0].grad is not None and leaves[4].grad is not None and leaves[2].grad is None
+
+
+def test_captured_training_step():
+    """Forward and gradients in one graph, replayed on new inputs with eager work between; the leaves are the graph's own
+    and no eager graph of them is alive."""
+    import gated_delta_rule_scan_amd as gdn
+
+    torch = _torch()
+    c = SeamCase("bf16", (2, 150), 136, True, "sequence", True, True, 0.9, "plain")
+
+    def step(x, y, gate, post, weight):
+        h, nn = gdn.residual_norm(x, y, gate, post, weight, 0.9)
+        loss = (h * c.dh).sum(-1) + nn.sum(-1)  # (n's gradient is expanded)
+        return h, nn, *torch.autograd.grad(loss, (x, y, gate, post, weight), torch.ones_like(loss))
+
+    def fresh():
+        return [t.detach().clone().requires_grad_() for t in (c.x, c.y, c.gate, c.post, c.weight)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*fresh())
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    leaves = fresh()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = step(*leaves)
+    r = Rng(8)
+    for i in range(3):
+        new = [r.t(*t.shape).to(t.dtype) for t in leaves]
+        with torch.no_grad():
+            for t, v in zip(leaves, new):
+                t.copy_(v)
+        want = [t.detach().clone() for t in step(*(v.requires_grad_() for v in new))]
+        torch.randn(1000, 1000, device="cuda").sum()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b), f"replay {i}"
