@@ -10,7 +10,7 @@
 // 4 bits is bound by the vector instructions that turn codes into operands: 128
 // sequences of up to 8192, 16 query heads on one, 72 MB in 32 us (cached).
 // A few short sequences end at the latency of one tile's chain and two launches:
-// 1560 tokens of 12 heads 6.2 + 2.8 us.
+// 1560 tokens of 12 heads 6.5 + 3.3 us.
 //
 // A wave walks tiles of 32 tokens of one head of the cache and up to 32 query
 // heads that share it, in registers alone.  With g = lane / 16, n = lane % 16:

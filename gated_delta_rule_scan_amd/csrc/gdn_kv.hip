@@ -2,8 +2,9 @@
 //
 // A copy, with a block's scale and codes in between where the cache has 8 or 4
 // bits: bound by memory on both sides (65520 tokens x 16 heads x 128 from bf16
-// into 8 bits 163 us and back 149, 5.0 and 5.5 TB/s; a window of 8 x 4680 tokens
-// x 12 heads out of a cache in bf16 69 us, 6.7 TB/s).  A thread moves eight channels of K and the
+// into 8 bits 160 us and back 148, 5.1 and 5.5 TB/s, into 4 bits 143 and back 138,
+// 4.8 and 4.9; a window of 8 x 4680 tokens x 12 heads out of a cache in bf16 68 us,
+// 6.8 TB/s).  A thread moves eight channels of K and the
 // same of V; four neighbouring lanes hold a block of 32 channels.  A workgroup
 // takes 16 tokens of a few heads, head by head: rows in 8 or 4 bits are parts
 // of cache lines, and a wave's lie beside each other in the pool.

@@ -15,8 +15,8 @@
 // (forward) and the sums over rows.  Those sums go to the workspace, one partial each
 // per workgroup, and a second kernel adds them in a fixed order.  bf16: forward 65520
 // x 2048 in 193 us (5.6 TB/s), backward 32760 x 2048 in 151 (5.3 TB/s) and 6 for
-// the sums; above 8192 channels the backward kernel spills (4096 x 16384: 522 us,
-// 1.5 TB/s).
+// the sums; above 8192 channels the backward kernel spills (4096 x 16384: 516 us,
+// 1.6 TB/s).
 #include "gdn_layer.h"
 
 namespace gdn {
