@@ -46,8 +46,8 @@ def attend(q, k, v, scale, short):
 
     A score is a product of d terms and a scale: (d + 4) U of the magnitudes.  A weight e^(s - m) takes that error, the
     rounding of its exponent's argument (2 U |s - m|, twice) and 8 U.  Weights enter products exactly, as fp32 or three
-    16-bit terms; ``short`` (rows in 16 bits) allows them 2^-16 all the same, a sixteenth of an output's last digit.  The
-    sums over n tokens round at most n + 64 times.
+    16-bit terms; ``short`` (rows in 16 bits) allows them 2^-16 all the same, far below an output's last digit.  The sums
+    over n tokens round at most n + 64 times.
 
     Below the least normal number, 2^-126, fp32 gives up digits.  A weight (at most 1, the largest is 1, so z >= 1) that
     lies there is taken for something between zero and 2^-126, so it is off by 2^-126 at most; so are the two factors,
