@@ -558,9 +558,10 @@ gdn_status_t gdn_kv_read(const gdn_kv_problem_t* p, const void* k_cache, const v
  * makes its row and lse NaN.  A channel with an infinite visible value is infinite
  * in a cache of the rows' own type if that token's weight is 2^-100 of the largest
  * or more; else, as in quantised caches, infinite or NaN.  fp32 queries make NaN of
- * a quantised key that reads back as an infinity.  Weights below 2^-126 of
- * the largest count as zero.  Sums are fp32 and divided last: finite values of
- * 2^127 / lengths[b] or more may overflow.  What lies in places that are not
+ * a quantised key that reads back as an infinity.  Weights below 2^-126 of the
+ * largest count as zero.  Sums are fp32, those of q . k before the scale, those of
+ * values before they are divided: finite values of 2^127 / lengths[b] or more may
+ * overflow.  What lies in places that are not
  * visible, NaN included, has no influence.  lengths beyond the table's reach
  * count as that.
  *   q, out  head h of sequence b at b * stride_b + h * stride_h, d contiguous
